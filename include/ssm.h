@@ -25,7 +25,9 @@
  * and the exact ZOH form, _noalloc without device allocation), its gradient
  * (ssm_selective_scan_bwd, _ex), the scan with a complex diagonal A
  * (ssm_selective_scan_fwd_complex), Mamba-2's SSD layer (ssm_ssd_scan_fwd),
- * the one-token decode step
+ * the gated delta rule (ssm_delta_rule_fwd, its token step
+ * ssm_delta_rule_update), layer and RMS norm with the gate (ssm_norm_fwd, its
+ * gradient ssm_norm_bwd), the one-token decode step
  * (ssm_selective_state_update), planning (ssm_scan_plan), the device status
  * word of the bounded waits (ssm_get_device_status) and error reporting.
  *
@@ -360,6 +362,80 @@ ssm_status ssm_ssd_scan_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *x, cons
                             const void *B, const void *C, const float *D, const void *z,
                             const float *dt_bias, int dt_softplus, void *out, float *last_state,
                             ssm_stream stream);
+
+/*
+ * The gated delta rule: a linear recurrence with a matrix state per head like
+ * the SSD layer's, whose update first takes out what the state already holds
+ * for the key.  For every batch row b, head h and time t, with the state S
+ * (headdim x dstate) and g' = h / (heads / groups) the group whose q, k the
+ * head reads:
+ *
+ *   a_t = exp(g[b,t,h])
+ *   u_t = beta[b,t,h] (v[b,t,h,:] - a_t S_{t-1} k[b,t,g',:])
+ *   S_t = a_t S_{t-1} + u_t k[b,t,g',:]^T
+ *   out = scale S_t q[b,t,g',:]
+ *
+ * Layouts (dense, row-major):
+ *   q, k       : (batch, seqlen, groups, dstate) io, used as given (a layer
+ *                normalises their rows first, e.g. with ssm_norm_fwd)
+ *   v, out     : (batch, seqlen, heads, headdim) io
+ *   g, beta    : (batch, seqlen, heads) float32; g is the log of the decay
+ *                (-infinity forgets the state)
+ *   last_state : (batch, heads, headdim, dstate) float32 or NULL; read as S_0
+ *                and overwritten with S_L (NULL: S_0 = 0, not returned).
+ * 1 <= dstate <= 128 (SSM_ERR_UNSUPPORTED above); any headdim, heads a
+ * multiple of groups.  A token with beta = 0 and g = 0 leaves the state as it
+ * is, so rows of a padded batch end with the state of their last token.
+ */
+ssm_status ssm_delta_rule_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, const void *k, const void *v,
+                              const float *g, const float *beta, float scale, void *out, float *last_state,
+                              ssm_stream stream);
+
+/*
+ * One token of the gated delta rule (decode): ssm_delta_rule_fwd for one time
+ * step, with the layouts
+ *   state (batch, heads, headdim, dstate) float32, updated in place;
+ *   q, k (batch, groups, dstate), v, out (batch, heads, headdim) io;
+ *   g, beta (batch, heads) float32.
+ * dims.seqlen is ignored.
+ */
+ssm_status ssm_delta_rule_update(ssm_ssd_dims dims, ssm_dtype io, float *state, const void *q, const void *k,
+                                 const void *v, const float *g, const float *beta, float scale, void *out,
+                                 ssm_stream stream);
+
+/*
+ * Normalisation of rows with the silu(z) gate the scans end with:
+ *
+ *   SSM_NORM_LAYER : xhat = (x - mean(x)) rstd, rstd = (mean((x - mean)^2) + eps)^-1/2
+ *   SSM_NORM_RMS   : xhat = x rstd,             rstd = (mean(x^2) + eps)^-1/2
+ *   out = (xhat weight + bias) silu(z)
+ *
+ *   x, z, out    : (rows, dim) io; z may be NULL (no gate).
+ *   weight, bias : (dim) float32 or NULL (one, zero).
+ *   mean, rstd   : (rows) float32 or NULL (not returned); mean must be NULL
+ *                  for an RMS norm.
+ * eps >= 0; a row of zeros with eps = 0 gives infinities or NaN.
+ */
+typedef enum { SSM_NORM_LAYER = 0, SSM_NORM_RMS = 1 } ssm_norm_mode;
+
+ssm_status ssm_norm_fwd(int64_t rows, int64_t dim, ssm_dtype io, int mode, const void *x, const float *weight,
+                        const float *bias, const void *z, float eps, void *out, float *mean, float *rstd,
+                        ssm_stream stream);
+
+/*
+ * Gradients of sum(dout * out) of one ssm_norm_fwd call; mean (layer norm
+ * only) and rstd are what that call returned.
+ *   dout, dx, dz    : (rows, dim) io; dz is required iff z is given.
+ *   dweight, dbias  : (dim) float32 or NULL (not computed).
+ * The column sums are added in a fixed order: equal inputs give equal bits.
+ * Workspace for them (at most 2 dim float32 per block of a launch) comes from
+ * the library's pool on "stream" (see ssm_selective_scan_fwd).  Outputs must
+ * not overlap each other or any input.
+ */
+ssm_status ssm_norm_bwd(int64_t rows, int64_t dim, ssm_dtype io, int mode, const void *x, const float *weight,
+                        const float *bias, const void *z, const float *mean, const float *rstd,
+                        const void *dout, void *dx, void *dz, float *dweight, float *dbias,
+                        ssm_stream stream);
 
 /*
  * Reads and clears the device status word of the current device, after

@@ -19,6 +19,7 @@ SSM_OK, SSM_ERR_INVALID_ARG, SSM_ERR_UNSUPPORTED, SSM_ERR_CUDA = 0, 1, 2, 3
 SSM_F32, SSM_BF16 = 0, 1
 VARIANTS = {"auto": 0, "slab": 1, "split": 2}
 FAMILIES = {"auto": 0, "generic": 1, "staged": 2}
+NORM_MODES = {"layer": 0, "rms": 1}
 
 # every symbol include/ssm.h declares
 EXPORTED = ("ssm_selective_scan_fwd", "ssm_selective_scan_fwd_ex", "ssm_selective_scan_fwd_noalloc",
@@ -26,7 +27,7 @@ EXPORTED = ("ssm_selective_scan_fwd", "ssm_selective_scan_fwd_ex", "ssm_selectiv
             "ssm_selective_scan_bwd", "ssm_selective_scan_bwd_ex", "ssm_selective_state_update",
             "ssm_scan_plan", "ssm_get_device_status", "ssm_test_inject_decode_wait_timeout",
             "ssm_status_string", "ssm_last_error", "ssm_version", "ssm_get_build_info", "ssm_ssd_scan_fwd",
-            "ssm_test_exp2_poly")
+            "ssm_test_exp2_poly", "ssm_delta_rule_fwd", "ssm_delta_rule_update", "ssm_norm_fwd", "ssm_norm_bwd")
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 
@@ -108,6 +109,15 @@ def _load() -> ctypes.CDLL:
     lib.ssm_get_build_info.restype = None
     lib.ssm_ssd_scan_fwd.argtypes = [SSMSsdDims, ctypes.c_int] + [_vp] * 8 + [ctypes.c_int, _vp, _vp, _vp]
     lib.ssm_ssd_scan_fwd.restype = ctypes.c_int
+    lib.ssm_delta_rule_fwd.argtypes = [SSMSsdDims, ctypes.c_int] + [_vp] * 5 + [ctypes.c_float] + [_vp] * 3
+    lib.ssm_delta_rule_fwd.restype = ctypes.c_int
+    lib.ssm_delta_rule_update.argtypes = [SSMSsdDims, ctypes.c_int] + [_vp] * 6 + [ctypes.c_float] + [_vp] * 2
+    lib.ssm_delta_rule_update.restype = ctypes.c_int
+    norm_args = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int]
+    lib.ssm_norm_fwd.argtypes = norm_args + [_vp] * 4 + [ctypes.c_float] + [_vp] * 4
+    lib.ssm_norm_fwd.restype = ctypes.c_int
+    lib.ssm_norm_bwd.argtypes = norm_args + [_vp] * 12
+    lib.ssm_norm_bwd.restype = ctypes.c_int
     lib.ssm_test_exp2_poly.argtypes = [_vp, _vp, _vp, ctypes.c_int64, _vp]
     lib.ssm_test_exp2_poly.restype = ctypes.c_int
     return lib
@@ -328,6 +338,101 @@ def ssd_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
         _ptr(last_state, "last_state", torch.float32, (batch, heads, headdim, dstate), dev),
         _stream_handle(stream)))
     return out
+
+
+def _stream_on(dev: torch.device, stream):
+    """The stream's handle; by default the current stream of ``dev``.  The
+    library launches on the current device, which therefore has to be ``dev``."""
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return _stream_handle(stream)
+
+
+def delta_rule_fwd(q, k, v, g, beta, scale: Optional[float] = None, out=None, last_state=None, stream=None):
+    """Gated delta rule over a sequence; returns ``out``.
+
+    q, k: (batch, seqlen, groups, dstate); v: (batch, seqlen, heads, headdim)
+    -- all float32 or all bfloat16; g (log decay), beta: (batch, seqlen,
+    heads) float32; ``scale`` defaults to dstate ** -0.5; last_state (batch,
+    heads, headdim, dstate) float32 is read as S_0 and overwritten with S_L."""
+    io = _io_of(v)
+    batch, seqlen, heads, headdim = v.shape
+    groups, dstate = q.shape[2], q.shape[3]
+    dev = v.device
+    if out is None:
+        out = torch.empty_like(v)
+    qk, hs = (batch, seqlen, groups, dstate), (batch, seqlen, heads)
+    args = [_ptr(q, "q", v.dtype, qk, dev), _ptr(k, "k", v.dtype, qk, dev), _ptr(v, "v", v.dtype, None, dev),
+            _ptr(g, "g", torch.float32, hs, dev), _ptr(beta, "beta", torch.float32, hs, dev),
+            float(dstate ** -0.5 if scale is None else scale), _ptr(out, "out", v.dtype, v.shape, dev),
+            _ptr(last_state, "last_state", torch.float32, (batch, heads, headdim, dstate), dev)]
+    check(lib.ssm_delta_rule_fwd(SSMSsdDims(batch, seqlen, heads, headdim, groups, dstate), io, *args,
+                                 _stream_on(dev, stream)))
+    return out
+
+
+def delta_rule_update(state, q, k, v, g, beta, scale: Optional[float] = None, out=None, stream=None):
+    """One token of the gated delta rule; ``state`` (batch, heads, headdim,
+    dstate) float32 is updated in place; returns ``out``.  q, k: (batch,
+    groups, dstate); v: (batch, heads, headdim); g, beta: (batch, heads)
+    float32; ``scale`` defaults to dstate ** -0.5."""
+    io = _io_of(v)
+    batch, heads, headdim = v.shape
+    groups, dstate = q.shape[1], q.shape[2]
+    dev = v.device
+    if out is None:
+        out = torch.empty_like(v)
+    qk, hs = (batch, groups, dstate), (batch, heads)
+    args = [_ptr(state, "state", torch.float32, (batch, heads, headdim, dstate), dev),
+            _ptr(q, "q", v.dtype, qk, dev), _ptr(k, "k", v.dtype, qk, dev), _ptr(v, "v", v.dtype, None, dev),
+            _ptr(g, "g", torch.float32, hs, dev), _ptr(beta, "beta", torch.float32, hs, dev),
+            float(dstate ** -0.5 if scale is None else scale), _ptr(out, "out", v.dtype, v.shape, dev)]
+    check(lib.ssm_delta_rule_update(SSMSsdDims(batch, 1, heads, headdim, groups, dstate), io, *args,
+                                    _stream_on(dev, stream)))
+    return out
+
+
+def norm_fwd(x, weight=None, bias=None, z=None, eps: float = 1e-5, mode: str = "layer", out=None, stream=None):
+    """Layer (``mode="layer"``) or RMS (``"rms"``) norm of the rows of x with
+    an optional silu(z) gate; returns (out, mean, rstd), mean None for RMS.
+
+    x, z: (..., dim) float32 or bfloat16; weight, bias: (dim,) float32; mean,
+    rstd: x's shape without its last axis, float32."""
+    io = _io_of(x)
+    dim = x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    dev = x.device
+    if out is None:
+        out = torch.empty_like(x)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    mean = torch.empty_like(rstd) if mode == "layer" else None
+    args = [_ptr(x, "x", x.dtype, None, dev), _ptr(weight, "weight", torch.float32, (dim,), dev),
+            _ptr(bias, "bias", torch.float32, (dim,), dev), _ptr(z, "z", x.dtype, x.shape, dev), float(eps),
+            _ptr(out, "out", x.dtype, x.shape, dev), _ptr(mean, "mean"), _ptr(rstd, "rstd")]
+    check(lib.ssm_norm_fwd(rows, dim, io, NORM_MODES[mode], *args, _stream_on(dev, stream)))
+    return out, mean, rstd
+
+
+def norm_bwd(x, weight, dout, rstd, mean=None, bias=None, z=None, stream=None):
+    """Gradients of sum(dout * out) of one ``norm_fwd`` call, whose mean (None
+    for an RMS norm) and rstd are given back.  Returns a dict: dx, dz (None
+    without z) in x's dtype; dweight, dbias (None without the argument)
+    (dim,) float32."""
+    io = _io_of(x)
+    dim = x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    dev = x.device
+    f32 = dict(dtype=torch.float32, device=dev)
+    g = {"dx": torch.empty_like(x), "dz": torch.empty_like(x) if z is not None else None,
+         "dweight": torch.empty((dim,), **f32) if weight is not None else None,
+         "dbias": torch.empty((dim,), **f32) if bias is not None else None}
+    args = [_ptr(x, "x", x.dtype, None, dev), _ptr(weight, "weight", torch.float32, (dim,), dev),
+            _ptr(bias, "bias", torch.float32, (dim,), dev), _ptr(z, "z", x.dtype, x.shape, dev),
+            _ptr(mean, "mean", torch.float32, x.shape[:-1], dev), _ptr(rstd, "rstd", torch.float32, x.shape[:-1], dev),
+            _ptr(dout, "dout", x.dtype, x.shape, dev)] + [_ptr(g[n], n) for n in ("dx", "dz", "dweight", "dbias")]
+    mode = "rms" if mean is None else "layer"
+    check(lib.ssm_norm_bwd(rows, dim, io, NORM_MODES[mode], *args, _stream_on(dev, stream)))
+    return g
 
 
 def test_exp2_poly(x: torch.Tensor, stream=None):

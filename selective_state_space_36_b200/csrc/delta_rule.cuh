@@ -1,0 +1,33 @@
+// delta_rule.cuh -- argument blocks and launch entry points of the gated delta
+// rule's kernels (internal to the library; the public ABI is include/ssm.h).
+//
+//   S_t = a_t S_{t-1} + u_t k_t^T,  u_t = beta_t (v_t - a_t S_{t-1} k_t),
+//   o_t = scale S_t q_t,            a_t = exp(g_t)
+//
+// with S (headdim x dstate) per (batch row, head); q, k are shared by the
+// heads / groups heads of a group.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ssm {
+
+constexpr int kDeltaMaxDstate = 128;
+
+struct DeltaArgs {
+    const void *q, *k, *v;     // (batch, seqlen, groups, dstate) x 2, (batch, seqlen, heads, headdim)
+    const float *g, *beta;     // (batch, seqlen, heads)
+    float scale;
+    void *out;                 // (batch, seqlen, heads, headdim)
+    const float *h0;           // (batch, heads, headdim, dstate) or null (zero)
+    float *state;              // the same shape or null (not returned); may be h0
+    int64_t batch, seqlen;
+    int heads, groups, headdim, dstate;
+};
+
+// One warp group per few state rows, token after token in fp32: any sizes and
+// alignment, both element types; the decode step is seqlen == 1.
+cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool bf16, cudaStream_t st);
+
+}  // namespace ssm

@@ -9,6 +9,8 @@
 #include <string.h>
 
 #include "../../include/ssm.h"
+#include "delta_rule.cuh"
+#include "norm.cuh"
 #include "scan_kernels.cuh"
 
 namespace {
@@ -837,5 +839,158 @@ ssm_status ssm_test_exp2_poly(const float *x, float *poly, float *sfu, int64_t n
 }
 
 void ssm_test_inject_decode_wait_timeout(int32_t enable) { g_inject_wait_bytes.store(enable ? 16u : 0u); }
+
+}  // extern "C"
+
+namespace {
+
+// Sizes common to the delta rule's entry points; *empty: nothing to compute.
+ssm_status check_delta_dims(const ssm_ssd_dims &d, ssm_dtype io, size_t *es, bool *empty) {
+    if (ssm_status s = check_io(io, es)) return s;
+    if (d.batch < 0 || d.seqlen < 0 || d.heads < 0 || d.headdim < 0 || d.groups < 0 || d.dstate < 0)
+        return fail(SSM_ERR_INVALID_ARG, "negative size");
+    if (d.groups < 1 || d.heads % d.groups != 0)
+        return fail(SSM_ERR_INVALID_ARG, "heads (%lld) must be a multiple of groups (%lld >= 1)",
+                    (long long)d.heads, (long long)d.groups);
+    if (d.dstate < 1) return fail(SSM_ERR_INVALID_ARG, "dstate must be >= 1");
+    if (d.dstate > ssm::kDeltaMaxDstate)
+        return fail(SSM_ERR_UNSUPPORTED, "dstate %lld > %d", (long long)d.dstate, ssm::kDeltaMaxDstate);
+    *empty = d.batch == 0 || d.seqlen == 0 || d.heads == 0 || d.headdim == 0;
+    if (*empty) return SSM_OK;
+    if (d.heads > 0x7fffffffLL || d.headdim > 0x7fffffffLL || d.heads * d.headdim > 0x7fffffffLL)
+        return fail(SSM_ERR_UNSUPPORTED, "heads * headdim exceeds 32 bits");
+    if (d.batch > INT64_MAX / d.seqlen || d.batch * d.seqlen > INT64_MAX / (d.heads * d.headdim) / 128 ||
+        d.batch > INT64_MAX / (d.heads * d.headdim) / 128)
+        return fail(SSM_ERR_INVALID_ARG, "batch * seqlen * heads * headdim overflows");
+    return SSM_OK;
+}
+
+ssm::DeltaArgs delta_args(const ssm_ssd_dims &d, const void *q, const void *k, const void *v, const float *g,
+                          const float *beta, float scale) {
+    ssm::DeltaArgs a{};
+    a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.scale = scale;
+    a.batch = d.batch; a.seqlen = d.seqlen;
+    a.heads = (int)d.heads; a.groups = (int)d.groups; a.headdim = (int)d.headdim; a.dstate = (int)d.dstate;
+    return a;
+}
+
+ssm_status delta_forward(ssm_ssd_dims dims, ssm_dtype io, const void *q, const void *k, const void *v,
+                         const float *g, const float *beta, float scale, void *out, const float *h0,
+                         float *state, ssm_stream stream) {
+    size_t es = 0;
+    bool empty = false;
+    if (ssm_status s = check_delta_dims(dims, io, &es, &empty)) return s;
+    if (empty) return SSM_OK;  // state unchanged
+    if (!q || !k || !v || !g || !beta || !out)
+        return fail(SSM_ERR_INVALID_ARG, "q, k, v, g, beta and out are required");
+    if (misaligned(q, es) || misaligned(k, es) || misaligned(v, es) || misaligned(out, es) ||
+        misaligned(g, 4) || misaligned(beta, 4) || misaligned(state, 4))
+        return fail(SSM_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+    if (dims.batch * dims.heads > kMaxGridX / ((dims.headdim + 15) / 16))
+        return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+    ssm::DeltaArgs a = delta_args(dims, q, k, v, g, beta, scale);
+    a.out = out; a.h0 = h0; a.state = state;
+    cudaError_t e = ssm::launch_delta_recurrent(a, io == SSM_BF16, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
+    return SSM_OK;
+}
+
+ssm_status check_norm(int64_t rows, int64_t dim, ssm_dtype io, int mode, size_t *es) {
+    if (ssm_status s = check_io(io, es)) return s;
+    if (rows < 0 || dim < 0) return fail(SSM_ERR_INVALID_ARG, "negative size");
+    if (mode != SSM_NORM_LAYER && mode != SSM_NORM_RMS)
+        return fail(SSM_ERR_INVALID_ARG, "norm mode %d is not SSM_NORM_LAYER or SSM_NORM_RMS", mode);
+    if (dim > (1 << 24)) return fail(SSM_ERR_UNSUPPORTED, "dim %lld > %d", (long long)dim, 1 << 24);
+    if (rows > kMaxGridX) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+    return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ssm_status ssm_delta_rule_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, const void *k, const void *v,
+                              const float *g, const float *beta, float scale, void *out, float *last_state,
+                              ssm_stream stream) {
+    g_last_error[0] = 0;
+    return delta_forward(dims, io, q, k, v, g, beta, scale, out, last_state, last_state, stream);
+}
+
+ssm_status ssm_delta_rule_update(ssm_ssd_dims dims, ssm_dtype io, float *state, const void *q, const void *k,
+                                 const void *v, const float *g, const float *beta, float scale, void *out,
+                                 ssm_stream stream) {
+    g_last_error[0] = 0;
+    dims.seqlen = 1;
+    if (!state && dims.batch > 0 && dims.heads > 0 && dims.headdim > 0)
+        return fail(SSM_ERR_INVALID_ARG, "state is required");
+    return delta_forward(dims, io, q, k, v, g, beta, scale, out, state, state, stream);
+}
+
+ssm_status ssm_norm_fwd(int64_t rows, int64_t dim, ssm_dtype io, int mode, const void *x, const float *weight,
+                        const float *bias, const void *z, float eps, void *out, float *mean, float *rstd,
+                        ssm_stream stream) {
+    g_last_error[0] = 0;
+    size_t es = 0;
+    if (ssm_status s = check_norm(rows, dim, io, mode, &es)) return s;
+    if (!(eps >= 0.f)) return fail(SSM_ERR_INVALID_ARG, "eps must be >= 0");
+    if (mode == SSM_NORM_RMS && mean) return fail(SSM_ERR_INVALID_ARG, "an RMS norm has no mean");
+    if (rows == 0 || dim == 0) return SSM_OK;
+    if (!x || !out) return fail(SSM_ERR_INVALID_ARG, "x and out are required");
+    if (misaligned(x, es) || misaligned(z, es) || misaligned(out, es) || misaligned(weight, 4) ||
+        misaligned(bias, 4) || misaligned(mean, 4) || misaligned(rstd, 4))
+        return fail(SSM_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+    ssm::NormArgs a{};
+    a.x = x; a.z = z; a.weight = weight; a.bias = bias; a.out = out; a.mean = mean; a.rstd = rstd;
+    a.rows = rows; a.dim = (int)dim; a.eps = eps; a.center = mode == SSM_NORM_LAYER;
+    cudaError_t e = ssm::launch_norm_fwd(a, io == SSM_BF16, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm launch");
+    return SSM_OK;
+}
+
+ssm_status ssm_norm_bwd(int64_t rows, int64_t dim, ssm_dtype io, int mode, const void *x, const float *weight,
+                        const float *bias, const void *z, const float *mean, const float *rstd,
+                        const void *dout, void *dx, void *dz, float *dweight, float *dbias,
+                        ssm_stream stream) {
+    g_last_error[0] = 0;
+    size_t es = 0;
+    if (ssm_status s = check_norm(rows, dim, io, mode, &es)) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (misaligned(dweight, 4) || misaligned(dbias, 4))
+        return fail(SSM_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+    if (dim == 0) return SSM_OK;
+    if (rows == 0) {  // sums over no rows
+        for (float *p : {dweight, dbias}) {
+            if (!p) continue;
+            cudaError_t e = cudaMemsetAsync(p, 0, (size_t)dim * sizeof(float), st);
+            if (e != cudaSuccess) return cuda_fail(e, "zeroing gradients");
+        }
+        return SSM_OK;
+    }
+    if (!x || !rstd || !dout || !dx) return fail(SSM_ERR_INVALID_ARG, "x, rstd, dout and dx are required");
+    if ((mode == SSM_NORM_LAYER) != (mean != nullptr))
+        return fail(SSM_ERR_INVALID_ARG, "mean is required by the layer norm and only by it");
+    if ((z != nullptr) != (dz != nullptr)) return fail(SSM_ERR_INVALID_ARG, "dz is required iff z is given");
+    if (misaligned(x, es) || misaligned(z, es) || misaligned(dout, es) || misaligned(dx, es) ||
+        misaligned(dz, es) || misaligned(weight, 4) || misaligned(bias, 4) || misaligned(mean, 4) ||
+        misaligned(rstd, 4))
+        return fail(SSM_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+    ssm::NormArgs a{};
+    a.x = x; a.z = z; a.dout = dout; a.weight = weight; a.bias = bias;
+    a.mean_in = mean; a.rstd_in = rstd;
+    a.dx = dx; a.dz = dz; a.dweight = dweight; a.dbias = dbias;
+    a.rows = rows; a.dim = (int)dim; a.center = mode == SSM_NORM_LAYER;
+    const int sms = device_info().sms;
+    void *ws = nullptr;
+    if (dweight || dbias) {
+        cudaError_t e = workspace_alloc(&ws, ssm::norm_bwd_partial_bytes(a, io == SSM_BF16, sms), st);
+        if (e != cudaSuccess) return cuda_fail(e, "norm workspace allocation");
+        a.partial = static_cast<float *>(ws);
+    }
+    cudaError_t e = ssm::launch_norm_bwd(a, io == SSM_BF16, sms, st);
+    cudaError_t ef = ws ? cudaFreeAsync(ws, st) : cudaSuccess;
+    if (e != cudaSuccess) return cuda_fail(e, "norm gradient launch");
+    if (ef != cudaSuccess) return cuda_fail(ef, "workspace release");
+    return SSM_OK;
+}
 
 }  // extern "C"

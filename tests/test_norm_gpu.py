@@ -1,0 +1,191 @@
+"""The layer / RMS norm with the silu gate on the GPU against float64.
+
+Tolerance: |got - ref| <= h |ref| + c big, h the rounding of the output's type
+(half a step: bf16 2^-8, float32 2^-24), big the largest |ref| of the row (of
+the whole sum for dweight, dbias).  c covers float32 sums in a row of n values
+(pairwise over at least 8 threads: at most (n / 8 + 12) 2^-24, below 2^-14 for
+n <= 8192) and the SFU's exponential in the bf16 gate (2^-21): c = 2^-13.  The
+column sums over r rows run in float32 over at most r / 1 terms of a thread and
+a fixed tree: (r + 64) 2^-24 of the sum of sizes, below 2^-12 of sqrt(r) times
+the largest term at the sizes here (r <= 3000): held against sum|terms|.
+"""
+import pytest
+import torch
+
+from tests import delta_testlib as R
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from selective_state_space_36_b200 import binding
+    return binding
+
+
+def inputs(rows, dim, io, weight, bias, gate, seed=1, shift=0.4):
+    gen = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=gen, dtype=torch.float64)
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[io]
+    return {"x": (1.3 * n(rows, dim) + shift).to(dt), "dout": n(rows, dim).to(dt),
+            "weight": (1 + 0.3 * n(dim)).float() if weight else None, "bias": (0.2 * n(dim)).float() if bias else None,
+            "z": n(rows, dim).to(dt) if gate else None}
+
+
+def near(got, ref, what, big=None):
+    half = torch.finfo(got.dtype).eps / 2
+    got, ref = got.detach().double().cpu(), ref.double()
+    assert got.shape == ref.shape, what
+    if not got.numel():
+        return
+    assert torch.isfinite(got).all(), what
+    if big is None:
+        big = ref.abs().amax(-1, keepdim=True)
+    over = (got - ref).abs() - half * ref.abs() - 2.0 ** -13 * big
+    assert over.max() <= 0, f"{what}: {over.max():.3e} over the bound"
+
+
+CASES = [
+    # rows, dim, io, mode, weight, bias, gate
+    (1, 1, "f32", "rms", True, True, True), (3, 2, "bf16", "layer", True, False, False),
+    (5, 64, "bf16", "rms", True, False, True), (130, 128, "bf16", "rms", True, False, True),
+    (33, 40, "bf16", "layer", False, False, True), (17, 256, "f32", "layer", True, True, False),
+    (9, 515, "f32", "layer", True, True, True), (40, 768, "bf16", "layer", True, True, False),
+    (7, 1000, "bf16", "layer", True, True, True), (600, 2048, "bf16", "layer", True, True, False),
+    (3, 4096, "f32", "rms", False, True, True), (700, 1023, "bf16", "rms", True, True, True),
+    (2, 8192, "bf16", "layer", True, True, True), (2, 8193, "bf16", "layer", True, True, True),
+    (5, 20000, "f32", "rms", True, False, False), (3000, 24, "bf16", "layer", True, True, True),
+]
+
+
+@gpu
+@pytest.mark.parametrize("rows,dim,io,mode,weight,bias,gate", CASES)
+def test_forward_and_gradient(lib, rows, dim, io, mode, weight, bias, gate):
+    x = inputs(rows, dim, io, weight, bias, gate)
+    d = {n: v.cuda() if v is not None else None for n, v in x.items()}
+    eps = 1e-5
+    out, mean, rstd = lib.norm_fwd(d["x"], d["weight"], d["bias"], z=d["z"], eps=eps, mode=mode)
+    leaf = {n: x[n].double().requires_grad_() for n in ("x", "weight", "bias", "z") if x[n] is not None}
+    ro, rm, rr = R.norm_ref(leaf["x"], leaf.get("weight"), leaf.get("bias"), leaf.get("z"), eps, mode)
+    near(out, ro, "out")
+    near(rstd[..., None], rr[..., None], "rstd")
+    assert (mean is None) == (mode == "rms")
+    if mean is not None:
+        near(mean[..., None], rm[..., None], "mean", x["x"].double().abs().mean(-1, keepdim=True))
+    g = lib.norm_bwd(d["x"], d["weight"], d["dout"], rstd, mean=mean, bias=d["bias"], z=d["z"])
+    ref = dict(zip(leaf, torch.autograd.grad(ro, list(leaf.values()), x["dout"].double())))
+    # a row of few values loses its gradient by cancellation (dim 1, 2: it is almost zero): against the terms' size
+    terms = (x["dout"].double() * (leaf["weight"].detach() if weight else 1) * rr.detach()[..., None]).abs()
+    near(g["dx"], ref["x"], "dx", 4 * terms.amax(-1, keepdim=True))
+    assert (g["dz"] is None) == (not gate) and (g["dweight"] is None) == (not weight)
+    if gate:
+        near(g["dz"], ref["z"], "dz")
+    dy = x["dout"].double() * ((x["z"].double() * torch.sigmoid(x["z"].double())) if gate else 1)
+    xh = (x["x"].double() - (rm.detach()[..., None] if rm is not None else 0)) * rr.detach()[..., None]
+    if weight:
+        near(g["dweight"], ref["weight"], "dweight", (dy * xh).abs().sum(0))
+    if bias:
+        near(g["dbias"], ref["bias"], "dbias", dy.abs().sum(0))
+    again = lib.norm_bwd(d["x"], d["weight"], d["dout"], rstd, mean=mean, bias=d["bias"], z=d["z"])
+    for n, v in g.items():
+        assert v is None or torch.equal(v, again[n]), n
+
+
+@gpu
+def test_large_mean_and_unaligned(lib):
+    """A mean far above the deviations keeps them; pointers off vector alignment."""
+    x = inputs(20, 256, "f32", True, True, True, shift=1000.0)
+
+    def off(t):
+        room = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        room[1:] = t.reshape(-1).cuda()
+        return room[1:].view(t.shape)
+
+    y = {n: off(v) for n, v in x.items()}
+    out, mean, rstd = lib.norm_fwd(y["x"], y["weight"], y["bias"], z=y["z"], out=off(x["x"]))
+    ro, rm, rr = R.norm_ref(x["x"], x["weight"], x["bias"], x["z"], 1e-5, "layer")
+    # the mean is a float32 near 1000: half a step of it (2^-15) in every deviation
+    big = ro.abs().amax(-1, keepdim=True) + 2.0 ** -15 * 2 ** 13 * 4 * rr[..., None]
+    near(out, ro, "out", big)
+    near(mean[..., None], rm[..., None], "mean")
+    g = lib.norm_bwd(y["x"], y["weight"], y["dout"], rstd, mean=mean, bias=y["bias"], z=y["z"])
+    g2 = lib.norm_bwd(x["x"].cuda(), x["weight"].cuda(), x["dout"].cuda(), rstd, mean=mean, bias=x["bias"].cuda(),
+                      z=x["z"].cuda())
+    for n in g:
+        near(g[n], g2[n].cpu(), n)
+
+
+@gpu
+def test_gate_limits_and_guards(lib):
+    """silu of far values, and nothing written beside the outputs."""
+    x = inputs(6, 48, "bf16", True, False, True)
+    x["z"][0, :6] = torch.tensor([-500.0, 500.0, 0.0, -88.0, 88.0, -30.0])
+    d = {n: v.cuda() if v is not None else None for n, v in x.items()}
+    room = torch.full((6 * 48 + 64,), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = room[32:-32].view(6, 48)
+    _, _, rstd = lib.norm_fwd(d["x"], d["weight"], z=d["z"], mode="rms", out=out)
+    ro, _, _ = R.norm_ref(x["x"], x["weight"], None, x["z"], 1e-5, "rms")
+    near(out, ro, "out")
+    assert (room[:32] == 3).all() and (room[-32:] == 3).all()
+    g = lib.norm_bwd(d["x"], d["weight"], d["dout"], rstd, z=d["z"])
+    assert all(torch.isfinite(v.float()).all() for v in g.values() if v is not None)
+
+
+@gpu
+def test_captured_graph(lib):
+    x = inputs(300, 768, "bf16", True, True, True)
+    d = {n: v.cuda() for n, v in x.items()}
+    _, mean, rstd = lib.norm_fwd(d["x"], d["weight"], d["bias"], z=d["z"])
+    ref = lib.norm_bwd(d["x"], d["weight"], d["dout"], rstd, mean=mean, bias=d["bias"], z=d["z"])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, m, r = lib.norm_fwd(d["x"], d["weight"], d["bias"], z=d["z"])
+        got = lib.norm_bwd(d["x"], d["weight"], d["dout"], r, mean=m, bias=d["bias"], z=d["z"])
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        for n in ref:
+            assert torch.equal(got[n], ref[n]), n
+
+
+def test_empty_and_refused():
+    """Host-side checks (no GPU)."""
+    from selective_state_space_36_b200 import binding as b
+    p = dict(x=0x10000, weight=0x20000, bias=None, z=None, out=0x30000, mean=None, rstd=0x40000)
+
+    def fwd(rows=4, dim=8, io=1, mode=0, eps=1e-5, **kw):
+        a = dict(p, **kw)
+        return b.lib.ssm_norm_fwd(rows, dim, io, mode, a["x"], a["weight"], a["bias"], a["z"], eps, a["out"], a["mean"],
+                                  a["rstd"], None)
+
+    assert fwd(io=4) == b.SSM_ERR_INVALID_ARG
+    assert fwd(mode=2) == b.SSM_ERR_INVALID_ARG
+    assert fwd(rows=-1) == b.SSM_ERR_INVALID_ARG
+    assert fwd(eps=-1.0) == b.SSM_ERR_INVALID_ARG
+    assert fwd(eps=float("nan")) == b.SSM_ERR_INVALID_ARG
+    assert fwd(mode=1, mean=0x50000) == b.SSM_ERR_INVALID_ARG
+    assert fwd(x=None) == b.SSM_ERR_INVALID_ARG
+    assert fwd(x=0x10001) == b.SSM_ERR_INVALID_ARG
+    assert fwd(weight=0x20002) == b.SSM_ERR_INVALID_ARG
+    assert fwd(dim=1 << 25) == b.SSM_ERR_UNSUPPORTED
+    assert fwd(rows=0, x=None) == b.SSM_OK and fwd(dim=0, x=None) == b.SSM_OK
+
+    def bwd(rows=4, dim=8, mode=1, **kw):
+        a = dict(x=0x10000, weight=0x20000, bias=None, z=None, mean=None, rstd=0x40000, dout=0x50000, dx=0x60000,
+                 dz=None, dw=None, db=None)
+        a.update(kw)
+        return b.lib.ssm_norm_bwd(rows, dim, 1, mode, a["x"], a["weight"], a["bias"], a["z"], a["mean"], a["rstd"],
+                                  a["dout"], a["dx"], a["dz"], a["dw"], a["db"], None)
+
+    assert bwd(mode=0) == b.SSM_ERR_INVALID_ARG            # a layer norm's gradient needs its mean
+    assert bwd(mean=0x70000) == b.SSM_ERR_INVALID_ARG      # an RMS norm has none
+    assert bwd(z=0x70000) == b.SSM_ERR_INVALID_ARG and bwd(dz=0x70000) == b.SSM_ERR_INVALID_ARG
+    assert bwd(rstd=None) == b.SSM_ERR_INVALID_ARG
+    assert bwd(dw=0x70002) == b.SSM_ERR_INVALID_ARG
+    assert bwd(dim=0, x=None) == b.SSM_OK and bwd(rows=0, x=None) == b.SSM_OK
+    with pytest.raises(KeyError):
+        b.norm_fwd(torch.zeros(2, 4), mode="batch")
+    with pytest.raises(ValueError):
+        b.norm_fwd(torch.zeros(2, 4), torch.ones(5))
