@@ -7,6 +7,7 @@ the library is missing this module raises at import; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -146,6 +147,9 @@ def _io_of(t: torch.Tensor) -> int:
 def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, device=None) -> Optional[int]:
     if t is None:
         return None
+    # everything in order: the usual case, in as few steps as Python allows
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr() or None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if device is not None and t.device != device:
@@ -343,9 +347,17 @@ def ssd_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
 def _stream_on(dev: torch.device, stream):
     """The stream's handle; by default the current stream of ``dev``.  The
     library launches on the current device, which therefore has to be ``dev``."""
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+    if dev.type != "cuda":
+        raise ValueError(f"tensors are on {dev}, a CUDA device is needed")
+    if dev.index != torch.cuda.current_device():
         raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return _stream_handle(stream)
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream_handle(stream)
+
+
+@functools.lru_cache(maxsize=256)
+def _ssd_dims(batch, seqlen, heads, headdim, groups, dstate) -> SSMSsdDims:
+    """The sizes as the C structure (read only: calls take it by value)."""
+    return SSMSsdDims(batch, seqlen, heads, headdim, groups, dstate)
 
 
 def delta_rule_fwd(q, k, v, g, beta, scale: Optional[float] = None, out=None, last_state=None, stream=None):
@@ -362,11 +374,11 @@ def delta_rule_fwd(q, k, v, g, beta, scale: Optional[float] = None, out=None, la
     if out is None:
         out = torch.empty_like(v)
     qk, hs = (batch, seqlen, groups, dstate), (batch, seqlen, heads)
-    args = [_ptr(q, "q", v.dtype, qk, dev), _ptr(k, "k", v.dtype, qk, dev), _ptr(v, "v", v.dtype, None, dev),
+    args = [_ptr(q, "q", v.dtype, qk, dev), _ptr(k, "k", v.dtype, qk, dev), _ptr(v, "v", v.dtype, v.shape, dev),
             _ptr(g, "g", torch.float32, hs, dev), _ptr(beta, "beta", torch.float32, hs, dev),
             float(dstate ** -0.5 if scale is None else scale), _ptr(out, "out", v.dtype, v.shape, dev),
             _ptr(last_state, "last_state", torch.float32, (batch, heads, headdim, dstate), dev)]
-    check(lib.ssm_delta_rule_fwd(SSMSsdDims(batch, seqlen, heads, headdim, groups, dstate), io, *args,
+    check(lib.ssm_delta_rule_fwd(_ssd_dims(batch, seqlen, heads, headdim, groups, dstate), io, *args,
                                  _stream_on(dev, stream)))
     return out
 
@@ -384,10 +396,10 @@ def delta_rule_update(state, q, k, v, g, beta, scale: Optional[float] = None, ou
         out = torch.empty_like(v)
     qk, hs = (batch, groups, dstate), (batch, heads)
     args = [_ptr(state, "state", torch.float32, (batch, heads, headdim, dstate), dev),
-            _ptr(q, "q", v.dtype, qk, dev), _ptr(k, "k", v.dtype, qk, dev), _ptr(v, "v", v.dtype, None, dev),
+            _ptr(q, "q", v.dtype, qk, dev), _ptr(k, "k", v.dtype, qk, dev), _ptr(v, "v", v.dtype, v.shape, dev),
             _ptr(g, "g", torch.float32, hs, dev), _ptr(beta, "beta", torch.float32, hs, dev),
             float(dstate ** -0.5 if scale is None else scale), _ptr(out, "out", v.dtype, v.shape, dev)]
-    check(lib.ssm_delta_rule_update(SSMSsdDims(batch, 1, heads, headdim, groups, dstate), io, *args,
+    check(lib.ssm_delta_rule_update(_ssd_dims(batch, 1, heads, headdim, groups, dstate), io, *args,
                                     _stream_on(dev, stream)))
     return out
 
@@ -406,7 +418,7 @@ def norm_fwd(x, weight=None, bias=None, z=None, eps: float = 1e-5, mode: str = "
         out = torch.empty_like(x)
     rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
     mean = torch.empty_like(rstd) if mode == "layer" else None
-    args = [_ptr(x, "x", x.dtype, None, dev), _ptr(weight, "weight", torch.float32, (dim,), dev),
+    args = [_ptr(x, "x", x.dtype, x.shape, dev), _ptr(weight, "weight", torch.float32, (dim,), dev),
             _ptr(bias, "bias", torch.float32, (dim,), dev), _ptr(z, "z", x.dtype, x.shape, dev), float(eps),
             _ptr(out, "out", x.dtype, x.shape, dev), _ptr(mean, "mean"), _ptr(rstd, "rstd")]
     check(lib.ssm_norm_fwd(rows, dim, io, NORM_MODES[mode], *args, _stream_on(dev, stream)))
@@ -426,7 +438,7 @@ def norm_bwd(x, weight, dout, rstd, mean=None, bias=None, z=None, stream=None):
     g = {"dx": torch.empty_like(x), "dz": torch.empty_like(x) if z is not None else None,
          "dweight": torch.empty((dim,), **f32) if weight is not None else None,
          "dbias": torch.empty((dim,), **f32) if bias is not None else None}
-    args = [_ptr(x, "x", x.dtype, None, dev), _ptr(weight, "weight", torch.float32, (dim,), dev),
+    args = [_ptr(x, "x", x.dtype, x.shape, dev), _ptr(weight, "weight", torch.float32, (dim,), dev),
             _ptr(bias, "bias", torch.float32, (dim,), dev), _ptr(z, "z", x.dtype, x.shape, dev),
             _ptr(mean, "mean", torch.float32, x.shape[:-1], dev), _ptr(rstd, "rstd", torch.float32, x.shape[:-1], dev),
             _ptr(dout, "dout", x.dtype, x.shape, dev)] + [_ptr(g[n], n) for n in ("dx", "dz", "dweight", "dbias")]

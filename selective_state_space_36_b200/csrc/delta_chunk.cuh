@@ -1,0 +1,116 @@
+// delta_chunk.cuh -- device helpers shared by the chunked kernels of the gated
+// delta rule: the chunk workspace, warp-level bf16 matrix products with
+// operands split into two bf16 terms, and the loads of a chunk's tiles.
+//
+// Chunks of C = 64 tokens.  With G_t the sum of the log decays of the chunk's
+// tokens up to t and Gam_ts = exp(G_t - G_s) for s <= t, the definition's
+// recurrence inside a chunk that starts from the state S0 is
+//   r = (I - N diag(beta)) (V - diag(exp G) K S0^T),    u = beta r
+//   O = scale diag(exp G) Q S0^T + P u,                 P = scale lower(Gam o Q K^T)
+//   S1 = exp(G_C) S0 + u^T diag(exp(G_C - G)) K
+// where N solves N = Abar - Abar diag(beta) N, Abar = strict_lower(Gam o K K^T)
+// (so that I - N diag(beta) is the inverse of I + Abar diag(beta); N itself
+// has no division by beta, which may be zero).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cp_async.cuh"
+#include "delta_rule.cuh"
+
+namespace ssm {
+namespace delta {
+
+constexpr int kC = 64;        // tokens per chunk
+constexpr int kMatLd = 72;    // row stride of a 64 x 64 bf16 tile in shared memory (conflict-free ldmatrix)
+constexpr int kMats = 4;      // per chunk and head: N high, N low, P high, P low, each 64 x 64
+constexpr int kDec = 3;       // per chunk and head: exp(G_t), exp(G_C - G_t), beta_t (zero behind the end)
+
+typedef __nv_bfloat16 bf16;
+
+// ------------------------------------------------------ matrix instructions
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], const bf16 *p) {
+    const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], const bf16 *p) {
+    const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void stm4t(bf16 *p, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n"
+                 ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+}
+// c (16 x 8) += a (16 x 16) b (16 x 8)
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};\n"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+__device__ __forceinline__ float low_of(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float high_of(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+
+// x, y as two bf16 terms each: x = hi + lo up to 2^-17 of |x| (the low term is
+// the bf16 rounding of the remainder, which float32 holds exactly).  Products
+// of two such operands drop low x low, 2^-16 of the product at most: the
+// accuracy of a state or gradient sum stays near float32's while the matrix
+// instructions run on bf16.
+__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack(x, y);
+    lo = pack(x - low_of(hi), y - high_of(hi));
+}
+
+// Row and column this lane addresses in a 16 x 16 block of ldmatrix.x4:
+// "rows first" gives registers (rows 0-7, 8-15) x (columns 0-7) then columns
+// 8-15; "columns first" the columns of rows 0-7, then those of rows 8-15.
+__device__ __forceinline__ int rows_first_row(int lane) { return (lane & 7) + ((lane >> 3) & 1) * 8; }
+__device__ __forceinline__ int rows_first_col(int lane) { return (lane >> 4) * 8; }
+__device__ __forceinline__ int cols_first_row(int lane) { return (lane & 7) + (lane >> 4) * 8; }
+__device__ __forceinline__ int cols_first_col(int lane) { return ((lane >> 3) & 1) * 8; }
+
+// ------------------------------------------------------------- tile loads
+// rows x cols of a row-major global matrix (row stride gld elements) into
+// shared memory (row stride sld), zeros outside [0, have_rows) x [0, have_cols).
+// VEC: rows start 16-byte aligned and have_cols is a multiple of 8 (an
+// asynchronous copy of 16 bytes at a time); otherwise element by element.
+template <bool VEC>
+__device__ __forceinline__ void load_tile(bf16 *s, int sld, const bf16 *g, int64_t gld, int rows, int cols,
+                                          int have_rows, int have_cols, int tid, int nthreads) {
+    if (VEC) {
+        const int per = cols / 8;
+        for (int i = tid; i < rows * per; i += nthreads) {
+            const int r = i / per, c = (i - r * per) * 8;
+            const bool in = r < have_rows && c < have_cols;
+            cp_async16(s + r * sld + c, in ? g + r * gld + c : g, in);
+        }
+    } else {
+        for (int i = tid; i < rows * cols; i += nthreads) {
+            const int r = i / cols, c = i - r * cols;
+            s[r * sld + c] = r < have_rows && c < have_cols ? g[r * gld + c] : __float2bfloat16_rn(0.f);
+        }
+    }
+}
+
+}  // namespace delta
+
+// Workspace of the chunked kernels; sizes in elements.
+struct DeltaChunkWs {
+    __nv_bfloat16 *mats;  // (batch, heads, chunks, kMats, 64, 64)
+    float *dec;           // (batch, heads, chunks, kDec, 64)
+};
+
+cudaError_t launch_delta_prep(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
+cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
+
+}  // namespace ssm

@@ -9,7 +9,7 @@
 #include <string.h>
 
 #include "../../include/ssm.h"
-#include "delta_rule.cuh"
+#include "delta_chunk.cuh"
 #include "norm.cuh"
 #include "scan_kernels.cuh"
 
@@ -844,6 +844,10 @@ void ssm_test_inject_decode_wait_timeout(int32_t enable) { g_inject_wait_bytes.s
 
 namespace {
 
+// bf16 sequences up to this many tokens run token by token (one launch, no
+// workspace), longer ones in chunks on the tensor cores.
+constexpr int64_t kDeltaRecurrentTokens = 32;
+
 // Sizes common to the delta rule's entry points; *empty: nothing to compute.
 ssm_status check_delta_dims(const ssm_ssd_dims &d, ssm_dtype io, size_t *es, bool *empty) {
     if (ssm_status s = check_io(io, es)) return s;
@@ -890,8 +894,26 @@ ssm_status delta_forward(ssm_ssd_dims dims, ssm_dtype io, const void *q, const v
         return fail(SSM_ERR_UNSUPPORTED, "grid too large");
     ssm::DeltaArgs a = delta_args(dims, q, k, v, g, beta, scale);
     a.out = out; a.h0 = h0; a.state = state;
-    cudaError_t e = ssm::launch_delta_recurrent(a, io == SSM_BF16, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (io != SSM_BF16 || dims.seqlen <= kDeltaRecurrentTokens) {
+        cudaError_t e = ssm::launch_delta_recurrent(a, io == SSM_BF16, st);
+        if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
+        return SSM_OK;
+    }
+    const int64_t units = dims.batch * dims.heads * ((dims.seqlen + ssm::delta::kC - 1) / ssm::delta::kC);
+    if (units > kMaxGridX) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+    const size_t mats = (size_t)units * ssm::delta::kMats * ssm::delta::kC * ssm::delta::kC;
+    const size_t dec = (size_t)units * ssm::delta::kDec * ssm::delta::kC;
+    void *mem = nullptr;
+    cudaError_t e = workspace_alloc(&mem, mats * 2 + dec * 4, st);
+    if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
+    ssm::DeltaChunkWs ws{static_cast<__nv_bfloat16 *>(mem),
+                         reinterpret_cast<float *>(static_cast<char *>(mem) + mats * 2)};
+    e = ssm::launch_delta_prep(a, ws, st);
+    if (e == cudaSuccess) e = ssm::launch_delta_chain(a, ws, device_info().sms, st);
+    cudaError_t ef = cudaFreeAsync(mem, st);
     if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
+    if (ef != cudaSuccess) return cuda_fail(ef, "workspace release");
     return SSM_OK;
 }
 
