@@ -25,8 +25,8 @@
  * and the exact ZOH form, _noalloc without device allocation), its gradient
  * (ssm_selective_scan_bwd, _ex), the scan with a complex diagonal A
  * (ssm_selective_scan_fwd_complex), Mamba-2's SSD layer (ssm_ssd_scan_fwd),
- * the gated delta rule (ssm_delta_rule_fwd, its token step
- * ssm_delta_rule_update), layer and RMS norm with the gate (ssm_norm_fwd, its
+ * the gated delta rule (ssm_delta_rule_fwd, its gradient ssm_delta_rule_bwd, its
+ * token step ssm_delta_rule_update), layer and RMS norm with the gate (ssm_norm_fwd, its
  * gradient ssm_norm_bwd), the one-token decode step
  * (ssm_selective_state_update), planning (ssm_scan_plan), the device status
  * word of the bounded waits (ssm_get_device_status) and error reporting.
@@ -390,6 +390,28 @@ ssm_status ssm_ssd_scan_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *x, cons
 ssm_status ssm_delta_rule_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, const void *k, const void *v,
                               const float *g, const float *beta, float scale, void *out, float *last_state,
                               ssm_stream stream);
+
+/*
+ * Gradients of sum(dout * out) + sum(dlast_state * S_L) of one
+ * ssm_delta_rule_fwd call.  Inputs as there (h0: the S_0 it started from or
+ * NULL for zero), dout (batch, seqlen, heads, headdim) io, dlast_state
+ * (batch, heads, headdim, dstate) float32 or NULL (zero).  Outputs, all
+ * written and none accumulated into:
+ *   dq, dk    : (batch, seqlen, groups, dstate) io, summed over a group's heads
+ *   dv        : (batch, seqlen, heads, headdim) io
+ *   dg, dbeta : (batch, seqlen, heads) float32
+ *   dh0       : (batch, heads, headdim, dstate) float32 or NULL (not computed).
+ * headdim <= 128 here.  No atomics: equal inputs give equal bits.  The states
+ * are recomputed: the workspace holds, per head and chunk of 64 tokens, two
+ * states and two (64, headdim) arrays at 4 bytes per value and 33 KB besides
+ * (float32 tensors: a state per 16 tokens, and per token and head headdim +
+ * 2 dstate floats), from the library's pool on "stream".  Outputs must not
+ * overlap each other or any input.
+ */
+ssm_status ssm_delta_rule_bwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, const void *k, const void *v,
+                              const float *g, const float *beta, float scale, const float *h0, const void *dout,
+                              const float *dlast_state, void *dq, void *dk, void *dv, float *dg, float *dbeta,
+                              float *dh0, ssm_stream stream);
 
 /*
  * One token of the gated delta rule (decode): ssm_delta_rule_fwd for one time

@@ -28,7 +28,8 @@ EXPORTED = ("ssm_selective_scan_fwd", "ssm_selective_scan_fwd_ex", "ssm_selectiv
             "ssm_selective_scan_bwd", "ssm_selective_scan_bwd_ex", "ssm_selective_state_update",
             "ssm_scan_plan", "ssm_get_device_status", "ssm_test_inject_decode_wait_timeout",
             "ssm_status_string", "ssm_last_error", "ssm_version", "ssm_get_build_info", "ssm_ssd_scan_fwd",
-            "ssm_test_exp2_poly", "ssm_delta_rule_fwd", "ssm_delta_rule_update", "ssm_norm_fwd", "ssm_norm_bwd")
+            "ssm_test_exp2_poly", "ssm_delta_rule_fwd", "ssm_delta_rule_bwd", "ssm_delta_rule_update",
+            "ssm_norm_fwd", "ssm_norm_bwd")
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 
@@ -112,6 +113,8 @@ def _load() -> ctypes.CDLL:
     lib.ssm_ssd_scan_fwd.restype = ctypes.c_int
     lib.ssm_delta_rule_fwd.argtypes = [SSMSsdDims, ctypes.c_int] + [_vp] * 5 + [ctypes.c_float] + [_vp] * 3
     lib.ssm_delta_rule_fwd.restype = ctypes.c_int
+    lib.ssm_delta_rule_bwd.argtypes = [SSMSsdDims, ctypes.c_int] + [_vp] * 5 + [ctypes.c_float] + [_vp] * 10
+    lib.ssm_delta_rule_bwd.restype = ctypes.c_int
     lib.ssm_delta_rule_update.argtypes = [SSMSsdDims, ctypes.c_int] + [_vp] * 6 + [ctypes.c_float] + [_vp] * 2
     lib.ssm_delta_rule_update.restype = ctypes.c_int
     norm_args = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int]
@@ -381,6 +384,33 @@ def delta_rule_fwd(q, k, v, g, beta, scale: Optional[float] = None, out=None, la
     check(lib.ssm_delta_rule_fwd(_ssd_dims(batch, seqlen, heads, headdim, groups, dstate), io, *args,
                                  _stream_on(dev, stream)))
     return out
+
+
+def delta_rule_bwd(q, k, v, g, beta, dout, scale: Optional[float] = None, h0=None, dlast_state=None,
+                   want_dh0=False, stream=None):
+    """Gradients of sum(dout * out) + sum(dlast_state * S_L) of one
+    ``delta_rule_fwd`` call; ``h0`` is the state it started from (None: zero).
+
+    Returns a dict: dq, dk, dv in v's dtype (dq, dk summed over the heads of a
+    group), dg, dbeta (batch, seqlen, heads) float32, dh0 float32 if
+    ``want_dh0`` (or h0 is given), else None."""
+    io = _io_of(v)
+    batch, seqlen, heads, headdim = v.shape
+    groups, dstate = q.shape[2], q.shape[3]
+    dev = v.device
+    qk, hs, st = (batch, seqlen, groups, dstate), (batch, seqlen, heads), (batch, heads, headdim, dstate)
+    f32 = dict(dtype=torch.float32, device=dev)
+    grads = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+             "dg": torch.empty(hs, **f32), "dbeta": torch.empty(hs, **f32),
+             "dh0": torch.empty(st, **f32) if (want_dh0 or h0 is not None) else None}
+    args = [_ptr(q, "q", v.dtype, qk, dev), _ptr(k, "k", v.dtype, qk, dev), _ptr(v, "v", v.dtype, v.shape, dev),
+            _ptr(g, "g", torch.float32, hs, dev), _ptr(beta, "beta", torch.float32, hs, dev),
+            float(dstate ** -0.5 if scale is None else scale), _ptr(h0, "h0", torch.float32, st, dev),
+            _ptr(dout, "dout", v.dtype, v.shape, dev), _ptr(dlast_state, "dlast_state", torch.float32, st, dev)]
+    args += [_ptr(grads[n], n) for n in ("dq", "dk", "dv", "dg", "dbeta", "dh0")]
+    check(lib.ssm_delta_rule_bwd(_ssd_dims(batch, seqlen, heads, headdim, groups, dstate), io, *args,
+                                 _stream_on(dev, stream)))
+    return grads
 
 
 def delta_rule_update(state, q, k, v, g, beta, scale: Optional[float] = None, out=None, stream=None):

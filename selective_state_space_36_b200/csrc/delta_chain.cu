@@ -24,7 +24,9 @@ constexpr int stage_bytes(int w) {
     return (2 * kC * (NP + 8) + kC * (16 * w + 8) + kMats * kC * kMatLd) * 2 + kDec * kC * 4;
 }
 
-template <int NP, bool VECQK, bool VECV>
+// STORE: the backward pass's first half -- no output, but the state entering
+// each chunk and r, as two bf16 terms each, go to the workspace.
+template <int NP, bool VECQK, bool VECV, bool STORE>
 __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChunkWs ws, int vtiles) {
     extern __shared__ __align__(16) unsigned char raw[];
     const int nthreads = blockDim.x, nwarps = nthreads >> 5;
@@ -41,7 +43,8 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
     const bf16 *gq = static_cast<const bf16 *>(a.q) + (b * a.seqlen * a.groups + gr) * a.dstate;
     const bf16 *gk = static_cast<const bf16 *>(a.k) + (b * a.seqlen * a.groups + gr) * a.dstate;
     const bf16 *gv = static_cast<const bf16 *>(a.v) + (b * a.seqlen * a.heads + h) * a.headdim + v0;
-    bf16 *go = static_cast<bf16 *>(a.out) + (b * a.seqlen * a.heads + h) * a.headdim + v0;
+    bf16 *go = STORE ? nullptr : static_cast<bf16 *>(a.out) + (b * a.seqlen * a.heads + h) * a.headdim + v0;
+    const int pp = (a.headdim + 15) / 16 * 16;  // rows of a stored state, columns of a stored r
 
     auto issue = [&](int64_t ch) {
         if (ch < nch) {
@@ -51,7 +54,8 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
             const int64_t t0 = ch * kC, unit = bh * nch + ch;
             const int live = (int)(a.seqlen - t0 < kC ? a.seqlen - t0 : kC);
             load_tile<VECQK>(sk, ldk, gk + t0 * qk_ld, qk_ld, kC, NP, live, a.dstate, tid, nthreads);
-            load_tile<VECQK>(sq, ldk, gq + t0 * qk_ld, qk_ld, kC, NP, live, a.dstate, tid, nthreads);
+            if (!STORE)
+                load_tile<VECQK>(sq, ldk, gq + t0 * qk_ld, qk_ld, kC, NP, live, a.dstate, tid, nthreads);
             load_tile<VECV>(sv, ldv, gv + t0 * v_ld, v_ld, kC, 16 * nwarps, live, a.headdim - v0, tid, nthreads);
             load_tile<true>(sm, kMatLd, ws.mats + unit * (kMats * kC * kC), kC, kMats * kC, kC, kMats * kC, kC, tid,
                             nthreads);
@@ -87,6 +91,7 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
         constexpr int kLow = kC * kMatLd;  // from a high term's tile to the low term's
         bf16 *mine = sv + 16 * warp;       // this warp's columns of V, later of the output
 
+        if constexpr (STORE) store_state<NP>(ws.s0 + (bh * nch + ch) * 2 * pp * NP, pp, s, v0 + 16 * warp, lane);
         float x[kC / 8][4], o[kC / 8][4];
 #pragma unroll
         for (int j = 0; j < kC / 8; ++j)
@@ -106,6 +111,7 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
                 mma(x[2 * jj + 1], hi, f[2], f[3]);
                 mma(x[2 * jj], lo, f[0], f[1]);
                 mma(x[2 * jj + 1], lo, f[2], f[3]);
+                if constexpr (STORE) continue;
                 ldm4(f, sq + (16 * jj + cf_row) * ldk + 16 * kk + cf_col);
                 mma(o[2 * jj], hi, f[0], f[1]);
                 mma(o[2 * jj + 1], hi, f[2], f[3]);
@@ -156,6 +162,9 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
                 mma(x[2 * jj + 1], hi, fl[2], fl[3]);
             }
         }
+        if constexpr (STORE) {
+            store_rows(ws.r + (bh * nch + ch) * 2 * kC * pp, pp, x, mine, ldv, v0 + 16 * warp, lane);
+        }
         // O^T += u^T P^T;  S = exp(G_C) S + (u w)^T K
         const float whole = gam[kC - 1];
 #pragma unroll
@@ -176,6 +185,7 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
             }
 #pragma unroll
             for (int jj = kk; jj < kC / 16; ++jj) {
+                if constexpr (STORE) continue;
                 uint32_t f[4], fl[4];
                 ldm4(f, sp + (16 * jj + cf_row) * kMatLd + 16 * kk + cf_col);
                 ldm4(fl, sp + kLow + (16 * jj + cf_row) * kMatLd + 16 * kk + cf_col);
@@ -196,7 +206,12 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
                 mma(s[2 * nn + 1], wlo, f[2], f[3]);
             }
         }
+        if constexpr (STORE) {
+            __syncthreads();
+            continue;
+        }
         // the output over this warp's columns of V, then to memory
+        __syncwarp();
 #pragma unroll
         for (int jj = 0; jj < kC / 16; ++jj)
             stm4t(mine + (16 * jj + cf_row) * ldv + cf_col, pack(o[2 * jj][0], o[2 * jj][1]),
@@ -234,7 +249,7 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <int NP, bool VECQK, bool VECV>
+template <int NP, bool VECQK, bool VECV, bool STORE>
 cudaError_t launch_t(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st) {
     // as many warps to a block as share its tiles of K, Q, N and P (eight
     // cover 128 columns), fewer while the grid would leave SMs empty
@@ -243,27 +258,35 @@ cudaError_t launch_t(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaSt
     while (w > 1 && a.batch * a.heads * ((a.headdim + 16 * w - 1) / (16 * w)) < sms) w = (w + 1) / 2;
     const int vtiles = (a.headdim + 16 * w - 1) / (16 * w);
     const int bytes = 2 * stage_bytes<NP>(w);
-    cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<NP, VECQK, VECV>,
+    cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<NP, VECQK, VECV, STORE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.batch * a.heads * vtiles));
-    delta_chain_kernel<NP, VECQK, VECV><<<grid, 32 * w, bytes, st>>>(a, ws, vtiles);
+    delta_chain_kernel<NP, VECQK, VECV, STORE><<<grid, 32 * w, bytes, st>>>(a, ws, vtiles);
     return cudaGetLastError();
 }
 
 }  // namespace
 }  // namespace delta
 
-cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st) {
+template <bool STORE>
+static cudaError_t launch_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st) {
     using namespace delta;
     const bool qk = a.dstate % 8 == 0 && aligned16(a.q) && aligned16(a.k);
     const bool v = a.headdim % 8 == 0 && aligned16(a.v) && aligned16(a.out);
     if (a.dstate <= 64) {
-        if (qk) return v ? launch_t<64, true, true>(a, ws, sms, st) : launch_t<64, true, false>(a, ws, sms, st);
-        return v ? launch_t<64, false, true>(a, ws, sms, st) : launch_t<64, false, false>(a, ws, sms, st);
+        if (qk) return v ? launch_t<64, true, true, STORE>(a, ws, sms, st) : launch_t<64, true, false, STORE>(a, ws, sms, st);
+        return v ? launch_t<64, false, true, STORE>(a, ws, sms, st) : launch_t<64, false, false, STORE>(a, ws, sms, st);
     }
-    if (qk) return v ? launch_t<128, true, true>(a, ws, sms, st) : launch_t<128, true, false>(a, ws, sms, st);
-    return v ? launch_t<128, false, true>(a, ws, sms, st) : launch_t<128, false, false>(a, ws, sms, st);
+    if (qk) return v ? launch_t<128, true, true, STORE>(a, ws, sms, st) : launch_t<128, true, false, STORE>(a, ws, sms, st);
+    return v ? launch_t<128, false, true, STORE>(a, ws, sms, st) : launch_t<128, false, false, STORE>(a, ws, sms, st);
+}
+
+cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st) {
+    return launch_chain<false>(a, ws, sms, st);
+}
+cudaError_t launch_delta_chain_store(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st) {
+    return launch_chain<true>(a, ws, sms, st);
 }
 
 }  // namespace ssm

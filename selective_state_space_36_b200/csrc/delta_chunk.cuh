@@ -102,15 +102,71 @@ __device__ __forceinline__ void load_tile(bf16 *s, int sld, const bf16 *g, int64
     }
 }
 
+// A warp's 16 x NP slice of a state (accumulators: rows row0 + lane / 4 (+ 8),
+// columns 8 j + 2 (lane % 4) (+ 1)) as two bf16 terms: high (pp, NP), then low.
+template <int NP>
+__device__ __forceinline__ void store_state(bf16 *dst, int pp, const float (&s)[NP / 8][4], int row0, int lane) {
+    if (row0 >= pp) return;
+#pragma unroll
+    for (int j = 0; j < NP / 8; ++j)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t hi, lo;
+            split(s[j][2 * half], s[j][2 * half + 1], hi, lo);
+            const int64_t at = (int64_t)(row0 + (lane >> 2) + 8 * half) * NP + 8 * j + 2 * (lane & 3);
+            *reinterpret_cast<uint32_t *>(dst + at) = hi;
+            *reinterpret_cast<uint32_t *>(dst + (int64_t)pp * NP + at) = lo;
+        }
+}
+
+// A warp's 16 columns of a (64, pp) matrix held transposed in accumulators
+// (x[j]: columns col0 + lane / 4 (+ 8), rows 8 j + 2 (lane % 4) (+ 1)) as two
+// bf16 terms: high (64, pp), then low.  `stage`: this warp's 16 columns of a
+// shared tile of 64 rows.
+__device__ __forceinline__ void store_rows(bf16 *dst, int pp, const float (&x)[kC / 8][4], bf16 *stage, int ld,
+                                           int col0, int lane) {
+    if (col0 >= pp) return;
+    __syncwarp();
+#pragma unroll
+    for (int term = 0; term < 2; ++term) {
+#pragma unroll
+        for (int jj = 0; jj < kC / 16; ++jj) {
+            uint32_t f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t hi, lo;
+                split(x[2 * jj + (i >> 1)][2 * (i & 1)], x[2 * jj + (i >> 1)][2 * (i & 1) + 1], hi, lo);
+                f[i] = term ? lo : hi;
+            }
+            stm4t(stage + (16 * jj + cols_first_row(lane)) * ld + cols_first_col(lane), f[0], f[1], f[2], f[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < kC / 16; ++it) {
+            const int t = 16 * it + (lane >> 1), c = 8 * (lane & 1);
+            *reinterpret_cast<uint4 *>(dst + (int64_t)(term * kC + t) * pp + col0 + c) =
+                *reinterpret_cast<const uint4 *>(stage + t * ld + c);
+        }
+        __syncwarp();
+    }
+}
+
 }  // namespace delta
 
 // Workspace of the chunked kernels; sizes in elements.
 struct DeltaChunkWs {
     __nv_bfloat16 *mats;  // (batch, heads, chunks, kMats, 64, 64)
     float *dec;           // (batch, heads, chunks, kDec, 64)
+    // backward only; headdim rounded up to 16 (pp), dstate to 64 or 128 (np)
+    __nv_bfloat16 *s0;    // (batch, heads, chunks, 2, pp, np): the state entering each chunk
+    __nv_bfloat16 *ds1;   // the same: the gradient of the state leaving it
+    __nv_bfloat16 *r, *e; // (batch, heads, chunks, 2, 64, pp): r and its gradient over beta
 };
 
 cudaError_t launch_delta_prep(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
 cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
+cudaError_t launch_delta_chain_store(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
+cudaError_t launch_delta_reverse(const DeltaBwdArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
+cudaError_t launch_delta_grad(const DeltaBwdArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
 
 }  // namespace ssm

@@ -41,9 +41,25 @@ __device__ __forceinline__ void row4(const T *row, int c, int n, float *v) {
     }
 }
 
+template <int PIECES, bool VEC>
+__device__ __forceinline__ void put_row(float *dst, const float (&s)[PIECES][4], int sub, int n) {
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+        const int c = 4 * (sub + kLanes * p);
+        if (VEC) {
+            if (c < n) *reinterpret_cast<float4 *>(dst + c) = make_float4(s[p][0], s[p][1], s[p][2], s[p][3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < n) dst[c + e] = s[p][e];
+        }
+    }
+}
+
 // PIECES pieces of four values per lane: dstate <= 32 PIECES.  VEC: dstate is
-// a multiple of 4 and q, k, the states are aligned to four elements.
-template <typename T, int PIECES, bool VEC>
+// a multiple of 4 and q, k, the states are aligned to four elements.  STORE:
+// the backward pass's first half (DeltaArgs::marks, r; no output).
+template <typename T, int PIECES, bool VEC, bool STORE>
 __global__ void __launch_bounds__(kWarps * 32) delta_recurrent_kernel(DeltaArgs a) {
     const int lane = threadIdx.x & 31, sub = lane & (kLanes - 1);
     constexpr int kRowsPerWarp = 4 * kRows;
@@ -57,7 +73,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recurrent_kernel(DeltaArgs 
     const T *q = static_cast<const T *>(a.q) + ((b * a.seqlen) * a.groups + gr) * n;
     const T *k = static_cast<const T *>(a.k) + ((b * a.seqlen) * a.groups + gr) * n;
     const T *v = static_cast<const T *>(a.v) + ((b * a.seqlen) * a.heads + h) * a.headdim;
-    T *out = static_cast<T *>(a.out) + ((b * a.seqlen) * a.heads + h) * a.headdim;
+    T *out = STORE ? nullptr : static_cast<T *>(a.out) + ((b * a.seqlen) * a.heads + h) * a.headdim;
     const float *g = a.g + (b * a.seqlen) * a.heads + h, *beta = a.beta + (b * a.seqlen) * a.heads + h;
 
     float s[kRows][PIECES][4];
@@ -85,6 +101,15 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recurrent_kernel(DeltaArgs 
         }
     }
     for (int64_t t = 0; t < a.seqlen; ++t) {
+        if (STORE && t % kDeltaStep == 0) {
+            const int64_t every = (a.seqlen + kDeltaStep - 1) / kDeltaStep;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const int row = row0 + 4 * r;
+                if (row < a.headdim)
+                    put_row<PIECES, VEC>(a.marks + ((bh * every + t / kDeltaStep) * a.headdim + row) * n, s[r], sub, n);
+            }
+        }
         float kk[PIECES][4], qq[PIECES][4];
 #pragma unroll
         for (int p = 0; p < PIECES; ++p) {
@@ -109,7 +134,9 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recurrent_kernel(DeltaArgs 
                     s[r][p][e] *= decay;
                     dot = fmaf(s[r][p][e], kk[p][e], dot);
                 }
-            const float u = bt * (vv[r] - sum8(dot));
+            const float res = vv[r] - sum8(dot), u = bt * res;
+            if (STORE && sub == 0 && row0 + 4 * r < a.headdim)
+                a.r[((b * a.seqlen + t) * a.heads + h) * a.headdim + row0 + 4 * r] = res;
             float o = 0.f;
 #pragma unroll
             for (int p = 0; p < PIECES; ++p)
@@ -120,12 +147,12 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recurrent_kernel(DeltaArgs 
                 }
             o = sum8(o);
             const int row = row0 + 4 * r;
-            if (sub == 0 && row < a.headdim) io_traits<T>::store(out + row, a.scale * o);
+            if (!STORE && sub == 0 && row < a.headdim) io_traits<T>::store(out + row, a.scale * o);
         }
         q += (int64_t)a.groups * n;
         k += (int64_t)a.groups * n;
         v += (int64_t)a.heads * a.headdim;
-        out += (int64_t)a.heads * a.headdim;
+        if (!STORE) out += (int64_t)a.heads * a.headdim;
         g += a.heads;
         beta += a.heads;
     }
@@ -134,26 +161,13 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recurrent_kernel(DeltaArgs 
     for (int r = 0; r < kRows; ++r) {
         const int row = row0 + 4 * r;
         if (row >= a.headdim) continue;
-        float *dst = a.state + (bh * a.headdim + row) * (int64_t)n;
-#pragma unroll
-        for (int p = 0; p < PIECES; ++p) {
-            const int c = 4 * (sub + kLanes * p);
-            if (VEC) {
-                if (c < n)
-                    *reinterpret_cast<float4 *>(dst + c) =
-                        make_float4(s[r][p][0], s[r][p][1], s[r][p][2], s[r][p][3]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < n) dst[c + e] = s[r][p][e];
-            }
-        }
+        put_row<PIECES, VEC>(a.state + (bh * a.headdim + row) * (int64_t)n, s[r], sub, n);
     }
 }
 
 bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-template <typename T>
+template <typename T, bool STORE>
 cudaError_t launch_t(const DeltaArgs &a, cudaStream_t st) {
     const int tiles = (a.headdim + kWarps * 4 * kRows - 1) / (kWarps * 4 * kRows);
     const int64_t blocks = a.batch * a.heads * tiles;
@@ -161,14 +175,14 @@ cudaError_t launch_t(const DeltaArgs &a, cudaStream_t st) {
                      aligned_to(a.h0, 16) && aligned_to(a.state, 16);
     const dim3 grid((unsigned)blocks), block(kWarps * 32);
     if (a.dstate <= 32) {
-        if (vec) delta_recurrent_kernel<T, 1, true><<<grid, block, 0, st>>>(a);
-        else delta_recurrent_kernel<T, 1, false><<<grid, block, 0, st>>>(a);
+        if (vec) delta_recurrent_kernel<T, 1, true, STORE><<<grid, block, 0, st>>>(a);
+        else delta_recurrent_kernel<T, 1, false, STORE><<<grid, block, 0, st>>>(a);
     } else if (a.dstate <= 64) {
-        if (vec) delta_recurrent_kernel<T, 2, true><<<grid, block, 0, st>>>(a);
-        else delta_recurrent_kernel<T, 2, false><<<grid, block, 0, st>>>(a);
+        if (vec) delta_recurrent_kernel<T, 2, true, STORE><<<grid, block, 0, st>>>(a);
+        else delta_recurrent_kernel<T, 2, false, STORE><<<grid, block, 0, st>>>(a);
     } else {
-        if (vec) delta_recurrent_kernel<T, 4, true><<<grid, block, 0, st>>>(a);
-        else delta_recurrent_kernel<T, 4, false><<<grid, block, 0, st>>>(a);
+        if (vec) delta_recurrent_kernel<T, 4, true, STORE><<<grid, block, 0, st>>>(a);
+        else delta_recurrent_kernel<T, 4, false, STORE><<<grid, block, 0, st>>>(a);
     }
     return cudaGetLastError();
 }
@@ -176,7 +190,8 @@ cudaError_t launch_t(const DeltaArgs &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool bf16, cudaStream_t st) {
-    return bf16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<float>(a, st);
+    if (a.marks) return bf16 ? launch_t<__nv_bfloat16, true>(a, st) : launch_t<float, true>(a, st);
+    return bf16 ? launch_t<__nv_bfloat16, false>(a, st) : launch_t<float, false>(a, st);
 }
 
 }  // namespace ssm

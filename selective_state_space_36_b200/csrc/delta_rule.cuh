@@ -24,10 +24,31 @@ struct DeltaArgs {
     float *state;              // the same shape or null (not returned); may be h0
     int64_t batch, seqlen;
     int heads, groups, headdim, dstate;
+    // backward in float32: the state before every kDeltaStep-th token
+    // (batch, heads, ceil(seqlen / kDeltaStep), headdim, dstate) and
+    // r = v - a S k (batch, seqlen, heads, headdim); null: not stored
+    float *marks, *r;
+};
+
+constexpr int kDeltaStep = 16;
+
+struct DeltaBwdArgs {
+    DeltaArgs f;               // the forward call's inputs; f.h0 its start state or null
+    const void *dout;          // (batch, seqlen, heads, headdim)
+    const float *dend;         // gradient of the end state or null (zero)
+    void *dq, *dk, *dv;
+    float *dg, *dbeta, *dh0;   // dh0 may be null
+    // float32 path: dq, dk of each head (batch, seqlen, heads, dstate), summed
+    // over a group's heads by a kernel of its own
+    float *dq_heads, *dk_heads;
 };
 
 // One warp group per few state rows, token after token in fp32: any sizes and
 // alignment, both element types; the decode step is seqlen == 1.
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool bf16, cudaStream_t st);
+
+// Gradients of float32 tensors, headdim and dstate up to kDeltaMaxDstate;
+// f.marks and f.r hold what launch_delta_recurrent stored.
+cudaError_t launch_delta_bwd_direct(const DeltaBwdArgs &a, cudaStream_t st);
 
 }  // namespace ssm

@@ -878,6 +878,24 @@ ssm::DeltaArgs delta_args(const ssm_ssd_dims &d, const void *q, const void *k, c
     return a;
 }
 
+// Workspace of `units` chunks; pp, np > 0: with what the backward pass keeps of
+// each (states of pp x np, r and e of 64 x pp, two bf16 terms each).
+cudaError_t delta_chunk_workspace(int64_t units, int64_t pp, int64_t np, void **mem, ssm::DeltaChunkWs *ws,
+                                  cudaStream_t st) {
+    constexpr int64_t c = ssm::delta::kC;
+    const int64_t mats = ssm::delta::kMats * c * c, dec = ssm::delta::kDec * c, state = 2 * pp * np, rows = 2 * c * pp;
+    cudaError_t e = workspace_alloc(mem, (size_t)units * (size_t)(2 * (mats + 2 * state + 2 * rows) + 4 * dec), st);
+    if (e != cudaSuccess) return e;
+    __nv_bfloat16 *at = static_cast<__nv_bfloat16 *>(*mem);
+    ws->mats = at; at += units * mats;
+    ws->s0 = at; at += units * state;
+    ws->ds1 = at; at += units * state;
+    ws->r = at; at += units * rows;
+    ws->e = at; at += units * rows;
+    ws->dec = reinterpret_cast<float *>(at);
+    return cudaSuccess;
+}
+
 ssm_status delta_forward(ssm_ssd_dims dims, ssm_dtype io, const void *q, const void *k, const void *v,
                          const float *g, const float *beta, float scale, void *out, const float *h0,
                          float *state, ssm_stream stream) {
@@ -902,13 +920,10 @@ ssm_status delta_forward(ssm_ssd_dims dims, ssm_dtype io, const void *q, const v
     }
     const int64_t units = dims.batch * dims.heads * ((dims.seqlen + ssm::delta::kC - 1) / ssm::delta::kC);
     if (units > kMaxGridX) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
-    const size_t mats = (size_t)units * ssm::delta::kMats * ssm::delta::kC * ssm::delta::kC;
-    const size_t dec = (size_t)units * ssm::delta::kDec * ssm::delta::kC;
     void *mem = nullptr;
-    cudaError_t e = workspace_alloc(&mem, mats * 2 + dec * 4, st);
+    ssm::DeltaChunkWs ws{};
+    cudaError_t e = delta_chunk_workspace(units, 0, 0, &mem, &ws, st);
     if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
-    ssm::DeltaChunkWs ws{static_cast<__nv_bfloat16 *>(mem),
-                         reinterpret_cast<float *>(static_cast<char *>(mem) + mats * 2)};
     e = ssm::launch_delta_prep(a, ws, st);
     if (e == cudaSuccess) e = ssm::launch_delta_chain(a, ws, device_info().sms, st);
     cudaError_t ef = cudaFreeAsync(mem, st);
@@ -936,6 +951,82 @@ ssm_status ssm_delta_rule_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, co
                               ssm_stream stream) {
     g_last_error[0] = 0;
     return delta_forward(dims, io, q, k, v, g, beta, scale, out, last_state, last_state, stream);
+}
+
+ssm_status ssm_delta_rule_bwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, const void *k, const void *v,
+                              const float *g, const float *beta, float scale, const float *h0, const void *dout,
+                              const float *dlast_state, void *dq, void *dk, void *dv, float *dg, float *dbeta,
+                              float *dh0, ssm_stream stream) {
+    g_last_error[0] = 0;
+    size_t es = 0;
+    bool empty = false;
+    if (ssm_status s = check_delta_dims(dims, io, &es, &empty)) return s;
+    if (dims.headdim > ssm::kDeltaMaxDstate)
+        return fail(SSM_ERR_UNSUPPORTED, "headdim %lld > %d in the backward pass", (long long)dims.headdim,
+                    ssm::kDeltaMaxDstate);
+    if (misaligned(q, es) || misaligned(k, es) || misaligned(v, es) || misaligned(dout, es) || misaligned(dq, es) ||
+        misaligned(dk, es) || misaligned(dv, es) || misaligned(g, 4) || misaligned(beta, 4) || misaligned(h0, 4) ||
+        misaligned(dlast_state, 4) || misaligned(dg, 4) || misaligned(dbeta, 4) || misaligned(dh0, 4))
+        return fail(SSM_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (empty) {
+        // no token: the end state is the start state; no state: no gradient
+        if (dims.heads > INT64_MAX / 128 / 128 || dims.groups > INT64_MAX / 128 / 4 ||
+            (dims.batch && dims.seqlen > INT64_MAX / 512 / dims.batch / (dims.heads + dims.groups)) ||
+            (dims.batch && dims.heads && dims.batch > INT64_MAX / 65536 / dims.heads))
+            return fail(SSM_ERR_INVALID_ARG, "sizes overflow");
+        const size_t hn = (size_t)dims.batch * dims.heads * dims.headdim * dims.dstate * 4;
+        const size_t bl = (size_t)dims.batch * dims.seqlen;
+        cudaError_t e = cudaSuccess;
+        if (dh0 && hn)
+            e = dlast_state ? cudaMemcpyAsync(dh0, dlast_state, hn, cudaMemcpyDeviceToDevice, st)
+                            : cudaMemsetAsync(dh0, 0, hn, st);
+        struct Z { void *p; size_t n; } zs[] = {{dq, bl * dims.groups * dims.dstate * es}, {dk, bl * dims.groups * dims.dstate * es},
+                                               {dg, bl * dims.heads * 4}, {dbeta, bl * dims.heads * 4}};
+        for (const Z &zz : zs)
+            if (e == cudaSuccess && zz.p && zz.n) e = cudaMemsetAsync(zz.p, 0, zz.n, st);
+        return e == cudaSuccess ? SSM_OK : cuda_fail(e, "zeroing gradients");
+    }
+    if (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta)
+        return fail(SSM_ERR_INVALID_ARG, "q, k, v, g, beta, dout, dq, dk, dv, dg and dbeta are required");
+    ssm::DeltaBwdArgs p{};
+    p.f = delta_args(dims, q, k, v, g, beta, scale);
+    p.f.h0 = h0;
+    p.dout = dout; p.dend = dlast_state;
+    p.dq = dq; p.dk = dk; p.dv = dv; p.dg = dg; p.dbeta = dbeta; p.dh0 = dh0;
+    const int64_t step = io == SSM_BF16 ? ssm::delta::kC : ssm::kDeltaStep;
+    const int64_t units = dims.batch * dims.heads * ((dims.seqlen + step - 1) / step);
+    const int64_t tokens = dims.batch * dims.seqlen;
+    if (units > kMaxGridX || dims.batch * dims.heads > kMaxGridX / 8 ||
+        tokens > (int64_t)kMaxGridX * 256 / (dims.groups * dims.dstate))
+        return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+    void *mem = nullptr;
+    cudaError_t e;
+    if (io == SSM_BF16) {
+        ssm::DeltaChunkWs ws{};
+        const int sms = device_info().sms;
+        e = delta_chunk_workspace(units, (dims.headdim + 15) / 16 * 16, dims.dstate <= 64 ? 64 : 128, &mem, &ws, st);
+        if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
+        e = ssm::launch_delta_prep(p.f, ws, st);
+        if (e == cudaSuccess) e = ssm::launch_delta_chain_store(p.f, ws, sms, st);
+        if (e == cudaSuccess) e = ssm::launch_delta_reverse(p, ws, sms, st);
+        if (e == cudaSuccess) e = ssm::launch_delta_grad(p, ws, st);
+    } else {
+        const size_t marks = (size_t)units * dims.headdim * dims.dstate, r = (size_t)tokens * dims.heads * dims.headdim;
+        const size_t per_head = (size_t)tokens * dims.heads * dims.dstate;
+        e = workspace_alloc(&mem, 4 * (marks + r + 2 * per_head), st);
+        if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
+        p.f.marks = static_cast<float *>(mem);
+        p.f.r = p.f.marks + marks;
+        p.dq_heads = p.f.r + r;
+        p.dk_heads = p.dq_heads + per_head;
+        e = ssm::launch_delta_recurrent(p.f, false, st);
+        if (e == cudaSuccess) e = ssm::launch_delta_bwd_direct(p, st);
+    }
+    cudaError_t ef = cudaFreeAsync(mem, st);
+    if (e != cudaSuccess) return cuda_fail(e, "delta rule gradient launch");
+    if (ef != cudaSuccess) return cuda_fail(ef, "workspace release");
+    return SSM_OK;
 }
 
 ssm_status ssm_delta_rule_update(ssm_ssd_dims dims, ssm_dtype io, float *state, const void *q, const void *k,

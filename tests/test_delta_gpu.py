@@ -25,7 +25,7 @@ def lib():
     return binding
 
 
-def near(got, ref, what, heads_axis):
+def near(got, ref, what, heads_axis, sizes=None):
     assert got.shape == ref.shape, what
     half = torch.finfo(got.dtype).eps / 2
     c = 2.0 ** -11 if got.dtype == torch.bfloat16 else 2.0 ** -13
@@ -35,8 +35,22 @@ def near(got, ref, what, heads_axis):
     assert torch.isfinite(got).all(), what
     axes = [i for i in range(ref.ndim) if i not in (0, heads_axis)]
     big = ref.abs().amax(axes, keepdim=True) if axes else ref.abs()
+    if sizes is not None:
+        big = torch.maximum(big, sizes.amax(axes, keepdim=True))
     over = (got - ref).abs() - half * ref.abs() - c * big
     assert over.max() <= 0, f"{what}: {over.max():.3e} over the bound, largest value {ref.abs().max():.3e}"
+
+
+def dg_sizes(x, scale):
+    """dg_t is a sum over the chunk's tokens s >= t of q_s . dq_s and k_s . dk_s
+    (in its two parts) and of <S, dS> at the chunk's end; each product is exact
+    up to c of the sizes of its terms, not of its value: without a state before
+    the token the sum is zero and its terms are not.  The sizes: |q| . |dq| +
+    |k| . |dk| of each head alone."""
+    rep = x["v"].shape[2] // x["q"].shape[2]
+    y = {**x, "q": x["q"].repeat_interleave(rep, 2), "k": x["k"].repeat_interleave(rep, 2)}
+    g = R.delta_grads(y, scale)
+    return sum((y[n].double() * g[n]).abs().sum(-1) for n in ("q", "k"))
 
 
 def dev(x):
@@ -75,6 +89,158 @@ def test_forward(lib, batch, seqlen, heads, groups, headdim, dstate, io, decay, 
     near(out, ro, "out", 2)
     if state:
         near(end, rs, "last_state", 1)
+
+
+@gpu
+@pytest.mark.parametrize("batch,seqlen,heads,groups,headdim,dstate,io,decay,state",
+                         [s for s in SHAPES if s[4] <= 128])
+def test_gradients(lib, batch, seqlen, heads, groups, headdim, dstate, io, decay, state):
+    x = R.delta_inputs(batch, seqlen, heads, groups, headdim, dstate, io, 17, decay, state)
+    d = dev(x)
+    got = lib.delta_rule_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["dout"], scale=0.37, h0=d["h0"],
+                             dlast_state=d["dend"])
+    ref = R.delta_grads(x, 0.37)
+    for n in ("q", "k", "v", "g", "beta"):
+        near(got["d" + n], ref[n], "d" + n, 2, dg_sizes(x, 0.37) if n == "g" else None)
+    assert (got["dh0"] is None) == (not state)
+    if state:
+        near(got["dh0"], ref["h0"], "dh0", 1)
+    again = lib.delta_rule_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["dout"], scale=0.37, h0=d["h0"],
+                               dlast_state=d["dend"])
+    for n, v in got.items():
+        assert v is None or torch.equal(v, again[n]), n
+
+
+@gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_gradients_at_limits(lib, io):
+    """beta = 0 (its gradient is not zero), g = -inf, a start state without a
+    gradient of the end state and the reverse."""
+    x = R.delta_inputs(2, 140, 4, 2, 64, 48, io, 19)
+    x["beta"][0, 3::5] = 0
+    x["beta"][1, 70:] = 0
+    x["g"][0, 50] = -200.0  # exp is zero in float32
+    x["g"][0, 51] = -1e5
+    for h0, dend in ((True, False), (False, True)):
+        y = {**x, "h0": x["h0"] if h0 else None, "dend": x["dend"] if dend else None}
+        d = dev(y)
+        got = lib.delta_rule_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["dout"], scale=0.2, h0=d["h0"],
+                                 dlast_state=d["dend"], want_dh0=True)
+        ref = R.delta_grads({**y, "h0": x["h0"] if h0 else torch.zeros_like(x["h0"])}, 0.2)
+        for n in ("q", "k", "v", "g", "beta"):
+            near(got["d" + n], ref[n], "d" + n, 2, dg_sizes(y, 0.2) if n == "g" else None)
+        near(got["dh0"], ref["h0"], "dh0", 1)
+    z = {n: d[n] for n in ("q", "k", "v", "g", "beta")}
+    z["g"] = z["g"].clone()
+    z["g"][0, 50] = -float("inf")
+    inf = lib.delta_rule_bwd(z["q"], z["k"], z["v"], z["g"], z["beta"], d["dout"], scale=0.2, h0=d["h0"],
+                             dlast_state=d["dend"], want_dh0=True)
+    for n, v in got.items():
+        near(inf[n], v.cpu(), n, 1 if n == "dh0" else 2)
+
+
+@gpu
+def test_gradients_unaligned_streams_and_graph(lib):
+    x = R.delta_inputs(2, 200, 4, 2, 64, 128, "bf16", 23)
+    d = dev(x)
+    names = ("q", "k", "v", "g", "beta", "dout")
+
+    def call(y):
+        return lib.delta_rule_bwd(*(y[n] for n in names), scale=0.1, h0=y["h0"], dlast_state=y["dend"])
+
+    def off(t):
+        room = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        room[1:] = t.reshape(-1)
+        return room[1:].view(t.shape)
+
+    ref = call(d)
+    moved = call({n: off(v) for n, v in d.items()})
+    for n in ref:
+        near(moved[n], ref[n].cpu(), n, 1 if n == "dh0" else 2)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(call(d))
+        torch.cuda.synchronize()
+        for g in got:
+            assert all(torch.equal(g[n], ref[n]) for n in ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = call(d)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(held[n], ref[n]) for n in ref)
+
+
+@gpu
+def test_gradients_of_no_tokens(lib):
+    z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t, device="cuda")
+    end = torch.randn(2, 4, 64, 32, device="cuda")
+    got = lib.delta_rule_bwd(z(2, 0, 2, 32), z(2, 0, 2, 32), z(2, 0, 4, 64), z(2, 0, 4, t=torch.float32),
+                             z(2, 0, 4, t=torch.float32), z(2, 0, 4, 64), h0=end, dlast_state=end)
+    assert torch.equal(got["dh0"], end)
+    got = lib.delta_rule_bwd(z(2, 0, 2, 32), z(2, 0, 2, 32), z(2, 0, 4, 64), z(2, 0, 4, t=torch.float32),
+                             z(2, 0, 4, t=torch.float32), z(2, 0, 4, 64), h0=end)
+    assert (got["dh0"] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_layer_of_norms_and_delta_rule(lib, io):
+    """The operators as a layer runs them: L2 norm of q and k (RMS norm with
+    weight dstate^-1/2), the rule, the gated RMS norm of each head's output;
+    forward, backward through all of it, and the same tokens one at a time.
+
+    Each stage is held against float64 of the values it was given (bf16
+    intermediates of a layer are rounded between the stages), the whole against
+    float64 end to end within 2^-5 of the largest value for bf16 (eight
+    roundings of 2^-8 in a row, each possibly passed on in full), 2^-13 for
+    float32."""
+    batch, seqlen, heads, groups, P, N = 2, 90, 4, 2, 64, 32
+    x = R.delta_inputs(batch, seqlen, heads, groups, P, N, io, 29)
+    gen = torch.Generator().manual_seed(3)
+    dt = x["v"].dtype
+    raw = {n: torch.randn(batch, seqlen, groups, N, generator=gen).to(dt) for n in ("q", "k")}
+    z = torch.randn(batch, seqlen, heads, P, generator=gen).to(dt)
+    w = (1 + 0.2 * torch.randn(P, generator=gen)).float()
+    unit = torch.full((N,), N ** -0.5)
+    d, rd, zd, wd, ud = dev(x), dev(raw), z.cuda(), w.cuda(), unit.cuda()
+
+    q, _, rq = lib.norm_fwd(rd["q"], ud, eps=1e-6, mode="rms")
+    k, _, rk = lib.norm_fwd(rd["k"], ud, eps=1e-6, mode="rms")
+    y = lib.delta_rule_fwd(q, k, d["v"], d["g"], d["beta"])
+    out, _, ry = lib.norm_fwd(y, wd, z=zd, mode="rms")
+    gn = lib.norm_bwd(y, wd, d["dout"], ry, z=zd)
+    gd = lib.delta_rule_bwd(q, k, d["v"], d["g"], d["beta"], gn["dx"])
+    gq, gk = (lib.norm_bwd(rd[n], ud, gd["d" + n], r) for n, r in (("q", rq), ("k", rk)))
+
+    leaf = {"q": raw["q"].double().requires_grad_(), "k": raw["k"].double().requires_grad_(),
+            "v": x["v"].double().requires_grad_(), "z": z.double().requires_grad_(), "w": w.double().requires_grad_(),
+            "g": x["g"].double().requires_grad_(), "beta": x["beta"].double().requires_grad_()}
+    q64 = R.norm_ref(leaf["q"], unit.double(), None, None, 1e-6, "rms")[0]
+    k64 = R.norm_ref(leaf["k"], unit.double(), None, None, 1e-6, "rms")[0]
+    y64, _ = R.delta_ref(q64, k64, leaf["v"], leaf["g"], leaf["beta"], N ** -0.5)
+    o64 = R.norm_ref(y64, leaf["w"], None, leaf["z"], 1e-5, "rms")[0]
+    ref = dict(zip(leaf, torch.autograd.grad(o64, list(leaf.values()), x["dout"].double())))
+    tol = 2.0 ** -5 if io == "bf16" else 2.0 ** -13
+    got = {"q": gq["dx"], "k": gk["dx"], "v": gd["dv"], "z": gn["dz"], "w": gn["dweight"], "g": gd["dg"],
+           "beta": gd["dbeta"]}
+    for n, r in {**ref, "out": o64.detach()}.items():
+        v = (out if n == "out" else got[n]).double().cpu()
+        assert (v - r).abs().max() <= tol * r.abs().max(), n
+
+    state = torch.zeros(batch, heads, P, N, device="cuda")
+    for t in range(seqlen):
+        tok = lambda v: v[:, t].contiguous()
+        q1, _, _ = lib.norm_fwd(tok(rd["q"]), ud, eps=1e-6, mode="rms")
+        k1, _, _ = lib.norm_fwd(tok(rd["k"]), ud, eps=1e-6, mode="rms")
+        y1 = lib.delta_rule_update(state, q1, k1, tok(d["v"]), tok(d["g"]), tok(d["beta"]))
+        o1, _, _ = lib.norm_fwd(y1, wd, z=tok(zd), mode="rms")
+        assert (o1.double().cpu() - o64[:, t]).abs().max() <= tol * o64.abs().max(), t
 
 
 @gpu
@@ -222,6 +388,25 @@ def test_empty_and_refused(request):
         assert b"aligned" in b.lib.ssm_last_error()
     for dims in [(0, 16, 4, 64, 2, 64), (2, 0, 4, 64, 2, 64), (2, 16, 0, 64, 2, 64), (2, 16, 4, 0, 2, 64)]:
         assert call(dims, q=None, out=None) == b.SSM_OK
+    names = ("q", "k", "v", "g", "beta", "scale", "h0", "dout", "dend", "dq", "dk", "dv", "dg", "dbeta", "dh0")
+    good = {n: 0x10000 * (i + 1) for i, n in enumerate(names)}
+    good["scale"] = 1.0
+
+    def back(dims, io=1, **kw):
+        p = {**good, **kw}
+        return b.lib.ssm_delta_rule_bwd(b.SSMSsdDims(*dims), io, *(p[n] for n in names), None)
+
+    assert back((2, 16, 4, 129, 2, 64)) == b.SSM_ERR_UNSUPPORTED
+    assert back((2, 16, 4, 64, 2, 129)) == b.SSM_ERR_UNSUPPORTED
+    assert back((2, 16, 5, 64, 2, 64)) == b.SSM_ERR_INVALID_ARG
+    assert back(ok, io=2) == b.SSM_ERR_INVALID_ARG
+    for name in ("q", "dout", "dq", "dk", "dv", "dg", "dbeta"):
+        assert back(ok, **{name: None}) == b.SSM_ERR_INVALID_ARG
+    for name in names:
+        if name != "scale":
+            assert back(ok, **{name: good[name] + 1}) == b.SSM_ERR_INVALID_ARG
+            assert b"aligned" in b.lib.ssm_last_error()
+    assert back((0, 16, 4, 64, 2, 64)) == b.SSM_OK
     none = b.lib.ssm_delta_rule_update(b.SSMSsdDims(2, 0, 4, 64, 2, 64), 1, None, 0x10000, 0x20000, 0x30000, 0x40000,
                                        0x50000, 1.0, 0x60000, None)
     assert none == b.SSM_ERR_INVALID_ARG
