@@ -446,8 +446,10 @@ def norm_fwd(x, weight=None, bias=None, z=None, eps: float = 1e-5, mode: str = "
     dev = x.device
     if out is None:
         out = torch.empty_like(x)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    mean = torch.empty_like(rstd) if mode == "layer" else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if mode == "layer" else None
+    if x.ndim != 2:
+        rstd, mean = (None if t is None else t.view(x.shape[:-1]) for t in (rstd, mean))
     args = [_ptr(x, "x", x.dtype, x.shape, dev), _ptr(weight, "weight", torch.float32, (dim,), dev),
             _ptr(bias, "bias", torch.float32, (dim,), dev), _ptr(z, "z", x.dtype, x.shape, dev), float(eps),
             _ptr(out, "out", x.dtype, x.shape, dev), _ptr(mean, "mean"), _ptr(rstd, "rstd")]

@@ -1,17 +1,21 @@
-// delta_recurrent.cu -- the gated delta rule token by token (the decode step
-// is one token), in fp32 for both element types.
+// delta_recurrent.cu -- the gated delta rule token by token, in fp32 for both
+// element types: the decode step, and whole sequences where the chunked kernels
+// do not apply (float32 tensors) or do not pay (a few dozen tokens).
 //
 // Eight lanes share one row of the state S (headdim x dstate): a row's
 // dstate values are dealt out in pieces of four, piece i to lane i mod 8, so
 // that the eight lanes read and write 128 contiguous bytes at a time.  A
 // warp holds 4 rows at once and kRows sets of them, all in registers for the
-// whole sequence; rows are independent, so no block-wide synchronisation
-// exists.  Per token a row needs two dot products over dstate (S k and S q),
-// each reduced over its eight lanes by three shuffles.
+// whole sequence; rows are independent.  Per token a row needs two dot products
+// over dstate (S k and S q), each reduced over its eight lanes by three shuffles.
 //
 // One token moves 8 headdim dstate bytes of state per head and computes 8
 // flops per state value, so the step is bound by HBM: the loads of all
-// kRows sets are issued before the first is used.
+// kRows sets are issued before the first is used (256 sequences x 32 heads of
+// 128 x 128: 165 us, the measured copy rate).  Over a sequence the state stays
+// in registers and the chain of a token's dot products bounds the kernel; k,
+// q, v, g and beta come a stage of kTok tokens ahead through shared memory.
+#include "cp_async.cuh"
 #include "delta_rule.cuh"
 #include "ssm_device.cuh"
 
@@ -21,6 +25,7 @@ namespace {
 constexpr int kLanes = 8;             // lanes that share a state row
 constexpr int kWarps = 4;             // warps per block
 constexpr int kRows = 2;              // row sets per warp
+constexpr int kRowsPerBlock = kWarps * 4 * kRows;
 
 __device__ __forceinline__ float sum8(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -56,38 +61,21 @@ __device__ __forceinline__ void put_row(float *dst, const float (&s)[PIECES][4],
     }
 }
 
-// PIECES pieces of four values per lane: dstate <= 32 PIECES.  VEC: dstate is
-// a multiple of 4 and q, k, the states are aligned to four elements.  STORE:
-// the backward pass's first half (DeltaArgs::marks, r; no output).
-template <typename T, int PIECES, bool VEC, bool STORE>
-__global__ void __launch_bounds__(kWarps * 32) delta_recurrent_kernel(DeltaArgs a) {
-    const int lane = threadIdx.x & 31, sub = lane & (kLanes - 1);
-    constexpr int kRowsPerWarp = 4 * kRows;
-    const int tiles = (a.headdim + kWarps * kRowsPerWarp - 1) / (kWarps * kRowsPerWarp);
-    const int64_t bh = blockIdx.x / tiles;
-    const int tile = (int)(blockIdx.x % tiles);
-    const int64_t b = bh / a.heads;
-    const int h = (int)(bh % a.heads), gr = h / (a.heads / a.groups);
-    const int row0 = (tile * kWarps + (threadIdx.x >> 5)) * kRowsPerWarp + (lane >> 3);
-    const int n = a.dstate;
-    const T *q = static_cast<const T *>(a.q) + ((b * a.seqlen) * a.groups + gr) * n;
-    const T *k = static_cast<const T *>(a.k) + ((b * a.seqlen) * a.groups + gr) * n;
-    const T *v = static_cast<const T *>(a.v) + ((b * a.seqlen) * a.heads + h) * a.headdim;
-    T *out = STORE ? nullptr : static_cast<T *>(a.out) + ((b * a.seqlen) * a.heads + h) * a.headdim;
-    const float *g = a.g + (b * a.seqlen) * a.heads + h, *beta = a.beta + (b * a.seqlen) * a.heads + h;
-
-    float s[kRows][PIECES][4];
+// The state rows of this lane, kRows sets; plain loads: the state may be
+// written back to the same place.
+template <int PIECES, bool VEC>
+__device__ __forceinline__ void get_rows(float (&s)[kRows][PIECES][4], const float *h0, int64_t bh, int row0,
+                                         int headdim, int sub, int n) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
         const int row = row0 + 4 * r;
-        const float *src = a.h0 ? a.h0 + (bh * a.headdim + row) * (int64_t)n : nullptr;
+        const float *src = h0 ? h0 + (bh * headdim + row) * (int64_t)n : nullptr;
 #pragma unroll
         for (int p = 0; p < PIECES; ++p) {
             const int c = 4 * (sub + kLanes * p);
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[r][p][e] = 0.f;
-            if (!src || row >= a.headdim) continue;
-            // plain loads: the state may be written back to the same place
+            if (!src || row >= headdim) continue;
             if (VEC) {
                 if (c < n) {
                     const float4 x = *reinterpret_cast<const float4 *>(src + c);
@@ -100,16 +88,73 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recurrent_kernel(DeltaArgs 
             }
         }
     }
-    for (int64_t t = 0; t < a.seqlen; ++t) {
-        if (STORE && t % kDeltaStep == 0) {
-            const int64_t every = (a.seqlen + kDeltaStep - 1) / kDeltaStep;
+}
+
+// One token for this lane's rows: o[r] = S_t q (all eight lanes), res[r] = v - a S k.
+template <int PIECES>
+__device__ __forceinline__ void token(float (&s)[kRows][PIECES][4], const float (&kk)[PIECES][4],
+                                      const float (&qq)[PIECES][4], float decay, float beta, const float (&v)[kRows],
+                                      float (&o)[kRows], float (&res)[kRows]) {
+    float dot[kRows];
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const int row = row0 + 4 * r;
-                if (row < a.headdim)
-                    put_row<PIECES, VEC>(a.marks + ((bh * every + t / kDeltaStep) * a.headdim + row) * n, s[r], sub, n);
+    for (int r = 0; r < kRows; ++r) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};  // four short chains
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[r][p][e] *= decay;
+                d[e] = fmaf(s[r][p][e], kk[p][e], d[e]);
             }
-        }
+        dot[r] = (d[0] + d[1]) + (d[2] + d[3]);
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) dot[r] = sum8(dot[r]);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        res[r] = v[r] - dot[r];
+        const float u = beta * res[r];
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[r][p][e] = fmaf(u, kk[p][e], s[r][p][e]);
+                d[e] = fmaf(s[r][p][e], qq[p][e], d[e]);
+            }
+        o[r] = (d[0] + d[1]) + (d[2] + d[3]);
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) o[r] = sum8(o[r]);
+}
+
+// One token (decode) or a few: the tokens' operands straight from global
+// memory.  PIECES pieces of four values per lane: dstate <= 32 PIECES.  VEC:
+// dstate is a multiple of 4 and q, k, the states are aligned to four elements.
+// For 256 sequences x 32 heads of 128 x 128 the order of a warp's accesses
+// decides: 166 us with the state's loads before, and its stores after, a token
+// loop that fetches its own operands; 186 to 206 us with everything fetched
+// ahead or a loop of one token unrolled away.
+template <typename T, int PIECES, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32) delta_step_kernel(DeltaArgs a) {
+    const int lane = threadIdx.x & 31, sub = lane & (kLanes - 1);
+    constexpr int kRowsPerWarp = 4 * kRows;
+    const int tiles = (a.headdim + kWarps * kRowsPerWarp - 1) / (kWarps * kRowsPerWarp);
+    const int64_t bh = blockIdx.x / tiles;
+    const int tile = (int)(blockIdx.x % tiles);
+    const int64_t b = bh / a.heads;
+    const int h = (int)(bh % a.heads), gr = h / (a.heads / a.groups);
+    const int row0 = (tile * kWarps + (threadIdx.x >> 5)) * kRowsPerWarp + (lane >> 3);
+    const int n = a.dstate;
+    const T *q = static_cast<const T *>(a.q) + ((b * a.seqlen) * a.groups + gr) * n;
+    const T *k = static_cast<const T *>(a.k) + ((b * a.seqlen) * a.groups + gr) * n;
+    const T *v = static_cast<const T *>(a.v) + ((b * a.seqlen) * a.heads + h) * a.headdim;
+    T *out = static_cast<T *>(a.out) + ((b * a.seqlen) * a.heads + h) * a.headdim;
+    const float *g = a.g + (b * a.seqlen) * a.heads + h, *beta = a.beta + (b * a.seqlen) * a.heads + h;
+
+    float s[kRows][PIECES][4];
+    get_rows<PIECES, VEC>(s, a.h0, bh, row0, a.headdim, sub, n);
+    for (int64_t t = 0; t < a.seqlen; ++t) {
         float kk[PIECES][4], qq[PIECES][4];
 #pragma unroll
         for (int p = 0; p < PIECES; ++p) {
@@ -134,9 +179,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recurrent_kernel(DeltaArgs 
                     s[r][p][e] *= decay;
                     dot = fmaf(s[r][p][e], kk[p][e], dot);
                 }
-            const float res = vv[r] - sum8(dot), u = bt * res;
-            if (STORE && sub == 0 && row0 + 4 * r < a.headdim)
-                a.r[((b * a.seqlen + t) * a.heads + h) * a.headdim + row0 + 4 * r] = res;
+            const float u = bt * (vv[r] - sum8(dot));
             float o = 0.f;
 #pragma unroll
             for (int p = 0; p < PIECES; ++p)
@@ -147,12 +190,12 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recurrent_kernel(DeltaArgs 
                 }
             o = sum8(o);
             const int row = row0 + 4 * r;
-            if (!STORE && sub == 0 && row < a.headdim) io_traits<T>::store(out + row, a.scale * o);
+            if (sub == 0 && row < a.headdim) io_traits<T>::store(out + row, a.scale * o);
         }
         q += (int64_t)a.groups * n;
         k += (int64_t)a.groups * n;
         v += (int64_t)a.heads * a.headdim;
-        if (!STORE) out += (int64_t)a.heads * a.headdim;
+        out += (int64_t)a.heads * a.headdim;
         g += a.heads;
         beta += a.heads;
     }
@@ -165,32 +208,173 @@ __global__ void __launch_bounds__(kWarps * 32) delta_recurrent_kernel(DeltaArgs 
     }
 }
 
+constexpr int kFewTokens = 4;  // up to this many go to delta_step_kernel
+constexpr int kTok = 16;       // tokens per stage of a sequence
+
+template <typename T, int PIECES>
+struct TokenStage {
+    T k[kTok][32 * PIECES], q[kTok][32 * PIECES];
+    T v[kTok][kRowsPerBlock];
+    float decay[kTok], beta[kTok];
+};
+
+// A sequence.  ASYNC: rows of q and k are multiples of 16 bytes and start
+// aligned (copied asynchronously); VEC as above.  STORE: the backward pass's
+// first half (DeltaArgs::marks, r; no output).
+template <typename T, int PIECES, bool VEC, bool ASYNC, bool STORE>
+__global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) {
+    __shared__ __align__(16) TokenStage<T, PIECES> stages[2];
+    constexpr int kThreads = kWarps * 32;
+    const int tid = threadIdx.x, lane = tid & 31, sub = lane & (kLanes - 1), n = a.dstate;
+    const int tiles = (a.headdim + kRowsPerBlock - 1) / kRowsPerBlock;
+    const int64_t bh = blockIdx.x / tiles, b = bh / a.heads;
+    const int tile = (int)(blockIdx.x % tiles), h = (int)(bh % a.heads), gr = h / (a.heads / a.groups);
+    const int first = tile * kRowsPerBlock, mine = (tid >> 5) * 4 * kRows + (lane >> 3), row0 = first + mine;
+    const int64_t qk_ld = (int64_t)a.groups * n, v_ld = (int64_t)a.heads * a.headdim;
+    const T *q = static_cast<const T *>(a.q) + (b * a.seqlen * a.groups + gr) * n;
+    const T *k = static_cast<const T *>(a.k) + (b * a.seqlen * a.groups + gr) * n;
+    const T *v = static_cast<const T *>(a.v) + (b * a.seqlen * a.heads + h) * a.headdim + first;
+    const float *g = a.g + b * a.seqlen * a.heads + h, *beta = a.beta + b * a.seqlen * a.heads + h;
+    const int have = a.headdim - first < kRowsPerBlock ? a.headdim - first : kRowsPerBlock;
+
+    auto issue = [&](int64_t t0) {
+        if (t0 < a.seqlen) {
+            TokenStage<T, PIECES> &st = stages[(t0 / kTok) & 1];
+            const int live = (int)(a.seqlen - t0 < kTok ? a.seqlen - t0 : kTok);
+            if (ASYNC) {
+                constexpr int E = 16 / sizeof(T), PER = 32 * PIECES / E;
+                for (int i = tid; i < kTok * PER; i += kThreads) {
+                    const int t = i / PER, c = (i % PER) * E;
+                    const bool in = t < live && c < n;
+                    const int64_t at = (t0 + t) * qk_ld + c;
+                    cp_async16(&st.k[t][c], in ? k + at : k, in);
+                    cp_async16(&st.q[t][c], in ? q + at : q, in);
+                }
+            } else {
+                for (int i = tid; i < live * 32 * PIECES; i += kThreads) {
+                    const int t = i / (32 * PIECES), c = i % (32 * PIECES);
+                    st.k[t][c] = c < n ? k[(t0 + t) * qk_ld + c] : T(0.f);
+                    st.q[t][c] = c < n ? q[(t0 + t) * qk_ld + c] : T(0.f);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    // v, g and beta have rows too short for asynchronous copies: loaded into
+    // registers when a stage begins, put into the next stage's tile at its end
+    constexpr int kV = kTok * kRowsPerBlock / kThreads;
+    T rv[kV];
+    float rg = 0.f, rb = 0.f;
+    auto small_loads = [&](int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const int t = (tid + i * kThreads) / kRowsPerBlock, c = tid % kRowsPerBlock;
+            rv[i] = t0 + t < a.seqlen && c < have ? v[(t0 + t) * v_ld + c] : T(0.f);
+        }
+        if (tid < kTok && t0 + tid < a.seqlen) {
+            rg = g[(t0 + tid) * a.heads];
+            rb = beta[(t0 + tid) * a.heads];
+        }
+    };
+    auto small_stores = [&](int64_t t0) {
+        TokenStage<T, PIECES> &st = stages[(t0 / kTok) & 1];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) st.v[(tid + i * kThreads) / kRowsPerBlock][tid % kRowsPerBlock] = rv[i];
+        if (tid < kTok) {
+            st.decay[tid] = expf(rg);
+            st.beta[tid] = rb;
+        }
+    };
+
+    static_assert(kThreads % kRowsPerBlock == 0, "a thread stays in its column of v");
+    float s[kRows][PIECES][4];
+    issue(0);
+    small_loads(0);
+    small_stores(0);
+    get_rows<PIECES, VEC>(s, a.h0, bh, row0, a.headdim, sub, n);
+    for (int64_t t0 = 0; t0 < a.seqlen; t0 += kTok) {
+        issue(t0 + kTok);
+        small_loads(t0 + kTok);
+        cp_async_wait<1>();
+        __syncthreads();
+        if (STORE) {
+            static_assert(kTok == kDeltaStep, "a stored state per stage");
+            const int64_t marks = (a.seqlen + kTok - 1) / kTok;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const int row = row0 + 4 * r;
+                if (row < a.headdim)
+                    put_row<PIECES, VEC>(a.marks + ((bh * marks + t0 / kTok) * a.headdim + row) * n, s[r], sub, n);
+            }
+        }
+        const TokenStage<T, PIECES> &st = stages[(t0 / kTok) & 1];
+        const int live = (int)(a.seqlen - t0 < kTok ? a.seqlen - t0 : kTok);
+        // two tokens' operands in registers: one is loaded while the other is used
+        float kk[2][PIECES][4], qq[2][PIECES][4], vv[2][kRows];
+        auto operands = [&](int t, int at) {
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                io_traits<T>::load4_smem(&st.k[t][4 * (sub + kLanes * p)], kk[at][p]);
+                io_traits<T>::load4_smem(&st.q[t][4 * (sub + kLanes * p)], qq[at][p]);
+            }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) vv[at][r] = io_traits<T>::load_smem(&st.v[t][mine + 4 * r]);
+        };
+        operands(0, 0);
+#pragma unroll
+        for (int t = 0; t < kTok; ++t) {
+            if (t >= live) break;
+            float o[kRows], res[kRows];
+            if (t + 1 < kTok) operands(t + 1, (t + 1) & 1);
+            token<PIECES>(s, kk[t & 1], qq[t & 1], st.decay[t], st.beta[t], vv[t & 1], o, res);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const int row = row0 + 4 * r;
+                if (sub != 0 || row >= a.headdim) continue;
+                const int64_t at = ((b * a.seqlen + t0 + t) * a.heads + h) * a.headdim + row;
+                if (STORE) a.r[at] = res[r];
+                else io_traits<T>::store(static_cast<T *>(a.out) + at, a.scale * o[r]);
+            }
+        }
+        small_stores(t0 + kTok);
+        __syncthreads();
+    }
+    if (!a.state) return;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const int row = row0 + 4 * r;
+        if (row < a.headdim) put_row<PIECES, VEC>(a.state + (bh * a.headdim + row) * (int64_t)n, s[r], sub, n);
+    }
+}
+
 bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+template <typename T, int PIECES, bool VEC, bool STORE>
+cudaError_t launch_pieces(const DeltaArgs &a, bool async, cudaStream_t st) {
+    const int tiles = (a.headdim + kRowsPerBlock - 1) / kRowsPerBlock;
+    const dim3 grid((unsigned)(a.batch * a.heads * tiles)), block(kWarps * 32);
+    if (a.seqlen <= kFewTokens && !STORE) delta_step_kernel<T, PIECES, VEC><<<grid, block, 0, st>>>(a);
+    else if (async) delta_tokens_kernel<T, PIECES, VEC, true, STORE><<<grid, block, 0, st>>>(a);
+    else delta_tokens_kernel<T, PIECES, VEC, false, STORE><<<grid, block, 0, st>>>(a);
+    return cudaGetLastError();
+}
 
 template <typename T, bool STORE>
 cudaError_t launch_t(const DeltaArgs &a, cudaStream_t st) {
-    const int tiles = (a.headdim + kWarps * 4 * kRows - 1) / (kWarps * 4 * kRows);
-    const int64_t blocks = a.batch * a.heads * tiles;
     const bool vec = a.dstate % 4 == 0 && aligned_to(a.q, 4 * sizeof(T)) && aligned_to(a.k, 4 * sizeof(T)) &&
                      aligned_to(a.h0, 16) && aligned_to(a.state, 16);
-    const dim3 grid((unsigned)blocks), block(kWarps * 32);
-    if (a.dstate <= 32) {
-        if (vec) delta_recurrent_kernel<T, 1, true, STORE><<<grid, block, 0, st>>>(a);
-        else delta_recurrent_kernel<T, 1, false, STORE><<<grid, block, 0, st>>>(a);
-    } else if (a.dstate <= 64) {
-        if (vec) delta_recurrent_kernel<T, 2, true, STORE><<<grid, block, 0, st>>>(a);
-        else delta_recurrent_kernel<T, 2, false, STORE><<<grid, block, 0, st>>>(a);
-    } else {
-        if (vec) delta_recurrent_kernel<T, 4, true, STORE><<<grid, block, 0, st>>>(a);
-        else delta_recurrent_kernel<T, 4, false, STORE><<<grid, block, 0, st>>>(a);
-    }
-    return cudaGetLastError();
+    const bool async = a.dstate * sizeof(T) % 16 == 0 && aligned_to(a.q, 16) && aligned_to(a.k, 16);
+    if (a.dstate <= 32)
+        return vec ? launch_pieces<T, 1, true, STORE>(a, async, st) : launch_pieces<T, 1, false, STORE>(a, async, st);
+    if (a.dstate <= 64)
+        return vec ? launch_pieces<T, 2, true, STORE>(a, async, st) : launch_pieces<T, 2, false, STORE>(a, async, st);
+    return vec ? launch_pieces<T, 4, true, STORE>(a, async, st) : launch_pieces<T, 4, false, STORE>(a, async, st);
 }
 
 }  // namespace
 
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool bf16, cudaStream_t st) {
-    if (a.marks) return bf16 ? launch_t<__nv_bfloat16, true>(a, st) : launch_t<float, true>(a, st);
+    if (a.marks) return launch_t<float, true>(a, st);
     return bf16 ? launch_t<__nv_bfloat16, false>(a, st) : launch_t<float, false>(a, st);
 }
 

@@ -19,32 +19,17 @@
 // where dim and the pointers allow, else single values).  Rows too long for
 // the registers are walked twice (forward, dx), and their column sums come
 // from a kernel of their own over tiles of columns.
+#include "cp_async.cuh"
 #include "norm.cuh"
 #include "ssm_device.cuh"
+
+#include <type_traits>
 
 namespace ssm {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarpsPerBlock = kThreads / 32;
-
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float *v) {
-    if constexpr (VEC == 1) {
-        v[0] = io_traits<T>::load(p);
-    } else if constexpr (sizeof(T) == 4) {
-        const float4 t = __ldg(reinterpret_cast<const float4 *>(p));
-        v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-    } else {
-        const uint4 t = __ldg(reinterpret_cast<const uint4 *>(p));
-        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-}
 
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T *p, const float *v) {
@@ -73,16 +58,20 @@ __device__ __forceinline__ void load_param(const float *p, float *v, float none)
         v[0] = __ldg(p);
     } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = __ldg(p + e);
+        for (int e = 0; e < VEC; e += 4) {
+            const float4 t = __ldg(reinterpret_cast<const float4 *>(p + e));
+            v[e] = t.x; v[e + 1] = t.y; v[e + 2] = t.z; v[e + 3] = t.w;
+        }
     }
 }
 
-// sigmoid(z): fp32 I/O with the full-precision exponential, bf16 I/O with the
-// SFU's (a few fp32 ulps, far below the output's rounding)
+// sigmoid(z): fp32 I/O with the full-precision exponential and division, bf16
+// I/O with the SFU's (a few fp32 ulps, far below the output's rounding; the
+// division's extra instructions cost 20 us on 524288 gated rows of 128)
 template <bool PRECISE>
 __device__ __forceinline__ float sigmoid(float z) {
     if (PRECISE) return 1.f / (1.f + expf(-z));
-    return 1.f / (1.f + __expf(-z));
+    return rcp_approx(1.f + ex2_approx(-z * kLog2e));
 }
 
 // Sum over the TPR threads of a row, in every one of them.  `red`: two floats
@@ -100,7 +89,8 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float (*red)[kWarpsPerBlo
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
             for (int i = 0; i < N; ++i) red[flip][warp][i] = x[i];
-        __syncthreads();
+        // only the row's threads wait for one another
+        asm volatile("bar.sync %0, %1;\n" ::"r"(1 + warp / W), "n"(TPR) : "memory");
         const int first = warp / W * W;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -112,69 +102,148 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float (*red)[kWarpsPerBlo
     }
 }
 
-template <typename T, int VEC, int TPR, int NV>
+// A thread's raw pieces (16 bytes or one value each) of the NT tensors' rows,
+// kept unconverted so that the next rows' loads are in flight while a row is
+// computed.  VEC > 1: a ring of kRing - 1 rows ahead in shared memory, filled by
+// asynchronous copies; a thread reads back only what it copied itself, so no
+// barrier is involved.  VEC == 1: one row ahead in registers.
+constexpr int kRing = 4;
+
+template <typename T, int VEC, int NV, int NT>
+struct Rows {
+    static constexpr int kBytes = VEC > 1 ? kRing * NT * NV * kThreads * 16 : 0;
+    T next[VEC > 1 ? 1 : NT][NV];
+    uint4 *ring;
+    int put = 0, at = 0;
+
+    // starts the copies of one row (row pointers; none if !live)
+    __device__ __forceinline__ void fetch(const T *const (&src)[NT], bool live, int lane, int tpr, int dim) {
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (lane + i * tpr) * VEC;
+                if (!live || c >= dim) continue;
+                if constexpr (VEC > 1) cp_async16(&ring[((put * NT + k) * NV + i) * kThreads + threadIdx.x], src[k] + c, true);
+                else next[k][i] = src[k][c];
+            }
+        if constexpr (VEC > 1) {
+            cp_async_commit();
+            put = put + 1 == kRing ? 0 : put + 1;
+        }
+    }
+    // rows in flight before the first is used
+    static constexpr int kAhead = VEC > 1 ? kRing - 1 : 1;
+    __device__ __forceinline__ void wait() {
+        if constexpr (VEC > 1) cp_async_wait<kAhead - 1>();
+    }
+    __device__ __forceinline__ void get(int k, int i, float *f) const {
+        if constexpr (VEC == 1) {
+            f[0] = static_cast<float>(next[k][i]);
+        } else {
+            const uint4 v = ring[((at * NT + k) * NV + i) * kThreads + threadIdx.x];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (sizeof(T) == 4) {
+                    f[e] = __uint_as_float(w[e]);
+                } else {
+                    f[2 * e] = __uint_as_float(w[e] << 16);
+                    f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void pop() {
+        if constexpr (VEC > 1) at = at + 1 == kRing ? 0 : at + 1;
+    }
+};
+
+// Each block walks over its rows (RPB at a time), the next ones' loads in
+// flight; weight and bias stay in registers.  One block per row set measured
+// 122 us on 524288 gated rows of 128 (3.3 TB/s): most of its loads were the
+// weight's.
+template <typename T, int VEC, int TPR, int NV, bool GATE>
 __global__ void __launch_bounds__(kThreads) norm_fwd_kernel(NormArgs a) {
     constexpr bool PRECISE = sizeof(T) == 4;
+    constexpr int RPB = kThreads / TPR;
     __shared__ float red[2][kWarpsPerBlock][2];
     int flip = 0;
-    const int lane = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
-    const bool live = row < a.rows;
-    const T *x = static_cast<const T *>(a.x) + row * a.dim;
-    const T *z = a.z ? static_cast<const T *>(a.z) + row * a.dim : nullptr;
+    const int lane = threadIdx.x % TPR, slot = threadIdx.x / TPR;
     const float inv = 1.f / a.dim;
-    float v[NV][VEC], zv[NV][VEC];
-    float sum[1] = {0.f};
+    float w[NV][VEC], bias[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (lane + i * TPR) * VEC;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] = zv[i][e] = 0.f;
-        if (live && c < a.dim) {
-            load_vec<T, VEC>(x + c, v[i]);
-            if (z) load_vec<T, VEC>(z + c, zv[i]);
-        }
+        load_param<VEC>(c < a.dim && a.weight ? a.weight + c : nullptr, w[i], 1.f);
+        load_param<VEC>(c < a.dim && a.bias ? a.bias + c : nullptr, bias[i], 0.f);
     }
-    float mean = 0.f;
-    if (a.center) {
+    constexpr int NT = GATE ? 2 : 1;  // x, z
+    extern __shared__ __align__(16) uint4 ring[];
+    Rows<T, VEC, NV, NT> rows;
+    rows.ring = ring;
+    auto fetch = [&](int64_t row) {
+        const T *src[NT];
+        src[0] = static_cast<const T *>(a.x) + row * a.dim;
+        if constexpr (GATE) src[1] = static_cast<const T *>(a.z) + row * a.dim;
+        rows.fetch(src, row < a.rows, lane, TPR, a.dim);
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    for (int i = 0; i < rows.kAhead; ++i) fetch((int64_t)blockIdx.x * RPB + slot + i * step);
+    for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += step) {
+        const int64_t row = base + slot;
+        const bool live = row < a.rows;
+        float v[NV][VEC], zv[NV][VEC], sum[1] = {0.f};
+        rows.wait();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool in = live && (lane + i * TPR) * VEC < a.dim;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) v[i][e] = zv[i][e] = 0.f;
+            if (in) rows.get(0, i, v[i]);
+            if constexpr (GATE)
+                if (in) rows.get(1, i, zv[i]);
+        }
+        rows.pop();
+        fetch(row + rows.kAhead * step);
+        float mean = 0.f;
+        if (a.center) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) sum[0] += v[i][e];
+            row_sum<TPR>(sum, red, flip);
+            mean = sum[0] * inv;
+            sum[0] = 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
+            if ((lane + i * TPR) * VEC < a.dim)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) sum[0] += v[i][e];
+                for (int e = 0; e < VEC; ++e) {
+                    v[i][e] -= mean;
+                    sum[0] = fmaf(v[i][e], v[i][e], sum[0]);
+                }
         row_sum<TPR>(sum, red, flip);
-        mean = sum[0] * inv;
-        sum[0] = 0.f;
-    }
+        const float rstd = 1.f / sqrtf(sum[0] * inv + a.eps);
+        if (!live) continue;
+        if (lane == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        T *out = static_cast<T *>(a.out) + row * a.dim;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if ((lane + i * TPR) * VEC < a.dim)
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + i * TPR) * VEC;
+            if (c >= a.dim) continue;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                v[i][e] -= mean;
-                sum[0] = fmaf(v[i][e], v[i][e], sum[0]);
+                float y = fmaf(v[i][e] * rstd, w[i][e], bias[i][e]);
+                if (GATE) y *= zv[i][e] * sigmoid<PRECISE>(zv[i][e]);
+                v[i][e] = y;
             }
-    row_sum<TPR>(sum, red, flip);
-    const float rstd = 1.f / sqrtf(sum[0] * inv + a.eps);
-    if (!live) return;
-    if (lane == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
-    }
-    T *out = static_cast<T *>(a.out) + row * a.dim;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (lane + i * TPR) * VEC;
-        if (c >= a.dim) continue;
-        float w[VEC], bias[VEC];
-        load_param<VEC>(a.weight ? a.weight + c : nullptr, w, 1.f);
-        load_param<VEC>(a.bias ? a.bias + c : nullptr, bias, 0.f);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float y = fmaf(v[i][e] * rstd, w[e], bias[e]);
-            if (z) y *= zv[i][e] * sigmoid<PRECISE>(zv[i][e]);
-            v[i][e] = y;
+            store_vec<T, VEC>(out + c, v[i]);
         }
-        store_vec<T, VEC>(out + c, v[i]);
     }
 }
 
@@ -225,7 +294,7 @@ __device__ __forceinline__ void gate_grad(float dout, float y, float z, float &d
     dz = dout * y * s * fmaf(z, 1.f - s, 1.f);
 }
 
-template <typename T, int VEC, int TPR, int NV>
+template <typename T, int VEC, int TPR, int NV, bool GATE>
 __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(NormArgs a) {
     constexpr bool PRECISE = sizeof(T) == 4;
     constexpr int RPB = kThreads / TPR;  // rows per block and step
@@ -239,28 +308,50 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(NormArgs a) {
         const int c = (lane + i * TPR) * VEC;
         const bool in = c < a.dim;
         load_param<VEC>(in && a.weight ? a.weight + c : nullptr, w[i], in ? 1.f : 0.f);
-        load_param<VEC>(in && a.bias ? a.bias + c : nullptr, bias[i], 0.f);
+        if (GATE) load_param<VEC>(in && a.bias ? a.bias + c : nullptr, bias[i], 0.f);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dw[i][e] = db[i][e] = 0.f;
     }
-    for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += (int64_t)gridDim.x * RPB) {
+    constexpr int NT = GATE ? 3 : 2;  // x, dout, z
+    extern __shared__ __align__(16) uint4 ring[];
+    Rows<T, VEC, NV, NT> rows;
+    rows.ring = ring;
+    float mean_next = 0.f, rstd_next = 0.f;
+    auto stats = [&](int64_t row) {
+        if (row >= a.rows) return;
+        if (a.mean_in) mean_next = __ldg(a.mean_in + row);
+        rstd_next = __ldg(a.rstd_in + row);
+    };
+    auto fetch = [&](int64_t row) {
+        const T *src[NT];
+        src[0] = static_cast<const T *>(a.x) + row * a.dim;
+        src[1] = static_cast<const T *>(a.dout) + row * a.dim;
+        if constexpr (GATE) src[2] = static_cast<const T *>(a.z) + row * a.dim;
+        rows.fetch(src, row < a.rows, lane, TPR, a.dim);
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    for (int i = 0; i < rows.kAhead; ++i) fetch((int64_t)blockIdx.x * RPB + slot + i * step);
+    stats((int64_t)blockIdx.x * RPB + slot);
+    for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += step) {
         const int64_t row = base + slot;
         const bool live = row < a.rows;
         const int64_t at = row * a.dim;
-        const float mean = live && a.mean_in ? __ldg(a.mean_in + row) : 0.f;
-        const float rstd = live ? __ldg(a.rstd_in + row) : 0.f;
+        const float mean = mean_next, rstd = rstd_next;
         float xh[NV][VEC], dy[NV][VEC], zv[NV][VEC], sums[2] = {0.f, 0.f};
+        rows.wait();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (lane + i * TPR) * VEC;
+            const bool in = live && (lane + i * TPR) * VEC < a.dim;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) xh[i][e] = dy[i][e] = zv[i][e] = 0.f;
-            if (live && c < a.dim) {
-                load_vec<T, VEC>(static_cast<const T *>(a.x) + at + c, xh[i]);
-                load_vec<T, VEC>(static_cast<const T *>(a.dout) + at + c, dy[i]);
-                if (a.z) load_vec<T, VEC>(static_cast<const T *>(a.z) + at + c, zv[i]);
-            }
+            if (!in) continue;
+            rows.get(0, i, xh[i]);
+            rows.get(1, i, dy[i]);
+            if constexpr (GATE) rows.get(2, i, zv[i]);
         }
+        rows.pop();
+        fetch(row + rows.kAhead * step);
+        stats(row + step);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + i * TPR) * VEC;
@@ -269,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(NormArgs a) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 xh[i][e] = (xh[i][e] - mean) * rstd;
-                if (a.z) {
+                if (GATE) {
                     float d;
                     gate_grad<PRECISE>(dy[i][e], fmaf(xh[i][e], w[i][e], bias[i][e]), zv[i][e], d, dz[e]);
                     dy[i][e] = d;
@@ -280,7 +371,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(NormArgs a) {
                 sums[0] += dy[i][e];
                 sums[1] = fmaf(dy[i][e], xh[i][e], sums[1]);
             }
-            if (a.z) store_vec<T, VEC>(static_cast<T *>(a.dz) + at + c, dz);
+            if (GATE) store_vec<T, VEC>(static_cast<T *>(a.dz) + at + c, dz);
         }
         row_sum<TPR>(sums, red, flip);
         const float m1 = a.center ? sums[0] * inv : 0.f, m2 = sums[1] * inv;
@@ -383,25 +474,26 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_columns_kernel(NormArgs a) 
     if (a.dbias) a.partial[((int64_t)gridDim.y + blockIdx.y) * a.dim + c] = db;
 }
 
-// Adds the partial rows in a fixed order: 32 columns per block, 8 threads per
-// column, each over every 8th partial row.
-__global__ void __launch_bounds__(kThreads) norm_bwd_reduce_kernel(const float *partial, int parts, int dim,
-                                                                  float *dweight, float *dbias) {
-    __shared__ float s[kWarpsPerBlock][32];
+// Adds the partial rows in a fixed order: 32 columns per block, 32 threads per
+// column, each over every 32nd partial row.
+__global__ void __launch_bounds__(1024) norm_bwd_reduce_kernel(const float *partial, int parts, int dim,
+                                                               float *dweight, float *dbias) {
+    __shared__ float s[32][33];
     float *dst = blockIdx.y ? dbias : dweight;
     if (!dst) return;
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
     float sum = 0.f;
-    if (col < dim)
-        for (int p = part; p < parts; p += kWarpsPerBlock)
-            sum += partial[((int64_t)blockIdx.y * parts + p) * dim + col];
-    s[part][threadIdx.x & 31] = sum;
-    __syncthreads();
-    if (part == 0 && col < dim) {
-#pragma unroll
-        for (int p = 1; p < kWarpsPerBlock; ++p) sum += s[p][threadIdx.x & 31];
-        dst[col] = sum;
+    if (col < dim) {
+        const float *src = partial + (int64_t)blockIdx.y * parts * dim + col;
+#pragma unroll 4
+        for (int p = part; p < parts; p += 32) sum += src[(int64_t)p * dim];
     }
+    s[part][lane] = sum;
+    __syncthreads();
+    sum = s[lane][part];  // column `part` of the block, its 32 sums over the lanes
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0 && blockIdx.x * 32 + part < dim) dst[blockIdx.x * 32 + part] = sum;
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -410,7 +502,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // the row does not fit the registers.
 struct Shape { int tpr, nv; };
 bool shape_of(int64_t pieces, Shape *s) {
-    static constexpr Shape shapes[] = {{8, 1}, {16, 1}, {32, 1}, {32, 2}, {32, 4}, {256, 1}, {256, 2}, {256, 4}};
+    static constexpr Shape shapes[] = {{8, 1}, {16, 1}, {32, 1}, {32, 2}, {64, 2}, {128, 2}, {256, 2}, {256, 4}};
     for (const Shape &x : shapes)
         if (pieces <= (int64_t)x.tpr * x.nv) {
             *s = x;
@@ -422,87 +514,121 @@ bool shape_of(int64_t pieces, Shape *s) {
 template <typename T>
 bool vectors(const NormArgs &a) {
     return a.dim % (16 / sizeof(T)) == 0 && aligned16(a.x) && aligned16(a.z) && aligned16(a.dout) &&
-           aligned16(a.out) && aligned16(a.dx) && aligned16(a.dz);
+           aligned16(a.out) && aligned16(a.dx) && aligned16(a.dz) && aligned16(a.weight) && aligned16(a.bias);
 }
 
 template <typename T, int VEC, typename F>
 cudaError_t with_shape(Shape s, F f) {
-    if (s.tpr == 8) return f.template run<T, VEC, 8, 1>();
-    if (s.tpr == 16) return f.template run<T, VEC, 16, 1>();
-    if (s.tpr == 32) {
-        if (s.nv == 1) return f.template run<T, VEC, 32, 1>();
-        if (s.nv == 2) return f.template run<T, VEC, 32, 2>();
-        return f.template run<T, VEC, 32, 4>();
+    switch (s.tpr) {
+        case 8: return f.template run<T, VEC, 8, 1>();
+        case 16: return f.template run<T, VEC, 16, 1>();
+        case 32: return s.nv == 1 ? f.template run<T, VEC, 32, 1>() : f.template run<T, VEC, 32, 2>();
+        case 64: return f.template run<T, VEC, 64, 2>();
+        case 128: return f.template run<T, VEC, 128, 2>();
+        default: return s.nv == 2 ? f.template run<T, VEC, 256, 2>() : f.template run<T, VEC, 256, 4>();
     }
-    if (s.nv == 1) return f.template run<T, VEC, 256, 1>();
-    if (s.nv == 2) return f.template run<T, VEC, 256, 2>();
-    return f.template run<T, VEC, 256, 4>();
+}
+
+// Blocks that walk over the rows: as many as are resident at once (those of the
+// backward pass each leave one partial row of column sums).
+int64_t walkers(int64_t rows, int rows_per_block, int per_sm, int sms) {
+    const int64_t all = (rows + rows_per_block - 1) / rows_per_block, most = (int64_t)per_sm * sms;
+    return all < most ? all : most;
+}
+
+template <typename K>
+cudaError_t resident(K kernel, int smem, int *per_sm) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kernel, kThreads, smem);
+    if (e == cudaSuccess && *per_sm < 1) *per_sm = 1;
+    return e;
 }
 
 struct Fwd {
     const NormArgs &a;
+    int sms;
     cudaStream_t st;
-    template <typename T, int VEC, int TPR, int NV>
-    cudaError_t run() const {
-        constexpr int RPB = kThreads / TPR;
-        norm_fwd_kernel<T, VEC, TPR, NV><<<(unsigned)((a.rows + RPB - 1) / RPB), kThreads, 0, st>>>(a);
+    template <typename T, int VEC, int TPR, int NV, bool GATE>
+    cudaError_t go() const {
+        constexpr int smem = Rows<T, VEC, NV, GATE ? 2 : 1>::kBytes;
+        int per_sm = 1;
+        cudaError_t e = resident(norm_fwd_kernel<T, VEC, TPR, NV, GATE>, smem, &per_sm);
+        if (e != cudaSuccess) return e;
+        const int64_t blocks = walkers(a.rows, kThreads / TPR, per_sm, sms);
+        norm_fwd_kernel<T, VEC, TPR, NV, GATE><<<(unsigned)blocks, kThreads, smem, st>>>(a);
         return cudaGetLastError();
     }
+    template <typename T, int VEC, int TPR, int NV>
+    cudaError_t run() const { return a.z ? go<T, VEC, TPR, NV, true>() : go<T, VEC, TPR, NV, false>(); }
 };
-
-// Blocks of the backward pass: each leaves one partial row of column sums.
-constexpr int kBwdBlocksPerSm = 4;
-int64_t bwd_blocks(int64_t rows, int rows_per_block, int sms) {
-    const int64_t all = (rows + rows_per_block - 1) / rows_per_block, most = (int64_t)kBwdBlocksPerSm * sms;
-    return all < most ? all : most;
-}
 
 struct Bwd {
     const NormArgs &a;
-    int64_t blocks;
+    int sms;
+    int64_t *parts;  // rows of the workspace: decided here when nothing is launched yet
+    bool launch;
     cudaStream_t st;
-    template <typename T, int VEC, int TPR, int NV>
-    cudaError_t run() const {
-        norm_bwd_kernel<T, VEC, TPR, NV><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    template <typename T, int VEC, int TPR, int NV, bool GATE>
+    cudaError_t go() const {
+        constexpr int smem = Rows<T, VEC, NV, GATE ? 3 : 2>::kBytes;
+        if (!launch) {
+            int per_sm = 1;
+            cudaError_t e = resident(norm_bwd_kernel<T, VEC, TPR, NV, GATE>, smem, &per_sm);
+            *parts = walkers(a.rows, kThreads / TPR, per_sm, sms);
+            return e;
+        }
+        norm_bwd_kernel<T, VEC, TPR, NV, GATE><<<(unsigned)*parts, kThreads, smem, st>>>(a);
         return cudaGetLastError();
     }
+    template <typename T, int VEC, int TPR, int NV>
+    cudaError_t run() const { return a.z ? go<T, VEC, TPR, NV, true>() : go<T, VEC, TPR, NV, false>(); }
 };
 
+// What a backward call launches, decided before its workspace is allocated.
 template <typename T>
 struct BwdPlan {
     bool vec, fits;
     Shape s;
-    int64_t parts;
+    int64_t parts = 1;
+    cudaError_t e = cudaSuccess;
     BwdPlan(const NormArgs &a, int sms) {
         vec = vectors<T>(a);
         fits = shape_of(vec ? a.dim / (16 / sizeof(T)) : a.dim, &s);
         if (fits) {
-            parts = bwd_blocks(a.rows, kThreads / s.tpr, sms);
+            e = go(a, sms, false, nullptr);
         } else {
             const int64_t tiles = (a.dim + kThreads - 1) / kThreads;
             const int64_t most = (8 * (int64_t)sms + tiles - 1) / tiles;
             parts = a.rows < most ? a.rows : most;
         }
     }
+    cudaError_t go(const NormArgs &a, int sms, bool launch, cudaStream_t st) {
+        const Bwd f{a, sms, &parts, launch, st};
+        return vec ? with_shape<T, 16 / sizeof(T)>(s, f) : with_shape<T, 1>(s, f);
+    }
 };
 
 template <typename T>
-cudaError_t fwd_t(const NormArgs &a, cudaStream_t st) {
+cudaError_t fwd_t(const NormArgs &a, int sms, cudaStream_t st) {
     const bool vec = vectors<T>(a);
     Shape s;
     if (shape_of(vec ? a.dim / (16 / sizeof(T)) : a.dim, &s))
-        return vec ? with_shape<T, 16 / sizeof(T)>(s, Fwd{a, st}) : with_shape<T, 1>(s, Fwd{a, st});
+        return vec ? with_shape<T, 16 / sizeof(T)>(s, Fwd{a, sms, st}) : with_shape<T, 1>(s, Fwd{a, sms, st});
     norm_fwd_long_kernel<T><<<(unsigned)a.rows, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t bwd_t(const NormArgs &a, int sms, cudaStream_t st) {
-    const BwdPlan<T> p(a, sms);
+cudaError_t bwd_t(NormArgs a, int sms, NormAlloc alloc, cudaStream_t st) {
+    BwdPlan<T> p(a, sms);
+    if (p.e != cudaSuccess) return p.e;
+    if (a.dweight || a.dbias) {
+        cudaError_t e = alloc((size_t)2 * p.parts * a.dim * sizeof(float), st, &a.partial);
+        if (e != cudaSuccess) return e;
+    }
     cudaError_t e;
     if (p.fits) {
-        const Bwd f{a, p.parts, st};
-        e = p.vec ? with_shape<T, 16 / sizeof(T)>(p.s, f) : with_shape<T, 1>(p.s, f);
+        e = p.go(a, sms, true, st);
     } else {
         norm_bwd_long_kernel<T><<<(unsigned)a.rows, kThreads, 0, st>>>(a);
         e = cudaGetLastError();
@@ -512,25 +638,24 @@ cudaError_t bwd_t(const NormArgs &a, int sms, cudaStream_t st) {
             e = cudaGetLastError();
         }
     }
-    if (e != cudaSuccess || !a.partial) return e;
-    const dim3 grid((unsigned)((a.dim + 31) / 32), 2);
-    norm_bwd_reduce_kernel<<<grid, kThreads, 0, st>>>(a.partial, (int)p.parts, a.dim, a.dweight, a.dbias);
-    return cudaGetLastError();
+    if (!a.partial) return e;
+    if (e == cudaSuccess) {
+        const dim3 grid((unsigned)((a.dim + 31) / 32), 2);
+        norm_bwd_reduce_kernel<<<grid, 1024, 0, st>>>(a.partial, (int)p.parts, a.dim, a.dweight, a.dbias);
+        e = cudaGetLastError();
+    }
+    const cudaError_t ef = cudaFreeAsync(a.partial, st);
+    return e != cudaSuccess ? e : ef;
 }
 
 }  // namespace
 
-cudaError_t launch_norm_fwd(const NormArgs &a, bool bf16, cudaStream_t st) {
-    return bf16 ? fwd_t<__nv_bfloat16>(a, st) : fwd_t<float>(a, st);
+cudaError_t launch_norm_fwd(const NormArgs &a, bool bf16, int sms, cudaStream_t st) {
+    return bf16 ? fwd_t<__nv_bfloat16>(a, sms, st) : fwd_t<float>(a, sms, st);
 }
 
-cudaError_t launch_norm_bwd(const NormArgs &a, bool bf16, int sms, cudaStream_t st) {
-    return bf16 ? bwd_t<__nv_bfloat16>(a, sms, st) : bwd_t<float>(a, sms, st);
-}
-
-size_t norm_bwd_partial_bytes(const NormArgs &a, bool bf16, int sms) {
-    const int64_t parts = bf16 ? BwdPlan<__nv_bfloat16>(a, sms).parts : BwdPlan<float>(a, sms).parts;
-    return (size_t)2 * parts * a.dim * sizeof(float);
+cudaError_t launch_norm_bwd(const NormArgs &a, bool bf16, int sms, NormAlloc alloc, cudaStream_t st) {
+    return bf16 ? bwd_t<__nv_bfloat16>(a, sms, alloc, st) : bwd_t<float>(a, sms, alloc, st);
 }
 
 }  // namespace ssm

@@ -18,15 +18,16 @@ struct NormArgs {
     void *out, *dx, *dz;
     float *mean, *rstd;                // forward: (rows) or null
     float *dweight, *dbias;            // (dim) or null
-    float *partial;                    // backward workspace: norm_bwd_partial_bytes()
+    float *partial;                    // backward workspace: partial column sums, set by the launcher
     int64_t rows;
     int dim;
     float eps;
     int center;                        // 1: layer norm, 0: RMS norm
 };
 
-cudaError_t launch_norm_fwd(const NormArgs &a, bool bf16, cudaStream_t st);
-cudaError_t launch_norm_bwd(const NormArgs &a, bool bf16, int sms, cudaStream_t st);
-size_t norm_bwd_partial_bytes(const NormArgs &a, bool bf16, int sms);
+cudaError_t launch_norm_fwd(const NormArgs &a, bool bf16, int sms, cudaStream_t st);
+// Stream-ordered workspace for the column sums (freed with cudaFreeAsync).
+typedef cudaError_t (*NormAlloc)(size_t bytes, cudaStream_t st, float **p);
+cudaError_t launch_norm_bwd(const NormArgs &a, bool bf16, int sms, NormAlloc alloc, cudaStream_t st);
 
 }  // namespace ssm

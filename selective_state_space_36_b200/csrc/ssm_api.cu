@@ -1055,7 +1055,7 @@ ssm_status ssm_norm_fwd(int64_t rows, int64_t dim, ssm_dtype io, int mode, const
     ssm::NormArgs a{};
     a.x = x; a.z = z; a.weight = weight; a.bias = bias; a.out = out; a.mean = mean; a.rstd = rstd;
     a.rows = rows; a.dim = (int)dim; a.eps = eps; a.center = mode == SSM_NORM_LAYER;
-    cudaError_t e = ssm::launch_norm_fwd(a, io == SSM_BF16, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = ssm::launch_norm_fwd(a, io == SSM_BF16, device_info().sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "norm launch");
     return SSM_OK;
 }
@@ -1092,17 +1092,11 @@ ssm_status ssm_norm_bwd(int64_t rows, int64_t dim, ssm_dtype io, int mode, const
     a.mean_in = mean; a.rstd_in = rstd;
     a.dx = dx; a.dz = dz; a.dweight = dweight; a.dbias = dbias;
     a.rows = rows; a.dim = (int)dim; a.center = mode == SSM_NORM_LAYER;
-    const int sms = device_info().sms;
-    void *ws = nullptr;
-    if (dweight || dbias) {
-        cudaError_t e = workspace_alloc(&ws, ssm::norm_bwd_partial_bytes(a, io == SSM_BF16, sms), st);
-        if (e != cudaSuccess) return cuda_fail(e, "norm workspace allocation");
-        a.partial = static_cast<float *>(ws);
-    }
-    cudaError_t e = ssm::launch_norm_bwd(a, io == SSM_BF16, sms, st);
-    cudaError_t ef = ws ? cudaFreeAsync(ws, st) : cudaSuccess;
+    const ssm::NormAlloc alloc = [](size_t bytes, cudaStream_t on, float **p) {
+        return workspace_alloc(reinterpret_cast<void **>(p), bytes, on);
+    };
+    cudaError_t e = ssm::launch_norm_bwd(a, io == SSM_BF16, device_info().sms, alloc, st);
     if (e != cudaSuccess) return cuda_fail(e, "norm gradient launch");
-    if (ef != cudaSuccess) return cuda_fail(ef, "workspace release");
     return SSM_OK;
 }
 
