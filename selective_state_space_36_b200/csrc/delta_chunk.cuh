@@ -163,6 +163,11 @@ struct DeltaChunkWs {
     __nv_bfloat16 *r, *e; // (batch, heads, chunks, 2, 64, pp): r and its gradient over beta
 };
 
+// The whole forward in one kernel on the tcgen05 tensor cores: dstate 64 or
+// 128, headdim a multiple of 64, 16-byte aligned tensors.
+bool delta_fused_eligible(const DeltaArgs &a);
+cudaError_t launch_delta_fused(const DeltaArgs &a, cudaStream_t st);
+
 cudaError_t launch_delta_prep(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
 cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
 cudaError_t launch_delta_chain_store(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);

@@ -41,6 +41,7 @@
 
 #include "scan_kernels.cuh"
 #include "ssm_device.cuh"
+#include "tma_maps.cuh"
 #include "umma.cuh"
 
 namespace ssm {
@@ -602,50 +603,10 @@ ssd_fwd_pipelined_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_
 
 namespace ssm {
 
-namespace {
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
-
-// cuTensorMapEncodeTiled, fetched through the runtime (no link-time
-// dependency on the driver library).
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess) {
-            (void)cudaGetLastError();
-            return (EncodeTiledFn) nullptr;
-        }
-        return reinterpret_cast<EncodeTiledFn>(f);
-    }();
-    return fn;
-}
-
-// A (batch, seqlen, width) bf16 tensor as a 3-D tiled map: boxes of 64
-// elements of the width x 128 steps x 1 row, 128-byte swizzle; steps past
-// the sequence read as zeros and are not written by stores.
-bool encode_btw(CUtensorMap *m, const void *p, int64_t batch, int64_t seqlen, int64_t width) {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)seqlen, (cuuint64_t)batch};
-    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)(width * seqlen) * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)kQ, 1};
-    const cuuint32_t es[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-}  // namespace
-
 bool ssd_fwd_supported(const SsdFwdArgs &a) {
     auto al = [](const void *p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16) == 0; };
     return a.headdim == kP && (a.dstate == 64 || a.dstate == 128) && a.groups >= 1 && a.heads % a.groups == 0 &&
-           al(a.x) && al(a.z) && al(a.B) && al(a.C) && al(a.out) && encode_fn() != nullptr;
+           al(a.x) && al(a.z) && al(a.B) && al(a.C) && al(a.out) && encode_tiled_fn() != nullptr;
 }
 
 cudaError_t launch_ssd_fwd(const SsdFwdArgs &a, cudaStream_t st) {
@@ -654,9 +615,9 @@ cudaError_t launch_ssd_fwd(const SsdFwdArgs &a, cudaStream_t st) {
     const int64_t hp = a.heads * a.headdim, gn = a.groups * a.dstate;
     // without a gate the z map is never read; it is encoded over x so that
     // the kernel parameter is a valid map
-    if (!encode_btw(&mx, a.x, a.batch, a.seqlen, hp) || !encode_btw(&mb, a.B, a.batch, a.seqlen, gn) ||
-        !encode_btw(&mc, a.C, a.batch, a.seqlen, gn) || !encode_btw(&mo, a.out, a.batch, a.seqlen, hp) ||
-        !encode_btw(&mz, a.z ? a.z : a.x, a.batch, a.seqlen, hp))
+    if (!encode_btw(&mx, a.x, a.batch, a.seqlen, hp, kQ) || !encode_btw(&mb, a.B, a.batch, a.seqlen, gn, kQ) ||
+        !encode_btw(&mc, a.C, a.batch, a.seqlen, gn, kQ) || !encode_btw(&mo, a.out, a.batch, a.seqlen, hp, kQ) ||
+        !encode_btw(&mz, a.z ? a.z : a.x, a.batch, a.seqlen, hp, kQ))
         return cudaErrorInvalidValue;
     SsdArgs k{};
     k.dt = a.dt;

@@ -6,6 +6,7 @@
 #include <atomic>
 #include <mutex>
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include "../../include/ssm.h"
@@ -915,6 +916,11 @@ ssm_status delta_forward(ssm_ssd_dims dims, ssm_dtype io, const void *q, const v
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (io != SSM_BF16 || dims.seqlen <= kDeltaRecurrentTokens) {
         cudaError_t e = ssm::launch_delta_recurrent(a, io == SSM_BF16, st);
+        if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
+        return SSM_OK;
+    }
+    if (ssm::delta_fused_eligible(a) && !getenv("NOFUSED")) {
+        cudaError_t e = ssm::launch_delta_fused(a, st);
         if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
         return SSM_OK;
     }
