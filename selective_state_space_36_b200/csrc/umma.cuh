@@ -239,6 +239,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
+// The same wait for long phases: a poll may suspend the thread for up to 1 ms
+// (it wakes when the phase completes), so that waiting warps leave the issue
+// slots to the others.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (ok) return true;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > limit_ns) return false;
+    }
+}
+
 // --------------------------------------------------------------------- TMA
 // 2-D tile load global -> shared, completing on `bar` with transaction bytes.
 // c0 is the innermost coordinate (elements); it must be a multiple of 8 for
