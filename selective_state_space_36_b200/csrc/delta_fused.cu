@@ -40,7 +40,6 @@ namespace {
 
 using namespace umma;
 
-constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
 constexpr int kRowWarps = 8, kMatWarps = 4;
 constexpr int kThreadsF = (kRowWarps + kMatWarps + 4) * 32;  // 13-15: products, copies, decays; one idle
 // Registers per thread: 128 at launch, then by group of four warps
@@ -58,7 +57,8 @@ __host__ __device__ constexpr uint32_t operand_col(uint32_t base, int kstep, int
 }
 
 struct __align__(16) Dec {         // per chunk, float32
-    float gam[kC], gs[kC], beta[kC], wb[kC];  // exp G, scale exp G, beta, exp(G_C - G) beta
+    float gam[kC], gs[kC], wb[kC];  // exp G, scale exp G, exp(G_C - G) beta
+    float beta[kC], sbeta[kC];      // beta, scale beta
     // G in units of ln 2 as two floats: the difference of two such sums keeps the
     // digits that a difference of two floats loses, without float64's cost
     float ch[kC], cl[kC];
@@ -197,21 +197,20 @@ __device__ __forceinline__ void put_block(unsigned char *high, unsigned char *lo
 }
 
 // This thread's row of K K^T (warps 0, 1: L) or Q K^T (warps 2, 3: Pb): the 32
-// columns from s0 in x become f exp(G_t - G_s) beta_s x for s + strict <= t and
+// columns from s0 in x become exp(G_t - G_s) beta_s x (beta: scaled for Pb) for s + strict <= t and
 // zero above, and go to row `row` of two tiles in both terms.
-__device__ __forceinline__ void decay_row(float (&x)[32], const Dec &dec, float f, int strict, int t, int s0,
+__device__ __forceinline__ void decay_row(float (&x)[32], const Dec &dec, const float *beta, int strict, int t, int s0,
                                           unsigned char *high, unsigned char *low, int row) {
     const float2 th = make_float2(dec.ch[t], dec.ch[t]), tl = make_float2(dec.cl[t], dec.cl[t]);
-    const float2 f2 = make_float2(f, f);
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
         const float4 h = *reinterpret_cast<const float4 *>(&dec.ch[s0 + i]);
         const float4 l = *reinterpret_cast<const float4 *>(&dec.cl[s0 + i]);
-        const float4 b = *reinterpret_cast<const float4 *>(&dec.beta[s0 + i]);
+        const float4 b = *reinterpret_cast<const float4 *>(&beta[s0 + i]);
         const float2 d0 = add2(sub2(th, make_float2(h.x, h.y)), sub2(tl, make_float2(l.x, l.y)));
         const float2 d1 = add2(sub2(th, make_float2(h.z, h.w)), sub2(tl, make_float2(l.z, l.w)));
-        const float2 e0 = mul2(make_float2(ex2_approx(d0.x), ex2_approx(d0.y)), mul2(f2, make_float2(b.x, b.y)));
-        const float2 e1 = mul2(make_float2(ex2_approx(d1.x), ex2_approx(d1.y)), mul2(f2, make_float2(b.z, b.w)));
+        const float2 e0 = mul2(make_float2(ex2_approx(d0.x), ex2_approx(d0.y)), make_float2(b.x, b.y));
+        const float2 e1 = mul2(make_float2(ex2_approx(d1.x), ex2_approx(d1.y)), make_float2(b.z, b.w));
         const int at = s0 + i + strict;
         x[i] = at <= t ? x[i] * e0.x : 0.f;
         x[i + 1] = at + 1 <= t ? x[i + 1] * e0.y : 0.f;
@@ -232,7 +231,7 @@ __device__ __forceinline__ void decay_row(float (&x)[32], const Dec &dec, float 
 // The matrices of chunk c from [K; Q] K^T in tensor memory (kq: this warp's 32
 // lanes); `taken` is called when it has been read.
 template <int NT, typename F>
-__device__ __forceinline__ void chunk_matrices(FusedSmem<NT> &sm, float scale, int c, int w, int lane, uint32_t kq,
+__device__ __forceinline__ void chunk_matrices(FusedSmem<NT> &sm, int c, int w, int lane, uint32_t kq,
                                                F taken) {
     const Dec &dec = sm.dec[c & 1];
     unsigned char *mh = sm.np[c & 1][0], *ml = sm.np[c & 1][1];
@@ -251,7 +250,7 @@ __device__ __forceinline__ void chunk_matrices(FusedSmem<NT> &sm, float scale, i
         // stay in the instruction cache (at 95 KB it ran at a third of its speed)
 #pragma unroll 1
         for (int half = w & 1; half >= 0; --half) {
-            decay_row(x, dec, strict ? 1.f : scale, strict, t, 32 * half, high, low, row);
+            decay_row(x, dec, strict ? dec.beta : dec.sbeta, strict, t, 32 * half, high, low, row);
             if (half == (w & 1) && strict) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
@@ -294,12 +293,12 @@ __device__ __forceinline__ void chunk_matrices(FusedSmem<NT> &sm, float scale, i
     block_columns<2>(mh, ml, sm.l[0], sm.l[1], 32, 0, 8 * w, lane);
     mats_sync();  // M
     // Pb - Pb M, rows 16 w ...: blocks of 16 columns, in place (M is strictly
-    // lower: a block changes itself and those before it)
+    // lower: a block changes itself and those before it).  The zero blocks above
+    // the diagonal are not left out: the last rows need as long without them.
     const int rf_row = rows_first_row(lane), rf_col = rows_first_col(lane);
     float acc[kC / 8][4];
 #pragma unroll
     for (int kk = 0; kk < kC / 16; ++kk) {
-        if (kk > w) continue;
         uint32_t hi[4], lo[4];  // as accumulators: negated Pb
         ldm4(hi, tile_at(mh, kC + 16 * w + rf_row, 16 * kk + rf_col));
         ldm4(lo, tile_at(ml, kC + 16 * w + rf_row, 16 * kk + rf_col));
@@ -328,8 +327,7 @@ __device__ __forceinline__ void chunk_matrices(FusedSmem<NT> &sm, float scale, i
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][e] = -acc[j][e];
 #pragma unroll
-    for (int jj = 0; jj < kC / 16; ++jj)
-        if (jj <= w) put_block(mh, ml, kC + 16 * w, 16 * jj, acc[2 * jj], acc[2 * jj + 1], lane);
+    for (int jj = 0; jj < kC / 16; ++jj) put_block(mh, ml, kC + 16 * w, 16 * jj, acc[2 * jj], acc[2 * jj + 1], lane);
 }
 
 // ------------------------------------------------------------- row-wise work
@@ -394,11 +392,8 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     __syncthreads();
     fence_after_sync();
     const uint32_t tm = sm.tmem;
-    auto wait = [&](uint64_t *bar, uint32_t par) {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait_long(bar, par & 1u, kWaitNs)) != 0;
-        if (!ok && lane == 0) atomicOr(a.status, 4u);
-        return ok;
-    };
+    auto wait = [&](uint64_t *bar, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait_2s(bar, par & 1u)) != 0; };
+    bool ok = true;  // false: a wait of this warp ran out
     auto signal = [&](uint64_t *bar) {  // one arrival per warp, after the warp's writes
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -412,101 +407,100 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         constexpr uint32_t id_k = idesc_bf16(128, 128, kMajorK, kMajorK);
         constexpr uint32_t id_kq = idesc_bf16(128, 64, kMajorK, kMajorK);
         constexpr uint32_t id_s = idesc_bf16(128, 64 * NT, kMajorK, kMajorMN);
-        bool ok = true;
         // [K; Q] K^T of chunk c where O2 will be: the rows' read of the last O2 is
         // behind s_ready, the next M2 waits for kq_read
         auto kq_product = [&](int c) {
             if (!(ok = wait(&sm.ld[c & 1], c >> 1))) return;
             fence_after_sync();
             const uint64_t d = desc_sw128(smem_u32(sm.kq[c & 1][0]), 16, 1024);
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < 4 * NT; ++k) {
                 const uint64_t at = d + (((k / 4) * 2 * kHalfTile + (k % 4) * 32) >> 4);
                 mma_bf16_if(el, tm + kTO2, at, at, id_kq, k > 0);
             }
             mma_commit_if(el, &sm.kqd);
         };
-        if (nch > 0) kq_product(0);
-        for (int c = 0; ok && c < nch; ++c) {
+        // (step -1: the first chunk's [K; Q] K^T only)
+        for (int c = -1; ok && c < nch; ++c) {
             const int st = c & 1;
-            if (!(ok = wait(&sm.s_ready, c))) break;
-            fence_after_sync();
-            const uint64_t dkq = desc_sw128(smem_u32(sm.kq[st][0]), 16, 1024);
-#pragma unroll
-            for (int term = 0; term < 2; ++term)
-#pragma unroll
-                for (int k = 0; k < 4 * NT; ++k)
-                    mma_bf16_ts_if(el, tm + kTX, tm + (term ? kTSl : kTSh) + 8 * k,
-                                   dkq + (((k / 4) * 2 * kHalfTile + (k % 4) * 32) >> 4), id_k, term > 0 || k > 0);
-            mma_commit_if(el, &sm.x);
-            // (chunk 0's product has been read when its matrices are there)
-            if (c == 0 && !(ok = wait(&sm.kq_read, 0))) break;
+            if (c >= 0) {
+                if (!(ok = wait(&sm.s_ready, c))) break;
+                fence_after_sync();
+                const uint64_t dkq = desc_sw128(smem_u32(sm.kq[st][0]), 16, 1024);
+#pragma unroll 1
+                for (int k = 0; k < 8 * NT; ++k) {  // high terms, then low ones
+                    const int kk = k & (4 * NT - 1);
+                    mma_bf16_ts_if(el, tm + kTX, tm + (k < 4 * NT ? kTSh : kTSl) + 8 * kk,
+                                   dkq + (((kk / 4) * 2 * kHalfTile + (kk % 4) * 32) >> 4), id_k, k > 0);
+                }
+                mma_commit_if(el, &sm.x);
+                // (chunk 0's product has to be read before chunk 1's replaces it)
+                if (c == 0 && !(ok = wait(&sm.kq_read, 0))) break;
+            }
             if (c + 1 < nch) kq_product(c + 1);
+            if (c < 0) continue;
             if (!ok || !(ok = wait(&sm.prep[st], c >> 1)) || !(ok = wait(&sm.r_ready, c))) break;
             if (c + 1 < nch && !(ok = wait(&sm.kq_read, c + 1))) break;
             fence_after_sync();
             const uint64_t dnh = desc_sw128(smem_u32(sm.np[st][0]), 16, 1024);
             const uint64_t dnl = desc_sw128(smem_u32(sm.np[st][1]), 16, 1024);
-#pragma unroll
-            for (int term = 0; term < 3; ++term)  // high high, low high, high low
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16_ts_if(el, tm + kTY, tm + operand_col(kTX, k, term == 1),
-                                   (term == 2 ? dnl : dnh) + ((k * 32) >> 4), id_k, term > 0 || k > 0);
+#pragma unroll 1
+            for (int k = 0; k < 12; ++k) {  // R high with high terms, R low with high, R high with low
+                const int kk = k & 3, term = k >> 2;
+                mma_bf16_ts_if(el, tm + kTY, tm + operand_col(kTX, kk, term == 1),
+                               (term == 2 ? dnl : dnh) + ((kk * 32) >> 4), id_k, k > 0);
+            }
             mma_commit_if(el, &sm.y);
             if (!(ok = wait(&sm.u_ready, c))) break;
             fence_after_sync();
             // K as the right operand with tokens as the summed index: rows of 64
             // state columns, the second 64 in the next tile
             const uint64_t dk = desc_sw128(smem_u32(sm.kq[st][0]), 2 * kHalfTile, 1024);
-#pragma unroll
-            for (int term = 0; term < 2; ++term)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16_ts_if(el, tm + kTS, tm + operand_col(kTY, k, term), dk + ((k * 2048) >> 4), id_s, true);
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k)
+                mma_bf16_ts_if(el, tm + kTS, tm + operand_col(kTY, k & 3, k >> 2), dk + (((k & 3) * 2048) >> 4), id_s, true);
             mma_commit_if(el, &sm.s[st]);
         }
         mma_commit_if(el, &sm.fin);  // whatever was issued completes before tensor memory goes away
-        (void)mbar_wait(&sm.fin, 0u, kWaitNs);
+        (void)mbar_wait_2s(&sm.fin, 0u);
         __syncwarp();
       } else if (warp == kRowWarps + kMatWarps + 1) {
         // -------------------------------------------------- the copies
         const uint32_t el = elect_one();
         int issued[2] = {0, 0};
-        auto load = [&](int c) {
+        // step c: chunk c's output leaves, chunk c + 2 comes (two steps ahead of the first chunk)
+        for (int c = -2; c < nch; ++c) {
             const int st = c & 1;
+            if (c >= 0) {
+                if (!(ok = wait(&sm.o_ready[st], c >> 1))) break;
+                if (el) {
+#pragma unroll 1
+                    for (int i = 0; i < halves; ++i)
+                        tma_store_3d(&mapO, h * a.headdim + v0 + 64 * i, c * kC, (int32_t)b, sm.v[st][i]);
+                    tma_store_commit();
+                    tma_store_wait_read<0>();
+                }
+                __syncwarp();
+            }
+            if (c + 2 >= nch) continue;
+            if (c >= 0 && !(ok = wait(&sm.s[st], c >> 1))) break;  // K and Q are read
             if (el) {
                 mbar_expect_tx(&sm.ld[st], (uint32_t)(2 * NT + halves) * kHalfTile);
-                const int32_t t0 = c * kC;
-#pragma unroll
+                const int32_t t0 = (c + 2) * kC;
+#pragma unroll 1
                 for (int i = 0; i < NT; ++i) {
                     tma_load_3d(sm.kq[st][i], &mapK, gr * a.dstate + 64 * i, t0, (int32_t)b, &sm.ld[st]);
                     tma_load_3d(sm.kq[st][i] + kHalfTile, &mapQ, gr * a.dstate + 64 * i, t0, (int32_t)b, &sm.ld[st]);
                 }
+#pragma unroll 1
                 for (int i = 0; i < halves; ++i)
                     tma_load_3d(sm.v[st][i], &mapV, h * a.headdim + v0 + 64 * i, t0, (int32_t)b, &sm.ld[st]);
             }
             if (st) ++issued[1]; else ++issued[0];
-        };
-        load(0);
-        if (nch > 1) load(1);
-        for (int c = 0; c < nch; ++c) {
-            const int st = c & 1;
-            if (!wait(&sm.o_ready[st], c >> 1)) break;
-            if (el) {
-                for (int i = 0; i < halves; ++i)
-                    tma_store_3d(&mapO, h * a.headdim + v0 + 64 * i, c * kC, (int32_t)b, sm.v[st][i]);
-                tma_store_commit();
-                tma_store_wait_read<0>();
-            }
-            __syncwarp();
-            if (c + 2 >= nch) continue;
-            if (!wait(&sm.s[st], c >> 1)) break;  // K and Q are read
-            load(c + 2);
         }
         if (el) tma_store_wait_all<0>();
-        if (issued[0] > 0) (void)mbar_wait(&sm.ld[0], (uint32_t)(issued[0] - 1) & 1u, kWaitNs);
-        if (issued[1] > 0) (void)mbar_wait(&sm.ld[1], (uint32_t)(issued[1] - 1) & 1u, kWaitNs);
+        if (issued[0] > 0) (void)mbar_wait_2s(&sm.ld[0], (uint32_t)(issued[0] - 1) & 1u);
+        if (issued[1] > 0) (void)mbar_wait_2s(&sm.ld[1], (uint32_t)(issued[1] - 1) & 1u);
         __syncwarp();
       } else if (warp == kRowWarps + kMatWarps + 2) {
         // -------------------------------------------------- the decays
@@ -531,25 +525,26 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             const float be2[2] = {bv[0], bv[1]};
             double sum = d0 + d1;
             if (c + 1 < nch) fetch(c + 1);
-#pragma unroll
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const double up = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += up;
             }
             const double end = __shfl_sync(0xffffffffu, sum, 31);
             // chunk c - 2 is done with its decays and matrices
-            if (c >= 2 && !wait(&sm.o_ready[st], (c - 2) >> 1)) break;
-#pragma unroll
+            if (c >= 2 && !(ok = wait(&sm.o_ready[st], (c - 2) >> 1))) break;
+#pragma unroll 1
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
                 const double cum = i ? sum : sum - d1;
-                const float gam = ex2_approx((float)cum);
+                const float gam = ex2_approx((float)cum), be = i ? be2[1] : be2[0];
                 dec.ch[t] = (float)cum;
                 dec.cl[t] = (float)(cum - (double)(float)cum);
                 dec.gam[t] = gam;
                 dec.gs[t] = a.scale * gam;
-                dec.beta[t] = be2[i];
-                dec.wb[t] = ex2_approx((float)(end - cum)) * be2[i];
+                dec.beta[t] = be;
+                dec.sbeta[t] = a.scale * be;
+                dec.wb[t] = ex2_approx((float)(end - cum)) * be;
             }
             if (lane == 31) dec.whole = ex2_approx((float)end);
             signal(&sm.cum[st]);
@@ -562,10 +557,10 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         for (int c = 0; c < nch; ++c) {
             const int st = c & 1;
             // (cum comes after chunk c - 2 is done with its matrices)
-            const bool ok = wait(&sm.cum[st], c >> 1) && wait(&sm.kqd, c);
+            ok = wait(&sm.cum[st], c >> 1) && wait(&sm.kqd, c);
             if (!mats_all(ok)) break;
             fence_after_sync();
-            chunk_matrices<NT>(sm, a.scale, c, w, lane, tm + kTO2 + ((uint32_t)(32 * w) << 16), [&] {
+            chunk_matrices<NT>(sm, c, w, lane, tm + kTO2 + ((uint32_t)(32 * w) << 16), [&] {
                 fence_before_sync();
                 signal(&sm.kq_read);
             });
@@ -607,7 +602,6 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             tmem_wait_st();
         }
         uint32_t ov[16];  // the last chunk's output values, packed
-        bool ok = true;
         // chunk c's state is there when chunk c - 1's last product is done; the
         // step behind the last chunk only stores the state and the output
         for (int c = 0; c <= nch; ++c) {
@@ -721,8 +715,8 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                 }
             }
         }
-        (void)ok;
     }
+    if (!ok && lane == 0) atomicOr(a.status, 4u);
     fence_before_sync();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tm, 512);

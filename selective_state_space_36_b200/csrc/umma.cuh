@@ -239,23 +239,30 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
-// The same wait for long phases: a poll may suspend the thread for up to 1 ms
-// (it wakes when the phase completes), so that waiting warps leave the issue
-// slots to the others.
-__device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
-    uint64_t t0 = 0;
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-            : "memory");
-        if (ok) return true;
-        const uint64_t now = global_timer_ns();
-        if (t0 == 0) t0 = now;
-        else if (now - t0 > limit_ns) return false;
-    }
+// The same wait in few instructions (a kernel with a dozen of them has to stay
+// in the instruction cache), for at most 2 s: a poll may suspend the thread for
+// up to 1 ms and wakes when the phase completes.
+__device__ __forceinline__ bool mbar_wait_2s(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b32 t0, t1;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        "@p bra DONE_%=;\n"
+        "mov.u32 t0, %globaltimer_lo;\n"
+        "WAIT_%=:\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        "@p bra DONE_%=;\n"
+        "mov.u32 t1, %globaltimer_lo;\n"
+        "sub.u32 t1, t1, t0;\n"
+        "setp.lt.u32 p, t1, 2000000000;\n"
+        "@p bra WAIT_%=;\n"
+        "setp.ne.u32 p, 0, 0;\n"
+        "DONE_%=:\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
 }
 
 // --------------------------------------------------------------------- TMA
