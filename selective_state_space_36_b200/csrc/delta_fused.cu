@@ -8,16 +8,17 @@
 // operand of the next -- never leave tensor memory, and the row-wise work is
 // one thread per lane.  Per chunk, three tcgen05 products:
 //   [X | O1]^T = S [K; Q]^T                       (128 x 128, K = dstate)
-//   [Y | O2]^T = R^T [M; Pb - Pb M]^T             (128 x 128, K = 64),  R = V - gam X
-//   S          = gam_C S + (w beta r)^T K         (128 x dstate, K = 64),  r = R - Y
+//   Y^T        = R^T M^T                          (128 x 64,  K = 64),      R = V - gam X
+//   S          = gam_C S + (w beta r)^T K         (128 x dstate, K = 64),   r = R - Y
+//   O2^T       = r^T Pb^T                         (128 x 64,  K = 64)
 //   out        = scale gam O1 + O2
-// with M = N beta = I - (I + L)^-1, L = Abar beta, and Pb = P beta.  O2 reads R
-// instead of r (Pb r = (Pb - Pb M) R), so the output needs no product behind r.
+// with M = N beta = I - (I + L)^-1, L = Abar beta, and Pb = P beta.  What the next
+// row-wise step waits for is issued first: X before O1, the state before O2.
 // Operands that are not bf16 already take two bf16 terms (state: 2 products
-// instead of 1; R with M, Pb: 3).
+// instead of 1; R, r with M, Pb: 3).
 //
-// M and Pb - Pb M of the next chunk are made meanwhile by four warps of their
-// own: [K; Q] K^T (tcgen05), the decays, then, on mma.sync, M: its 16 x 16 diagonal
+// M and Pb of the next chunk are made meanwhile by eight warps of their own:
+// [K; Q] K^T (tcgen05), the decays, then, on mma.sync, M: its 16 x 16 diagonal
 // blocks by substitution, one column per thread, and from them twice as large
 // blocks, 16 to 32 to 64, by M21 = (I - M22) L21 (I - M11) with products of
 // two-term operands.  (Every factor is part of an inverse whose entries stay
@@ -25,7 +26,7 @@
 // and read 64 KB per chunk and head, as much as q, k, v and out together.
 //
 // Warps: 0-7 row-wise work (two per lane quarter, each half of the columns),
-// 8-11 the chunk matrices, 12 issues the products, 13 the TMA copies, 14 the
+// 8-15 the chunk matrices, 16 issues the products, 17 the TMA copies, 18 the
 // decays.  They meet at mbarriers only; every wait is bounded and reports
 // through the device status word.
 #include "delta_chunk.cuh"
@@ -40,17 +41,17 @@ namespace {
 
 using namespace umma;
 
-constexpr int kRowWarps = 8, kMatWarps = 4;
-constexpr int kThreadsF = (kRowWarps + kMatWarps + 4) * 32;  // 13-15: products, copies, decays; one idle
-// Registers per thread: 128 at launch, then by group of four warps
-constexpr int kRowRegs = 152, kMatRegs = 168, kRestRegs = 40;
-static_assert(2 * kRowRegs + kMatRegs + kRestRegs <= 4 * 128, "no more than the block was launched with");
+constexpr int kRowWarps = 8, kMatWarps = 8;
+constexpr int kThreadsF = (kRowWarps + kMatWarps + 4) * 32;  // 16-18: products, copies, decays; one idle
+// Registers per thread: 96 at launch, then by group of four warps
+constexpr int kLaunchRegs = 96, kRowRegs = 144, kMatRegs = 80, kRestRegs = 32;
+static_assert(2 * kRowRegs + 2 * kMatRegs + kRestRegs <= 5 * kLaunchRegs, "no more than the block was launched with");
 constexpr uint32_t kHalfTile = kC * 128;  // 64 rows x 128 bytes
 constexpr int kDLd = 36;                 // row stride of a 32 x 32 float32 block: 16-byte rows
 
 // tensor memory columns
 constexpr uint32_t kTX = 0, kTO1 = 64, kTY = 128, kTO2 = 192, kTS = 256, kTSh = 384, kTSl = 448;
-// R (where X was) and w u (where Y was): tokens 32 wg .. 32 wg + 31 of
+// R, later r (where X was) and w beta r (where Y was): tokens 32 wg .. 32 wg + 31 of
 // both terms stay within the columns that their warps have read themselves
 __host__ __device__ constexpr uint32_t operand_col(uint32_t base, int kstep, int term) {
     return base + 32 * (kstep >> 1) + 16 * term + 8 * (kstep & 1);
@@ -69,15 +70,16 @@ template <int NT>
 struct FusedSmem {
     unsigned char kq[2][NT][2 * kHalfTile];  // per stage and 64 columns: K rows, then Q rows
     unsigned char v[2][2][kHalfTile];        // V, later the output
-    unsigned char np[2][2][2 * kHalfTile];   // [M; Pb - Pb M]: high, low term
+    unsigned char np[2][2][2 * kHalfTile];   // [M; Pb]: high, low term
     unsigned char l[2][kHalfTile];           // L: high, low term
     float ld32[kC][kDLd];                    // L's 32 x 32 diagonal blocks
     Dec dec[2];
     // Barriers whose waiters may fall a chunk behind have one per stage, so that
     // a phase cannot be overtaken.
-    uint64_t ld[2], cum[2], prep[2];         // copies landed; decays, chunk matrices ready
-    uint64_t kqd, x, y, s[2];                // products complete ([K; Q] K^T first)
-    uint64_t s_ready, r_ready, u_ready, o_ready[2];  // row-wise results written
+    uint64_t ldk[2], ldv[2], cum[2], m[2], pb[2];  // K and Q, V landed; decays, M, Pb ready
+    uint64_t kqd, x, y, o, s[2];             // products complete ([K; Q] K^T first)
+    uint64_t s_ready[NT], r_ready, w_ready, u_ready, o_ready[2];  // row-wise results written
+    uint64_t o_taken[2];                     // O1 and O2 are in registers
     uint64_t kq_read;                        // [K; Q] K^T is in registers
     uint64_t fin;
     uint32_t tmem;
@@ -98,12 +100,14 @@ __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.
 template <int N>
 __device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-__device__ __forceinline__ void mats_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// all eight warps of the chunk matrices; the first four of them
+__device__ __forceinline__ void mats_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void solve_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
-// The same barrier; true where `ok` holds in all four warps.
+// The barrier of all eight; true where `ok` holds in every warp.
 __device__ __forceinline__ bool mats_all(bool ok) {
     uint32_t all;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.and.pred p, 1, 128, q;\nselp.u32 %0, 1, 0, p;\n}\n"
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.and.pred p, 1, 256, q;\nselp.u32 %0, 1, 0, p;\n}\n"
                  : "=r"(all) : "r"((uint32_t)ok) : "memory");
     return all != 0;
 }
@@ -182,20 +186,6 @@ __device__ __forceinline__ void block_columns(unsigned char *mh, unsigned char *
     }
 }
 
-// A 16 x 16 block (two accumulators side by side) in both terms.
-__device__ __forceinline__ void put_block(unsigned char *high, unsigned char *low, int row, int col,
-                                          const float (&x)[4], const float (&y)[4], int lane) {
-    uint32_t h[4], l[4];
-    split(x[0], x[1], h[0], l[0]);
-    split(x[2], x[3], h[1], l[1]);
-    split(y[0], y[1], h[2], l[2]);
-    split(y[2], y[3], h[3], l[3]);
-    row += rows_first_row(lane);
-    col += rows_first_col(lane);
-    stm4(tile_at(high, row, col), h[0], h[1], h[2], h[3]);
-    stm4(tile_at(low, row, col), l[0], l[1], l[2], l[3]);
-}
-
 // This thread's row of K K^T (warps 0, 1: L) or Q K^T (warps 2, 3: Pb): the 32
 // columns from s0 in x become exp(G_t - G_s) beta_s x (beta: scaled for Pb) for s + strict <= t and
 // zero above, and go to row `row` of two tiles in both terms.
@@ -228,106 +218,67 @@ __device__ __forceinline__ void decay_row(float (&x)[32], const Dec &dec, const 
     }
 }
 
-// The matrices of chunk c from [K; Q] K^T in tensor memory (kq: this warp's 32
-// lanes); `taken` is called when it has been read.
-template <int NT, typename F>
-__device__ __forceinline__ void chunk_matrices(FusedSmem<NT> &sm, int c, int w, int lane, uint32_t kq,
-                                               F taken) {
+// The matrices of chunk c from [K; Q] K^T in tensor memory (kq: the 32 lanes of
+// this warp's quarter).  Eight warps: those of a quarter share its 32 rows of
+// K K^T (quarters 0, 1) or Q K^T, the first set with the 32 x 32 block on the
+// diagonal, the second with the block left of it.  The first set alone then
+// makes M.  `taken`: the tensor memory has been read, `decayed`: Pb is there.
+template <int NT, typename F, typename G>
+__device__ __forceinline__ void chunk_matrices(FusedSmem<NT> &sm, int c, int w, int set, int lane, uint32_t kq,
+                                               F taken, G decayed) {
     const Dec &dec = sm.dec[c & 1];
     unsigned char *mh = sm.np[c & 1][0], *ml = sm.np[c & 1][1];
-    {
-        // rows 32 (w % 2) ...: the columns of the first half, and for the lower rows
-        // those of the second
-        const int t = 32 * (w & 1) + lane, strict = w < 2;
-        unsigned char *high = strict ? sm.l[0] : mh, *low = strict ? sm.l[1] : ml;
-        const int row = strict ? t : kC + t;
-        float x[32], y[32];
-        tmem_ld32(kq + 32 * (w & 1), x);  // the columns of the block on the diagonal
-        tmem_ld32(kq, y);
+    if (set == 0 || (w & 1)) {
+        const int t = 32 * (w & 1) + lane, strict = w < 2, s0 = set == 0 ? 32 * (w & 1) : 0;
+        float x[32];
+        tmem_ld32(kq + s0, x);
         tmem_wait_ld();
         taken();
-        // one copy of the code for both halves: the kernel's instructions have to
-        // stay in the instruction cache (at 95 KB it ran at a third of its speed)
-#pragma unroll 1
-        for (int half = w & 1; half >= 0; --half) {
-            decay_row(x, dec, strict ? dec.beta : dec.sbeta, strict, t, 32 * half, high, low, row);
-            if (half == (w & 1) && strict) {
+        decay_row(x, dec, strict ? dec.beta : dec.sbeta, strict, t, s0, strict ? sm.l[0] : mh, strict ? sm.l[1] : ml,
+                  strict ? t : kC + t);
+        if (set == 0 && strict) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<float4 *>(&sm.ld32[t][i]) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = y[i];
+            for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(&sm.ld32[t][i]) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
         }
+    } else {
+        taken();
     }
-    mats_sync();  // L and Pb
-    // the diagonal blocks of M, column lane % 16 from its top
-    {
-        const int o = 16 * w, oc = 16 * (w & 1), j = lane & 15;
-        float x[16];
+    fence_proxy_async();
+    decayed();
+    mats_sync();  // L
+    if (set == 0) {
+        // the diagonal blocks of M, column lane % 16 from its top
+        {
+            const int o = 16 * w, oc = 16 * (w & 1), j = lane & 15;
+            float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s[2] = {sm.ld32[o + i][oc + j], 0.f};  // zero for i <= j
+            for (int i = 0; i < 16; ++i) {
+                float s[2] = {sm.ld32[o + i][oc + j], 0.f};  // zero for i <= j
 #pragma unroll
-            for (int k = 0; k < i; k += 4) {
-                const float4 m = *reinterpret_cast<const float4 *>(&sm.ld32[o + i][oc + k]);
-                s[0] = fmaf(-m.x, x[k], s[0]);
-                if (k + 1 < i) s[1] = fmaf(-m.y, x[k + 1], s[1]);
-                if (k + 2 < i) s[0] = fmaf(-m.z, x[k + 2], s[0]);
-                if (k + 3 < i) s[1] = fmaf(-m.w, x[k + 3], s[1]);
+                for (int k = 0; k < i; k += 4) {
+                    const float4 m = *reinterpret_cast<const float4 *>(&sm.ld32[o + i][oc + k]);
+                    s[0] = fmaf(-m.x, x[k], s[0]);
+                    if (k + 1 < i) s[1] = fmaf(-m.y, x[k + 1], s[1]);
+                    if (k + 2 < i) s[0] = fmaf(-m.z, x[k + 2], s[0]);
+                    if (k + 3 < i) s[1] = fmaf(-m.w, x[k + 3], s[1]);
+                }
+                x[i] = s[0] + s[1];
             }
-            x[i] = s[0] + s[1];
-        }
-        // lanes 0-15 write the high terms, the others the low ones
-        unsigned char *dst = lane < 16 ? mh : ml;
+            // lanes 0-15 write the high terms, the others the low ones
+            unsigned char *dst = lane < 16 ? mh : ml;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float hi = __bfloat162float(__float2bfloat16_rn(x[i]));
-            *tile_at(dst, o + i, o + j) = __float2bfloat16_rn(lane < 16 ? hi : x[i] - hi);
-        }
-    }
-    mats_sync();  // the diagonal blocks
-    // 16 to 32: warps 0, 1 the block at (16, 0), warps 2, 3 that at (48, 32)
-    block_columns<1>(mh, ml, sm.l[0], sm.l[1], 32 * (w >> 1) + 16, 32 * (w >> 1), 32 * (w >> 1) + 8 * (w & 1), lane);
-    mats_sync();  // the 32 x 32 blocks on the diagonal
-    block_columns<2>(mh, ml, sm.l[0], sm.l[1], 32, 0, 8 * w, lane);
-    mats_sync();  // M
-    // Pb - Pb M, rows 16 w ...: blocks of 16 columns, in place (M is strictly
-    // lower: a block changes itself and those before it).  The zero blocks above
-    // the diagonal are not left out: the last rows need as long without them.
-    const int rf_row = rows_first_row(lane), rf_col = rows_first_col(lane);
-    float acc[kC / 8][4];
-#pragma unroll
-    for (int kk = 0; kk < kC / 16; ++kk) {
-        uint32_t hi[4], lo[4];  // as accumulators: negated Pb
-        ldm4(hi, tile_at(mh, kC + 16 * w + rf_row, 16 * kk + rf_col));
-        ldm4(lo, tile_at(ml, kC + 16 * w + rf_row, 16 * kk + rf_col));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float(&x)[4] = acc[2 * kk + (i >> 1)];
-            x[2 * (i & 1)] = -(low_of(hi[i]) + low_of(lo[i]));
-            x[2 * (i & 1) + 1] = -(high_of(hi[i]) + high_of(lo[i]));
-        }
-#pragma unroll
-        for (int jj = 0; jj <= kk; ++jj) {
-            uint32_t f[4], fl[4];
-            ldm4t(f, tile_at(mh, 16 * kk + rf_row, 16 * jj + rf_col));
-            ldm4t(fl, tile_at(ml, 16 * kk + rf_row, 16 * jj + rf_col));
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                mma(acc[2 * jj + i], hi, f[2 * i], f[2 * i + 1]);
-                mma(acc[2 * jj + i], lo, f[2 * i], f[2 * i + 1]);
-                mma(acc[2 * jj + i], hi, fl[2 * i], fl[2 * i + 1]);
+            for (int i = 0; i < 16; ++i) {
+                const float hi = __bfloat162float(__float2bfloat16_rn(x[i]));
+                *tile_at(dst, o + i, o + j) = __float2bfloat16_rn(lane < 16 ? hi : x[i] - hi);
             }
         }
+        solve_sync();  // the diagonal blocks
+        // 16 to 32: warps 0, 1 the block at (16, 0), warps 2, 3 that at (48, 32)
+        block_columns<1>(mh, ml, sm.l[0], sm.l[1], 32 * (w >> 1) + 16, 32 * (w >> 1), 32 * (w >> 1) + 8 * (w & 1), lane);
+        solve_sync();  // the 32 x 32 blocks on the diagonal
+        block_columns<2>(mh, ml, sm.l[0], sm.l[1], 32, 0, 8 * w, lane);
     }
-    __syncwarp();  // (a warp reads and writes only its own rows of Pb)
-#pragma unroll
-    for (int j = 0; j < kC / 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = -acc[j][e];
-#pragma unroll
-    for (int jj = 0; jj < kC / 16; ++jj) put_block(mh, ml, kC + 16 * w, 16 * jj, acc[2 * jj], acc[2 * jj + 1], lane);
 }
 
 // ------------------------------------------------------------- row-wise work
@@ -356,8 +307,9 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                    const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapO,
                    const FusedArgs a) {
     extern __shared__ unsigned char raw[];
-    FusedSmem<NT> &sm = *reinterpret_cast<FusedSmem<NT> *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
-                                                           ~static_cast<uintptr_t>(1023));
+    // 1024-byte aligned by an offset, not by a rounded address: a pointer made from
+    // an integer would turn every shared access into a generic one
+    FusedSmem<NT> &sm = *reinterpret_cast<FusedSmem<NT> *>(raw + ((0u - smem_u32(raw)) & 1023u));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t bh = blockIdx.x / a.vtiles;
     const int v0 = (int)(blockIdx.x - bh * a.vtiles) * 128;
@@ -365,26 +317,32 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     const int h = (int)(bh - b * a.heads), gr = h / a.rep;
     const int nch = (int)((a.seqlen + kC - 1) / kC);
     const int halves = a.headdim - v0 > 64 ? 2 : 1;  // 64-column halves of V in this CTA
+    const int row_warps = 4 * halves;                // whose lanes hold rows of the state
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.ld[i], 1);
+            mbar_init(&sm.ldk[i], 1);
+            mbar_init(&sm.ldv[i], 1);
+            mbar_init(&sm.o_taken[i], row_warps);
             mbar_init(&sm.cum[i], 1);
-            mbar_init(&sm.prep[i], kMatWarps);
+            mbar_init(&sm.m[i], 4);
+            mbar_init(&sm.pb[i], kMatWarps);
             mbar_init(&sm.s[i], 1);
-            mbar_init(&sm.o_ready[i], kRowWarps);
+            mbar_init(&sm.o_ready[i], row_warps);
         }
         mbar_init(&sm.kqd, 1);
         mbar_init(&sm.kq_read, kMatWarps);
         mbar_init(&sm.x, 1);
         mbar_init(&sm.y, 1);
-        mbar_init(&sm.s_ready, kRowWarps);
-        mbar_init(&sm.r_ready, kRowWarps);
-        mbar_init(&sm.u_ready, kRowWarps);
+        mbar_init(&sm.o, 1);
+        for (int i = 0; i < NT; ++i) mbar_init(&sm.s_ready[i], row_warps);
+        mbar_init(&sm.r_ready, row_warps);
+        mbar_init(&sm.w_ready, row_warps);
+        mbar_init(&sm.u_ready, row_warps);
         mbar_init(&sm.fin, 1);
         mbar_fence_init();
     }
-    // the parts of [M; Pb - Pb M] above the diagonal are written here only
+    // the parts of [M; Pb] above the diagonal are written here only
     for (int i = tid; i < (int)sizeof(sm.np) / 16; i += kThreadsF)
         reinterpret_cast<uint4 *>(sm.np)[i] = make_uint4(0, 0, 0, 0);
     if (warp == 0) tmem_alloc(&sm.tmem, 512);
@@ -404,62 +362,80 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
       if (warp == kRowWarps + kMatWarps) {
         // ------------------------------------------------ the products
         const uint32_t el = elect_one();
-        constexpr uint32_t id_k = idesc_bf16(128, 128, kMajorK, kMajorK);
-        constexpr uint32_t id_kq = idesc_bf16(128, 64, kMajorK, kMajorK);
+        constexpr uint32_t id_64 = idesc_bf16(128, 64, kMajorK, kMajorK);
         constexpr uint32_t id_s = idesc_bf16(128, 64 * NT, kMajorK, kMajorMN);
-        // [K; Q] K^T of chunk c where O2 will be: the rows' read of the last O2 is
-        // behind s_ready, the next M2 waits for kq_read
-        auto kq_product = [&](int c) {
-            if (!(ok = wait(&sm.ld[c & 1], c >> 1))) return;
-            fence_after_sync();
-            const uint64_t d = desc_sw128(smem_u32(sm.kq[c & 1][0]), 16, 1024);
-#pragma unroll 1
-            for (int k = 0; k < 4 * NT; ++k) {
-                const uint64_t at = d + (((k / 4) * 2 * kHalfTile + (k % 4) * 32) >> 4);
-                mma_bf16_if(el, tm + kTO2, at, at, id_kq, k > 0);
+        // (unrolled: in a loop one product took 110 clocks to issue, 32 to run)
+        // Tiles as right operands: K rows, then Q rows (M, then Pb - Pb M).
+        auto state_product = [&](uint64_t tile, uint32_t d, int part) {  // S's 32-column pieces `part` of both halves
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // two pieces of two steps, high terms, then low ones
+                const int k = 2 * NT * ((i >> 1) & 1) + 2 * part + (i & 1);
+                mma_bf16_ts_if(el, tm + d, tm + (i < 4 ? kTSh : kTSl) + 8 * k,
+                               tile + (((k / 4) * 2 * kHalfTile + (k % 4) * 32) >> 4), id_64, part > 0 || i > 0);
             }
-            mma_commit_if(el, &sm.kqd);
+        };
+        auto r_product = [&](uint64_t high, uint64_t low, uint32_t d) {
+#pragma unroll
+            for (int k = 0; k < 12; ++k) {  // R high with high terms, R low with high, R high with low
+                const int kk = k & 3, term = k >> 2;
+                mma_bf16_ts_if(el, tm + d, tm + operand_col(kTX, kk, term == 1),
+                               (term == 2 ? low : high) + ((kk * 32) >> 4), id_64, k > 0);
+            }
         };
         // (step -1: the first chunk's [K; Q] K^T only)
         for (int c = -1; ok && c < nch; ++c) {
             const int st = c & 1;
             if (c >= 0) {
-                if (!(ok = wait(&sm.s_ready, c))) break;
-                fence_after_sync();
-                const uint64_t dkq = desc_sw128(smem_u32(sm.kq[st][0]), 16, 1024);
-#pragma unroll 1
-                for (int k = 0; k < 8 * NT; ++k) {  // high terms, then low ones
-                    const int kk = k & (4 * NT - 1);
-                    mma_bf16_ts_if(el, tm + kTX, tm + (k < 4 * NT ? kTSh : kTSl) + 8 * kk,
-                                   dkq + (((kk / 4) * 2 * kHalfTile + (kk % 4) * 32) >> 4), id_k, k > 0);
+                const uint64_t dk = desc_sw128(smem_u32(sm.kq[st][0]), 16, 1024), dq = dk + (kHalfTile >> 4);
+#pragma unroll
+                for (int part = 0; part < NT; ++part) {
+                    if (!(ok = wait(&sm.s_ready[part], c))) break;
+                    fence_after_sync();
+                    state_product(dk, kTX, part);
                 }
+                if (!ok) break;
                 mma_commit_if(el, &sm.x);
+                if (c > 0 && !(ok = wait(&sm.o_taken[st ^ 1], (c - 1) >> 1))) break;
+                fence_after_sync();
+#pragma unroll
+                for (int part = 0; part < NT; ++part) state_product(dq, kTO1, part);
                 // (chunk 0's product has to be read before chunk 1's replaces it)
                 if (c == 0 && !(ok = wait(&sm.kq_read, 0))) break;
             }
-            if (c + 1 < nch) kq_product(c + 1);
-            if (c < 0) continue;
-            if (!ok || !(ok = wait(&sm.prep[st], c >> 1)) || !(ok = wait(&sm.r_ready, c))) break;
-            if (c + 1 < nch && !(ok = wait(&sm.kq_read, c + 1))) break;
-            fence_after_sync();
-            const uint64_t dnh = desc_sw128(smem_u32(sm.np[st][0]), 16, 1024);
-            const uint64_t dnl = desc_sw128(smem_u32(sm.np[st][1]), 16, 1024);
-#pragma unroll 1
-            for (int k = 0; k < 12; ++k) {  // R high with high terms, R low with high, R high with low
-                const int kk = k & 3, term = k >> 2;
-                mma_bf16_ts_if(el, tm + kTY, tm + operand_col(kTX, kk, term == 1),
-                               (term == 2 ? dnl : dnh) + ((kk * 32) >> 4), id_k, k > 0);
+            if (c + 1 < nch) {
+                // [K; Q] K^T of chunk c + 1 where O2 will be: the last O2 has been taken,
+                // the next waits for kq_read
+                if (!(ok = wait(&sm.ldk[st ^ 1], (c + 1) >> 1))) break;
+                fence_after_sync();
+                const uint64_t d = desc_sw128(smem_u32(sm.kq[st ^ 1][0]), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < 4 * NT; ++k) {
+                    const uint64_t at = d + (((k / 4) * 2 * kHalfTile + (k % 4) * 32) >> 4);
+                    mma_bf16_if(el, tm + kTO2, at, at, id_64, k > 0);
+                }
+                mma_commit_if(el, &sm.kqd);
             }
+            if (c < 0) continue;
+            const uint64_t dh = desc_sw128(smem_u32(sm.np[st][0]), 16, 1024);
+            const uint64_t dl = desc_sw128(smem_u32(sm.np[st][1]), 16, 1024);
+            if (!(ok = wait(&sm.m[st], c >> 1)) || !(ok = wait(&sm.r_ready, c))) break;
+            fence_after_sync();
+            r_product(dh, dl, kTY);
             mma_commit_if(el, &sm.y);
-            if (!(ok = wait(&sm.u_ready, c))) break;
+            if (!(ok = wait(&sm.w_ready, c))) break;
             fence_after_sync();
             // K as the right operand with tokens as the summed index: rows of 64
             // state columns, the second 64 in the next tile
             const uint64_t dk = desc_sw128(smem_u32(sm.kq[st][0]), 2 * kHalfTile, 1024);
-#pragma unroll 1
+#pragma unroll
             for (int k = 0; k < 8; ++k)
                 mma_bf16_ts_if(el, tm + kTS, tm + operand_col(kTY, k & 3, k >> 2), dk + (((k & 3) * 2048) >> 4), id_s, true);
             mma_commit_if(el, &sm.s[st]);
+            if (!(ok = wait(&sm.u_ready, c)) || !(ok = wait(&sm.pb[st], c >> 1))) break;
+            if (c + 1 < nch && !(ok = wait(&sm.kq_read, c + 1))) break;
+            fence_after_sync();
+            r_product(dh + (kHalfTile >> 4), dl + (kHalfTile >> 4), kTO2);
+            mma_commit_if(el, &sm.o);
         }
         mma_commit_if(el, &sm.fin);  // whatever was issued completes before tensor memory goes away
         (void)mbar_wait_2s(&sm.fin, 0u);
@@ -467,10 +443,24 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
       } else if (warp == kRowWarps + kMatWarps + 1) {
         // -------------------------------------------------- the copies
         const uint32_t el = elect_one();
-        int issued[2] = {0, 0};
-        // step c: chunk c's output leaves, chunk c + 2 comes (two steps ahead of the first chunk)
+        int issued[2] = {0, 0}, issued_v[2] = {0, 0};
+        // step c: chunk c + 2's K and Q replace chunk c's, its output leaves and chunk
+        // c + 2's V comes (two steps ahead of the first chunk)
         for (int c = -2; c < nch; ++c) {
             const int st = c & 1;
+            const int32_t t0 = (c + 2) * kC;
+            if (c >= 0 && !(ok = wait(&sm.s[st], c >> 1))) break;
+            if (c + 2 < nch && el) {
+                mbar_expect_tx(&sm.ldk[st], (uint32_t)(2 * NT) * kHalfTile);
+#pragma unroll 1
+                for (int i = 0; i < NT; ++i) {
+                    tma_load_3d(sm.kq[st][i], &mapK, gr * a.dstate + 64 * i, t0, (int32_t)b, &sm.ldk[st]);
+                    tma_load_3d(sm.kq[st][i] + kHalfTile, &mapQ, gr * a.dstate + 64 * i, t0, (int32_t)b, &sm.ldk[st]);
+                }
+            }
+            if (c + 2 < nch) {
+                if (st) ++issued[1]; else ++issued[0];
+            }
             if (c >= 0) {
                 if (!(ok = wait(&sm.o_ready[st], c >> 1))) break;
                 if (el) {
@@ -482,25 +472,22 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                 }
                 __syncwarp();
             }
-            if (c + 2 >= nch) continue;
-            if (c >= 0 && !(ok = wait(&sm.s[st], c >> 1))) break;  // K and Q are read
-            if (el) {
-                mbar_expect_tx(&sm.ld[st], (uint32_t)(2 * NT + halves) * kHalfTile);
-                const int32_t t0 = (c + 2) * kC;
+            if (c + 2 < nch) {
+                if (el) {
+                    mbar_expect_tx(&sm.ldv[st], (uint32_t)halves * kHalfTile);
 #pragma unroll 1
-                for (int i = 0; i < NT; ++i) {
-                    tma_load_3d(sm.kq[st][i], &mapK, gr * a.dstate + 64 * i, t0, (int32_t)b, &sm.ld[st]);
-                    tma_load_3d(sm.kq[st][i] + kHalfTile, &mapQ, gr * a.dstate + 64 * i, t0, (int32_t)b, &sm.ld[st]);
+                    for (int i = 0; i < halves; ++i)
+                        tma_load_3d(sm.v[st][i], &mapV, h * a.headdim + v0 + 64 * i, t0, (int32_t)b, &sm.ldv[st]);
                 }
-#pragma unroll 1
-                for (int i = 0; i < halves; ++i)
-                    tma_load_3d(sm.v[st][i], &mapV, h * a.headdim + v0 + 64 * i, t0, (int32_t)b, &sm.ld[st]);
+                if (st) ++issued_v[1]; else ++issued_v[0];
             }
-            if (st) ++issued[1]; else ++issued[0];
         }
         if (el) tma_store_wait_all<0>();
-        if (issued[0] > 0) (void)mbar_wait_2s(&sm.ld[0], (uint32_t)(issued[0] - 1) & 1u);
-        if (issued[1] > 0) (void)mbar_wait_2s(&sm.ld[1], (uint32_t)(issued[1] - 1) & 1u);
+        for (int i = 0; i < 2; ++i) {  // no copy outlives the block
+            const int n = i ? issued[1] : issued[0], nv = i ? issued_v[1] : issued_v[0];
+            if (n > 0) (void)mbar_wait_2s(&sm.ldk[i], (uint32_t)(n - 1) & 1u);
+            if (nv > 0) (void)mbar_wait_2s(&sm.ldv[i], (uint32_t)(nv - 1) & 1u);
+        }
         __syncwarp();
       } else if (warp == kRowWarps + kMatWarps + 2) {
         // -------------------------------------------------- the decays
@@ -532,7 +519,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             }
             const double end = __shfl_sync(0xffffffffu, sum, 31);
             // chunk c - 2 is done with its decays and matrices
-            if (c >= 2 && !(ok = wait(&sm.o_ready[st], (c - 2) >> 1))) break;
+            if (c >= 2 && !(ok = wait(&sm.o_taken[st], (c - 2) >> 1))) break;
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
@@ -552,31 +539,36 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
       }
     } else if (warp >= kRowWarps) {
         // ------------------------------------------- the chunk matrices
-        more_regs<kMatRegs>();
-        const int w = warp - kRowWarps;
+        fewer_regs<kMatRegs>();
+        const int w = (warp - kRowWarps) & 3, set = (warp - kRowWarps) >> 2;
         for (int c = 0; c < nch; ++c) {
             const int st = c & 1;
             // (cum comes after chunk c - 2 is done with its matrices)
             ok = wait(&sm.cum[st], c >> 1) && wait(&sm.kqd, c);
             if (!mats_all(ok)) break;
             fence_after_sync();
-            chunk_matrices<NT>(sm, c, w, lane, tm + kTO2 + ((uint32_t)(32 * w) << 16), [&] {
-                fence_before_sync();
-                signal(&sm.kq_read);
-            });
-            fence_proxy_async();
-            signal(&sm.prep[st]);
+            chunk_matrices<NT>(
+                sm, c, w, set, lane, tm + kTO2 + ((uint32_t)(32 * w) << 16),
+                [&] {
+                    fence_before_sync();
+                    signal(&sm.kq_read);
+                },
+                [&] { signal(&sm.pb[st]); });
+            if (set == 0) {
+                fence_proxy_async();
+                signal(&sm.m[st]);
+            }
         }
     } else {
         // --------------------------------------------- the row-wise work
         more_regs<kRowRegs>();
         const int quad = warp & 3, wg = warp >> 2, r = 32 * quad + lane;
-        const bool active = 32 * quad < 64 * halves;  // the warp's lanes hold rows of the state
         const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
         const int64_t row = bh * a.headdim + v0 + r;
-        const int vp = (r & 63) >> 3, vo = (r & 7) * 2;  // this row's place in a row of the V tile
+        const int vp = (((r & 63) >> 3) << 4) + (r & 7) * 2;  // this row's place in row 0 of the V tile
+      if (32 * quad < 64 * halves) {
         // the start state, where the first chunk's "last product" would have left it
-        if (active) {
+        {
 #pragma unroll 1
             for (int p = 0; p < NT; ++p) {
                 const int col = 32 * (NT * wg + p);
@@ -601,120 +593,128 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             }
             tmem_wait_st();
         }
-        uint32_t ov[16];  // the last chunk's output values, packed
-        // chunk c's state is there when chunk c - 1's last product is done; the
-        // step behind the last chunk only stores the state and the output
+        uint32_t vv[16], ov[16];  // this row's values of V and of the output, packed pairs of tokens
+        auto load_v = [&](int c) {
+            const unsigned char *vt = sm.v[c & 1][r >> 6] + 32 * wg * 128;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const unsigned short u0 = *reinterpret_cast<const unsigned short *>(vt + ((vp ^ ((i & 7) << 4)) + 128 * i));
+                const unsigned short u1 =
+                    *reinterpret_cast<const unsigned short *>(vt + ((vp ^ (((i + 1) & 7) << 4)) + 128 * (i + 1)));
+                vv[i / 2] = (uint32_t)u0 | ((uint32_t)u1 << 16);
+            }
+        };
+        // Chunk c's state is there when chunk c - 1's last product is done.  Work that
+        // no product waits for -- the last chunk's output, the next V -- stands where
+        // the warp would wait for one.  The step behind the last chunk only stores the
+        // state and the output.
         for (int c = 0; c <= nch; ++c) {
             const int st = c & 1;
             const Dec &dec = sm.dec[st];
             if (c < nch && !(ok = wait(&sm.cum[st], c >> 1))) break;
+            if (c < nch && !(ok = wait(&sm.ldv[st], c >> 1))) break;
+            if (c < nch) load_v(c);
             if (c > 0 && !(ok = wait(&sm.s[st ^ 1], (c - 1) >> 1))) break;
             fence_after_sync();
-            if (active) {
 #pragma unroll 1
-                for (int p = 0; p < NT; ++p) {
-                    const int col = 32 * (NT * wg + p);
-                    float s[32];
-                    tmem_ld32(tl + kTS + col, s);
-                    tmem_wait_ld();
-                    if (c < nch) {
-                        put_state(tl, col, s, dec.whole);
-                    } else if (a.state) {
-                        float *dst = a.state + row * a.dstate + col;
-                        if (a.vec_state) {
+            for (int p = 0; p < NT; ++p) {
+                const int col = 32 * (NT * wg + p);
+                float s[32];
+                tmem_ld32(tl + kTS + col, s);
+                tmem_wait_ld();
+                if (c < nch) {
+                    put_state(tl, col, s, dec.whole);
+                    tmem_wait_st();
+                    fence_before_sync();
+                    signal(&sm.s_ready[p]);
+                } else if (a.state) {
+                    float *dst = a.state + row * a.dstate + col;
+                    if (a.vec_state) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<float4 *>(dst + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
-                        } else {
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(dst + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+                    } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) dst[i] = s[i];
-                        }
+                        for (int i = 0; i < 32; ++i) dst[i] = s[i];
                     }
                 }
-                tmem_wait_st();
             }
-            fence_before_sync();
-            if (c < nch) signal(&sm.s_ready);
-            // while the first product runs: the last chunk's output over its V
             if (c > 0) {
-                if (active) {
-                    unsigned char *vt = sm.v[st ^ 1][r >> 6];
+                if (!(ok = wait(&sm.o, c - 1))) break;
+                fence_after_sync();
+                float o1[32], o2[32];
+                tmem_ld32(tl + kTO1 + 32 * wg, o1);
+                tmem_ld32(tl + kTO2 + 32 * wg, o2);
+                tmem_wait_ld();
+                const float *gs = sm.dec[st ^ 1].gs + 32 * wg;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int t = 32 * wg + 2 * i;
-                        *reinterpret_cast<unsigned short *>(vt + sw128_offset(t, vp) + vo) = (unsigned short)(ov[i] & 0xffffu);
-                        *reinterpret_cast<unsigned short *>(vt + sw128_offset(t + 1, vp) + vo) = (unsigned short)(ov[i] >> 16);
-                    }
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 g4 = *reinterpret_cast<const float4 *>(gs + i);
+                    ov[i / 2] = pack(fmaf(g4.x, o1[i], o2[i]), fmaf(g4.y, o1[i + 1], o2[i + 1]));
+                    ov[i / 2 + 1] = pack(fmaf(g4.z, o1[i + 2], o2[i + 2]), fmaf(g4.w, o1[i + 3], o2[i + 3]));
+                }
+                fence_before_sync();
+                signal(&sm.o_taken[st ^ 1]);
+            }
+            float res[32];
+            if (c < nch) {
+                // R = V - gam X, and R as an operand
+                if (!(ok = wait(&sm.x, c))) break;
+                fence_after_sync();
+                tmem_ld32(tl + kTX + 32 * wg, res);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 g4 = *reinterpret_cast<const float4 *>(&dec.gam[32 * wg + i]);
+                    res[i] = fmaf(-g4.x, res[i], low_of(vv[i / 2]));
+                    res[i + 1] = fmaf(-g4.y, res[i + 1], high_of(vv[i / 2]));
+                    res[i + 2] = fmaf(-g4.z, res[i + 2], low_of(vv[i / 2 + 1]));
+                    res[i + 3] = fmaf(-g4.w, res[i + 3], high_of(vv[i / 2 + 1]));
+                }
+                put_terms(tl + kTX + 32 * wg, tl + kTX + 32 * wg + 16, res);
+                tmem_wait_st();
+                fence_before_sync();
+                signal(&sm.r_ready);
+            }
+            if (c > 0) {  // the last chunk's output over its V
+                unsigned char *vt = sm.v[st ^ 1][r >> 6] + 32 * wg * 128;
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    *reinterpret_cast<unsigned short *>(vt + ((vp ^ ((i & 7) << 4)) + 128 * i)) =
+                        (unsigned short)(ov[i / 2] & 0xffffu);
+                    *reinterpret_cast<unsigned short *>(vt + ((vp ^ (((i + 1) & 7) << 4)) + 128 * (i + 1))) =
+                        (unsigned short)(ov[i / 2] >> 16);
                 }
                 fence_proxy_async();
                 signal(&sm.o_ready[st ^ 1]);
             }
             if (c == nch) break;
-            // this row's 32 values of V, R = V - gam X, and R as an operand
-            float res[32];
-            if (!(ok = wait(&sm.ld[st], c >> 1))) break;
-            if (active) {
-                const unsigned char *vt = sm.v[st][r >> 6];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const unsigned short u =
-                        *reinterpret_cast<const unsigned short *>(vt + sw128_offset(32 * wg + i, vp) + vo);
-                    res[i] = __uint_as_float((uint32_t)u << 16);
-                }
-            }
-            if (!(ok = wait(&sm.x, c))) break;
-            fence_after_sync();
-            if (active) {
-                float x[32];
-                tmem_ld32(tl + kTX + 32 * wg, x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 g4 = *reinterpret_cast<const float4 *>(&dec.gam[32 * wg + i]);
-                    res[i] = fmaf(-g4.x, x[i], res[i]);
-                    res[i + 1] = fmaf(-g4.y, x[i + 1], res[i + 1]);
-                    res[i + 2] = fmaf(-g4.z, x[i + 2], res[i + 2]);
-                    res[i + 3] = fmaf(-g4.w, x[i + 3], res[i + 3]);
-                }
-                put_terms(tl + kTX + 32 * wg, tl + kTX + 32 * wg + 16, res);
-                tmem_wait_st();
-            }
-            fence_before_sync();
-            signal(&sm.r_ready);
-            // r = R - Y, and w beta r as an operand
+            // r = R - Y; w beta r and then r as operands
             if (!(ok = wait(&sm.y, c))) break;
             fence_after_sync();
-            if (active) {
-                float y[32];
-                tmem_ld32(tl + kTY + 32 * wg, y);
-                tmem_wait_ld();
+            float y[32];
+            tmem_ld32(tl + kTY + 32 * wg, y);
+            tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 w4 = *reinterpret_cast<const float4 *>(&dec.wb[32 * wg + i]);
-                    y[i] = w4.x * (res[i] - y[i]);
-                    y[i + 1] = w4.y * (res[i + 1] - y[i + 1]);
-                    y[i + 2] = w4.z * (res[i + 2] - y[i + 2]);
-                    y[i + 3] = w4.w * (res[i + 3] - y[i + 3]);
+            for (int i = 0; i < 32; i += 4) {
+                const float4 w4 = *reinterpret_cast<const float4 *>(&dec.wb[32 * wg + i]);
+                const float ww[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    res[i + e] -= y[i + e];
+                    y[i + e] = ww[e] * res[i + e];
                 }
-                put_terms(tl + kTY + 32 * wg, tl + kTY + 32 * wg + 16, y);
-                tmem_wait_st();
             }
+            put_terms(tl + kTY + 32 * wg, tl + kTY + 32 * wg + 16, y);
+            tmem_wait_st();
+            fence_before_sync();
+            signal(&sm.w_ready);
+            put_terms(tl + kTX + 32 * wg, tl + kTX + 32 * wg + 16, res);
+            tmem_wait_st();
             fence_before_sync();
             signal(&sm.u_ready);
-            // the output's values, while the state's product runs
-            if (active) {
-                float o1[32], o2[32];
-                tmem_ld32(tl + kTO1 + 32 * wg, o1);
-                tmem_ld32(tl + kTO2 + 32 * wg, o2);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 g4 = *reinterpret_cast<const float4 *>(&dec.gs[32 * wg + i]);
-                    ov[i / 2] = pack(fmaf(g4.x, o1[i], o2[i]), fmaf(g4.y, o1[i + 1], o2[i + 1]));
-                    ov[i / 2 + 1] = pack(fmaf(g4.z, o1[i + 2], o2[i + 2]), fmaf(g4.w, o1[i + 3], o2[i + 3]));
-                }
-            }
         }
+      }
     }
     if (!ok && lane == 0) atomicOr(a.status, 4u);
     fence_before_sync();
