@@ -12,8 +12,8 @@
 //   S          = gam_C S + (w beta r)^T K         (128 x dstate, K = 64),   r = R - Y
 //   O2^T       = r^T Pb^T                         (128 x 64,  K = 64)
 //   out        = scale gam O1 + O2
-// with M = N beta = I - (I + L)^-1, L = Abar beta, and Pb = P beta.  What the next
-// row-wise step waits for is issued first: X before O1, the state before O2.
+// with M = N beta = I - (I + L)^-1, L = Abar beta, and Pb = P beta.  The state's
+// product, which the next chunk waits for, goes before O2.
 // Operands that are not bf16 already take two bf16 terms (state: 2 products
 // instead of 1; R, r with M, Pb: 3).
 //
@@ -362,16 +362,17 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
       if (warp == kRowWarps + kMatWarps) {
         // ------------------------------------------------ the products
         const uint32_t el = elect_one();
+        constexpr uint32_t id_128 = idesc_bf16(128, 128, kMajorK, kMajorK);
         constexpr uint32_t id_64 = idesc_bf16(128, 64, kMajorK, kMajorK);
         constexpr uint32_t id_s = idesc_bf16(128, 64 * NT, kMajorK, kMajorMN);
         // (unrolled: in a loop one product took 110 clocks to issue, 32 to run)
         // Tiles as right operands: K rows, then Q rows (M, then Pb - Pb M).
-        auto state_product = [&](uint64_t tile, uint32_t d, int part) {  // S's 32-column pieces `part` of both halves
+        auto state_product = [&](uint64_t tile, int part) {  // S's 32-column pieces `part` of both halves
 #pragma unroll
             for (int i = 0; i < 8; ++i) {  // two pieces of two steps, high terms, then low ones
                 const int k = 2 * NT * ((i >> 1) & 1) + 2 * part + (i & 1);
-                mma_bf16_ts_if(el, tm + d, tm + (i < 4 ? kTSh : kTSl) + 8 * k,
-                               tile + (((k / 4) * 2 * kHalfTile + (k % 4) * 32) >> 4), id_64, part > 0 || i > 0);
+                mma_bf16_ts_if(el, tm + kTX, tm + (i < 4 ? kTSh : kTSl) + 8 * k,
+                               tile + (((k / 4) * 2 * kHalfTile + (k % 4) * 32) >> 4), id_128, part > 0 || i > 0);
             }
         };
         auto r_product = [&](uint64_t high, uint64_t low, uint32_t d) {
@@ -386,19 +387,16 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         for (int c = -1; ok && c < nch; ++c) {
             const int st = c & 1;
             if (c >= 0) {
-                const uint64_t dk = desc_sw128(smem_u32(sm.kq[st][0]), 16, 1024), dq = dk + (kHalfTile >> 4);
+                const uint64_t dk = desc_sw128(smem_u32(sm.kq[st][0]), 16, 1024);
+                if (c > 0 && !(ok = wait(&sm.o_taken[st ^ 1], (c - 1) >> 1))) break;
 #pragma unroll
                 for (int part = 0; part < NT; ++part) {
                     if (!(ok = wait(&sm.s_ready[part], c))) break;
                     fence_after_sync();
-                    state_product(dk, kTX, part);
+                    state_product(dk, part);
                 }
                 if (!ok) break;
                 mma_commit_if(el, &sm.x);
-                if (c > 0 && !(ok = wait(&sm.o_taken[st ^ 1], (c - 1) >> 1))) break;
-                fence_after_sync();
-#pragma unroll
-                for (int part = 0; part < NT; ++part) state_product(dq, kTO1, part);
                 // (chunk 0's product has to be read before chunk 1's replaces it)
                 if (c == 0 && !(ok = wait(&sm.kq_read, 0))) break;
             }
@@ -614,6 +612,23 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             if (c < nch && !(ok = wait(&sm.cum[st], c >> 1))) break;
             if (c < nch && !(ok = wait(&sm.ldv[st], c >> 1))) break;
             if (c < nch) load_v(c);
+            if (c > 0) {
+                if (!(ok = wait(&sm.o, c - 1))) break;
+                fence_after_sync();
+                float o1[32], o2[32];
+                tmem_ld32(tl + kTO1 + 32 * wg, o1);
+                tmem_ld32(tl + kTO2 + 32 * wg, o2);
+                tmem_wait_ld();
+                const float *gs = sm.dec[st ^ 1].gs + 32 * wg;
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 g4 = *reinterpret_cast<const float4 *>(gs + i);
+                    ov[i / 2] = pack(fmaf(g4.x, o1[i], o2[i]), fmaf(g4.y, o1[i + 1], o2[i + 1]));
+                    ov[i / 2 + 1] = pack(fmaf(g4.z, o1[i + 2], o2[i + 2]), fmaf(g4.w, o1[i + 3], o2[i + 3]));
+                }
+                fence_before_sync();
+                signal(&sm.o_taken[st ^ 1]);
+            }
             if (c > 0 && !(ok = wait(&sm.s[st ^ 1], (c - 1) >> 1))) break;
             fence_after_sync();
 #pragma unroll 1
@@ -638,23 +653,6 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                         for (int i = 0; i < 32; ++i) dst[i] = s[i];
                     }
                 }
-            }
-            if (c > 0) {
-                if (!(ok = wait(&sm.o, c - 1))) break;
-                fence_after_sync();
-                float o1[32], o2[32];
-                tmem_ld32(tl + kTO1 + 32 * wg, o1);
-                tmem_ld32(tl + kTO2 + 32 * wg, o2);
-                tmem_wait_ld();
-                const float *gs = sm.dec[st ^ 1].gs + 32 * wg;
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 g4 = *reinterpret_cast<const float4 *>(gs + i);
-                    ov[i / 2] = pack(fmaf(g4.x, o1[i], o2[i]), fmaf(g4.y, o1[i + 1], o2[i + 1]));
-                    ov[i / 2 + 1] = pack(fmaf(g4.z, o1[i + 2], o2[i + 2]), fmaf(g4.w, o1[i + 3], o2[i + 3]));
-                }
-                fence_before_sync();
-                signal(&sm.o_taken[st ^ 1]);
             }
             float res[32];
             if (c < nch) {
