@@ -18,6 +18,7 @@
 // dG needs no difference of large sums: its terms are row products that exist
 // anyway, and <S1, dS1> = gam_C <S0, dS1> + sum_t k_t . (w u dS1)_t.
 #include "delta_chunk.cuh"
+#include "kernel_setup.cuh"
 
 namespace ssm {
 namespace delta {
@@ -249,8 +250,7 @@ cudaError_t launch_reverse_t(const DeltaBwdArgs &p, const DeltaChunkWs &ws, int 
     while (w > 1 && a.batch * a.heads * ((a.headdim + 16 * w - 1) / (16 * w)) < sms) w = (w + 1) / 2;
     const int vtiles = (a.headdim + 16 * w - 1) / (16 * w);
     const int bytes = 2 * stage_bytes<NP>(w);
-    cudaError_t e = cudaFuncSetAttribute(delta_reverse_kernel<NP, VECQK, VECV>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_smem<delta_reverse_kernel<NP, VECQK, VECV>, 2 * stage_bytes<NP>(8)>();
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.batch * a.heads * vtiles));
     delta_reverse_kernel<NP, VECQK, VECV><<<grid, 32 * w, bytes, st>>>(p, ws, vtiles);
@@ -271,7 +271,7 @@ struct GradSmem {  // headdim rounded up to 16 (pp) decides the sizes of the res
     float part[kGradThreads / 32];
 };
 template <int NP>
-size_t grad_smem_bytes(int pp) {
+constexpr size_t grad_smem_bytes(int pp) {
     return sizeof(GradSmem<NP>) + (size_t)(5 * kC * (pp + 8) + 2 * pp * (NP + 8)) * sizeof(bf16);
 }
 
@@ -618,8 +618,7 @@ template <int NP, bool VECQK, bool VECV>
 cudaError_t launch_grad_t(const DeltaBwdArgs &p, const DeltaChunkWs &ws, cudaStream_t st) {
     const DeltaArgs &a = p.f;
     const size_t bytes = grad_smem_bytes<NP>((a.headdim + 15) / 16 * 16);
-    cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<NP, VECQK, VECV>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    cudaError_t e = allow_smem<delta_grad_kernel<NP, VECQK, VECV>, (int)grad_smem_bytes<NP>(kDeltaMaxDstate)>();
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.batch * a.groups * ((a.seqlen + kC - 1) / kC)));
     delta_grad_kernel<NP, VECQK, VECV><<<grid, kGradThreads, bytes, st>>>(p, ws);

@@ -9,6 +9,7 @@
 // divided over blocks.  e solves e = dU - Abar^T (beta e) by substitution from
 // the last token, one thread per column of V.
 #include "delta_rule.cuh"
+#include "kernel_setup.cuh"
 #include "ssm_device.cuh"
 
 namespace ssm {
@@ -18,9 +19,8 @@ constexpr int kT = kDeltaStep, kThreadsD = 256;
 
 struct Layout {  // float offsets in shared memory
     int ldn, ldp, ds, s0, q, k, o, r, e, l, kk, pm, x, em, cum, total;
-    __host__ __device__ Layout(int P, int N) {
-        ldn = N | 1;  // odd strides: a column read by a warp falls into different banks
-        ldp = P | 1;
+    __host__ __device__ constexpr Layout(int P, int N) : ldn(N | 1), ldp(P | 1), ds(0), s0(0), q(0), k(0), o(0), r(0), e(0), l(0), kk(0), pm(0), x(0), em(0), cum(0), total(0) {
+        // odd strides: a column read by a warp falls into different banks
         int at = 0;
         cum = at; at += 2 * (kT + 2);  // doubles first
         ds = at; at += P * ldn;
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(256) delta_group_sum_kernel(const float *dq_he
 cudaError_t launch_delta_bwd_direct(const DeltaBwdArgs &p, cudaStream_t st) {
     const DeltaArgs &a = p.f;
     const int bytes = Layout(a.headdim, a.dstate).total * (int)sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(delta_bwd_direct_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_smem<delta_bwd_direct_kernel, 4 * Layout(kDeltaMaxDstate, kDeltaMaxDstate).total>();
     if (e != cudaSuccess) return e;
     delta_bwd_direct_kernel<<<(unsigned)(a.batch * a.heads), kThreadsD, bytes, st>>>(p);
     e = cudaGetLastError();

@@ -13,6 +13,7 @@
 // K, Q, V, N and P, which cp.async brings one chunk ahead (two stages).
 // Products of the state or of r take two bf16 terms of each (delta_chunk.cuh).
 #include "delta_chunk.cuh"
+#include "kernel_setup.cuh"
 
 namespace ssm {
 namespace delta {
@@ -258,8 +259,7 @@ cudaError_t launch_t(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaSt
     while (w > 1 && a.batch * a.heads * ((a.headdim + 16 * w - 1) / (16 * w)) < sms) w = (w + 1) / 2;
     const int vtiles = (a.headdim + 16 * w - 1) / (16 * w);
     const int bytes = 2 * stage_bytes<NP>(w);
-    cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<NP, VECQK, VECV, STORE>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_smem<delta_chain_kernel<NP, VECQK, VECV, STORE>, 2 * stage_bytes<NP>(8)>();
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.batch * a.heads * vtiles));
     delta_chain_kernel<NP, VECQK, VECV, STORE><<<grid, 32 * w, bytes, st>>>(a, ws, vtiles);

@@ -30,6 +30,7 @@
 // decays.  They meet at mbarriers only; every wait is bounded and reports
 // through the device status word.
 #include "delta_chunk.cuh"
+#include "kernel_setup.cuh"
 #include "scan_kernels.cuh"
 #include "ssm_device.cuh"
 #include "tma_maps.cuh"
@@ -737,7 +738,7 @@ cudaError_t launch_t(const DeltaArgs &a, cudaStream_t st) {
     cudaError_t e = device_status_address(&f.status);
     if (e != cudaSuccess) return e;
     constexpr int bytes = (int)sizeof(FusedSmem<NT>) + 1024;
-    e = cudaFuncSetAttribute(delta_fused_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = allow_smem<delta_fused_kernel<NT>, bytes>();
     if (e != cudaSuccess) return e;
     delta_fused_kernel<NT><<<(unsigned)(a.batch * a.heads * f.vtiles), kThreadsF, bytes, st>>>(mq, mk, mv, mo, f);
     return cudaGetLastError();

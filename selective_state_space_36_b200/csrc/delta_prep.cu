@@ -11,6 +11,7 @@
 // rows above enter as a product with broadcast reads, the 16 x 16 block on
 // the diagonal is unrolled.
 #include "delta_chunk.cuh"
+#include "kernel_setup.cuh"
 
 namespace ssm {
 namespace delta {
@@ -166,8 +167,7 @@ template <int NP, bool VEC>
 cudaError_t launch_t(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st) {
     const int64_t units = a.batch * a.heads * ((a.seqlen + kC - 1) / kC);
     const size_t bytes = sizeof(PrepSmem<NP>);
-    cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel<NP, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)bytes);
+    cudaError_t e = allow_smem<delta_prep_kernel<NP, VEC>, (int)sizeof(PrepSmem<NP>)>();
     if (e != cudaSuccess) return e;
     delta_prep_kernel<NP, VEC><<<(unsigned)units, kPrepThreads, bytes, st>>>(a, ws);
     return cudaGetLastError();

@@ -20,6 +20,7 @@
 // the registers are walked twice (forward, dx), and their column sums come
 // from a kernel of their own over tiles of columns.
 #include "cp_async.cuh"
+#include "kernel_setup.cuh"
 #include "norm.cuh"
 #include "ssm_device.cuh"
 
@@ -536,14 +537,6 @@ int64_t walkers(int64_t rows, int rows_per_block, int per_sm, int sms) {
     return all < most ? all : most;
 }
 
-template <typename K>
-cudaError_t resident(K kernel, int smem, int *per_sm) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kernel, kThreads, smem);
-    if (e == cudaSuccess && *per_sm < 1) *per_sm = 1;
-    return e;
-}
-
 struct Fwd {
     const NormArgs &a;
     int sms;
@@ -552,7 +545,7 @@ struct Fwd {
     cudaError_t go() const {
         constexpr int smem = Rows<T, VEC, NV, GATE ? 2 : 1>::kBytes;
         int per_sm = 1;
-        cudaError_t e = resident(norm_fwd_kernel<T, VEC, TPR, NV, GATE>, smem, &per_sm);
+        cudaError_t e = resident_blocks<norm_fwd_kernel<T, VEC, TPR, NV, GATE>, kThreads, smem>(&per_sm);
         if (e != cudaSuccess) return e;
         const int64_t blocks = walkers(a.rows, kThreads / TPR, per_sm, sms);
         norm_fwd_kernel<T, VEC, TPR, NV, GATE><<<(unsigned)blocks, kThreads, smem, st>>>(a);
@@ -573,7 +566,7 @@ struct Bwd {
         constexpr int smem = Rows<T, VEC, NV, GATE ? 3 : 2>::kBytes;
         if (!launch) {
             int per_sm = 1;
-            cudaError_t e = resident(norm_bwd_kernel<T, VEC, TPR, NV, GATE>, smem, &per_sm);
+            cudaError_t e = resident_blocks<norm_bwd_kernel<T, VEC, TPR, NV, GATE>, kThreads, smem>(&per_sm);
             *parts = walkers(a.rows, kThreads / TPR, per_sm, sms);
             return e;
         }

@@ -845,6 +845,16 @@ void ssm_test_inject_decode_wait_timeout(int32_t enable) { g_inject_wait_bytes.s
 
 namespace {
 
+// The current device's SMs, asked of the runtime once per device.
+int device_sms() {
+    static std::atomic<int> sms[kMaxPoolDevices];
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxPoolDevices) return device_info().sms;
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (n == 0) sms[dev].store(n = device_info().sms, std::memory_order_relaxed);
+    return n;
+}
+
 // bf16 sequences up to this many tokens run token by token (one launch, no
 // workspace), longer ones in chunks on the tensor cores.
 constexpr int64_t kDeltaRecurrentTokens = 32;
@@ -931,7 +941,7 @@ ssm_status delta_forward(ssm_ssd_dims dims, ssm_dtype io, const void *q, const v
     cudaError_t e = delta_chunk_workspace(units, 0, 0, &mem, &ws, st);
     if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
     e = ssm::launch_delta_prep(a, ws, st);
-    if (e == cudaSuccess) e = ssm::launch_delta_chain(a, ws, device_info().sms, st);
+    if (e == cudaSuccess) e = ssm::launch_delta_chain(a, ws, device_sms(), st);
     cudaError_t ef = cudaFreeAsync(mem, st);
     if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
     if (ef != cudaSuccess) return cuda_fail(ef, "workspace release");
@@ -1010,7 +1020,7 @@ ssm_status ssm_delta_rule_bwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, co
     cudaError_t e;
     if (io == SSM_BF16) {
         ssm::DeltaChunkWs ws{};
-        const int sms = device_info().sms;
+        const int sms = device_sms();
         e = delta_chunk_workspace(units, (dims.headdim + 15) / 16 * 16, dims.dstate <= 64 ? 64 : 128, &mem, &ws, st);
         if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
         e = ssm::launch_delta_prep(p.f, ws, st);
@@ -1061,7 +1071,7 @@ ssm_status ssm_norm_fwd(int64_t rows, int64_t dim, ssm_dtype io, int mode, const
     ssm::NormArgs a{};
     a.x = x; a.z = z; a.weight = weight; a.bias = bias; a.out = out; a.mean = mean; a.rstd = rstd;
     a.rows = rows; a.dim = (int)dim; a.eps = eps; a.center = mode == SSM_NORM_LAYER;
-    cudaError_t e = ssm::launch_norm_fwd(a, io == SSM_BF16, device_info().sms, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = ssm::launch_norm_fwd(a, io == SSM_BF16, device_sms(), reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "norm launch");
     return SSM_OK;
 }
@@ -1101,7 +1111,7 @@ ssm_status ssm_norm_bwd(int64_t rows, int64_t dim, ssm_dtype io, int mode, const
     const ssm::NormAlloc alloc = [](size_t bytes, cudaStream_t on, float **p) {
         return workspace_alloc(reinterpret_cast<void **>(p), bytes, on);
     };
-    cudaError_t e = ssm::launch_norm_bwd(a, io == SSM_BF16, device_info().sms, alloc, st);
+    cudaError_t e = ssm::launch_norm_bwd(a, io == SSM_BF16, device_sms(), alloc, st);
     if (e != cudaSuccess) return cuda_fail(e, "norm gradient launch");
     return SSM_OK;
 }
