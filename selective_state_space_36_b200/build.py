@@ -1,4 +1,5 @@
-"""Compile the CUDA sources of the library into libssm_b200.so (sm_100a).
+"""Compile the CUDA sources of the library into libssm_b200.so (sm_100a) and the
+binding's native part into _native.so.
 
 Run as ``python -m selective_state_space_36_b200.build`` or call ``build()``.
 nvcc cross-compiles, so no GPU is needed to build.
@@ -15,6 +16,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libssm_b200.so")
+NATIVE_SRC = os.path.join(CSRC, "binding_native.cpp")
+NATIVE = os.path.join(HERE, "_native.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -34,15 +37,15 @@ def sources():
 
 
 def _deps():
-    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    files = sources() + [NATIVE_SRC] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "ssm.h"))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -71,7 +74,30 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_native()
     return LIB
+
+
+def build_native() -> str:
+    """The binding's C++ part: a CPython module on torch's headers, linked to the
+    library beside it."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
+           *(a for p in include for a in ("-isystem", p)), f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           NATIVE_SRC, "-o", tmp, "-L" + HERE, "-l:" + os.path.basename(LIB), "-L" + os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {NATIVE_SRC}:\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+    return NATIVE
 
 
 if __name__ == "__main__":

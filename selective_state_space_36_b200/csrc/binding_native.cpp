@@ -1,0 +1,273 @@
+// binding_native.cpp -- argument marshalling of the small entry points (delta
+// rule, norm) for torch tensors, as a CPython module.
+//
+// The same checks as binding.py's, on the tensors' C++ side: a decode step or a
+// norm of a few rows runs for 2-3 us on the GPU, the checks and allocations in
+// Python alone take 8-12 us.  A call whose arguments are in order goes straight
+// to the C ABI; for any other call the function returns NotImplemented, and
+// binding.py repeats the checks to raise the error that names the argument.
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cmath>
+
+#include "../../include/ssm.h"
+
+namespace {
+
+// A call's tensors: their device and I/O type, and whether all are in order.
+struct Args {
+    c10::Device dev;
+    at::ScalarType io;
+    bool ok = true;
+
+    explicit Args(const at::Tensor &lead) : dev(lead.device()), io(lead.scalar_type()) {
+        ok = dev.is_cuda() && dev.index() == c10::cuda::current_device() && (io == at::kFloat || io == at::kBFloat16) &&
+             lead.is_contiguous();
+    }
+    ssm_dtype dtype() const { return io == at::kFloat ? SSM_F32 : SSM_BF16; }
+
+    // The data pointer of a tensor of this type and shape; null for None and for
+    // tensors without elements, as binding.py passes them.
+    void *ptr(PyObject *o, at::ScalarType type, at::IntArrayRef shape) {
+        if (o == Py_None || !ok) return nullptr;
+        if (!THPVariable_Check(o)) {
+            ok = false;
+            return nullptr;
+        }
+        const at::Tensor &t = THPVariable_Unpack(o);
+        if (t.scalar_type() != type || t.device() != dev || t.sizes() != shape || !t.is_contiguous()) {
+            ok = false;
+            return nullptr;
+        }
+        return t.numel() ? t.data_ptr() : nullptr;
+    }
+    at::Tensor empty(at::ScalarType type, at::IntArrayRef shape) const {
+        return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+    }
+    ssm_stream stream() const {
+        return reinterpret_cast<ssm_stream>(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
+    }
+};
+
+PyObject *not_implemented() { Py_RETURN_NOTIMPLEMENTED; }
+
+// Strided, real, non-subclassed: THPVariable_Check accepts all kinds of tensors.
+bool plain(PyObject *o, int64_t ndim) {
+    if (!THPVariable_CheckExact(o)) return false;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    return t.layout() == at::kStrided && t.dim() == ndim;
+}
+
+void *data(const at::Tensor &t) { return t.numel() ? t.data_ptr() : nullptr; }
+
+// (status, result): the result is returned if the status is SSM_OK, else the
+// status, which binding.py turns into its error.
+PyObject *finish(ssm_status s, PyObject *result) {
+    if (s == SSM_OK) return result;
+    Py_DECREF(result);
+    return PyLong_FromLong(s);
+}
+
+// a kernel launch needs no interpreter
+template <typename F>
+ssm_status unlocked(F f) {
+    ssm_status s;
+    Py_BEGIN_ALLOW_THREADS
+    s = f();
+    Py_END_ALLOW_THREADS
+    return s;
+}
+
+bool scale_of(PyObject *o, int64_t dstate, float *scale) {
+    if (o == Py_None) {
+        *scale = (float)std::pow((double)dstate, -0.5);
+        return true;
+    }
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        return false;
+    }
+    *scale = (float)v;
+    return true;
+}
+
+// (q, k, v, g, beta, scale, out, last_state) -> out
+PyObject *delta_rule_fwd(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    if (n != 8 || !plain(o[0], 4) || !plain(o[2], 4)) return not_implemented();
+    const at::Tensor &q = THPVariable_Unpack(o[0]), &v = THPVariable_Unpack(o[2]);
+    Args a(v);
+    const int64_t B = v.size(0), L = v.size(1), H = v.size(2), P = v.size(3), G = q.size(2), N = q.size(3);
+    float scale;
+    if (!a.ok || !scale_of(o[5], N, &scale)) return not_implemented();
+    void *pq = a.ptr(o[0], a.io, {B, L, G, N}), *pk = a.ptr(o[1], a.io, {B, L, G, N});
+    float *g = (float *)a.ptr(o[3], at::kFloat, {B, L, H}), *beta = (float *)a.ptr(o[4], at::kFloat, {B, L, H});
+    void *po = a.ptr(o[6], a.io, {B, L, H, P});
+    float *state = (float *)a.ptr(o[7], at::kFloat, {B, H, P, N});
+    if (!a.ok) return not_implemented();
+    PyObject *result = o[6];
+    if (result == Py_None) {
+        const at::Tensor out = a.empty(a.io, {B, L, H, P});
+        po = data(out);
+        result = THPVariable_Wrap(out);
+    } else {
+        Py_INCREF(result);
+    }
+    void *pv = data(v);
+    const ssm_stream st = a.stream();
+    return finish(unlocked([&] { return ssm_delta_rule_fwd({B, L, H, P, G, N}, a.dtype(), pq, pk, pv, g, beta, scale, po, state, st); }), result);
+}
+
+// (state, q, k, v, g, beta, scale, out) -> out
+PyObject *delta_rule_update(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    if (n != 8 || !plain(o[1], 3) || !plain(o[3], 3)) return not_implemented();
+    const at::Tensor &q = THPVariable_Unpack(o[1]), &v = THPVariable_Unpack(o[3]);
+    Args a(v);
+    const int64_t B = v.size(0), H = v.size(1), P = v.size(2), G = q.size(1), N = q.size(2);
+    float scale;
+    if (!a.ok || !scale_of(o[6], N, &scale)) return not_implemented();
+    float *state = (float *)a.ptr(o[0], at::kFloat, {B, H, P, N});
+    void *pq = a.ptr(o[1], a.io, {B, G, N}), *pk = a.ptr(o[2], a.io, {B, G, N});
+    float *g = (float *)a.ptr(o[4], at::kFloat, {B, H}), *beta = (float *)a.ptr(o[5], at::kFloat, {B, H});
+    void *po = a.ptr(o[7], a.io, {B, H, P});
+    if (!a.ok) return not_implemented();
+    PyObject *result = o[7];
+    if (result == Py_None) {
+        const at::Tensor out = a.empty(a.io, {B, H, P});
+        po = data(out);
+        result = THPVariable_Wrap(out);
+    } else {
+        Py_INCREF(result);
+    }
+    void *pv = data(v);
+    const ssm_stream st = a.stream();
+    return finish(unlocked([&] { return ssm_delta_rule_update({B, 1, H, P, G, N}, a.dtype(), state, pq, pk, pv, g, beta, scale, po, st); }), result);
+}
+
+// (q, k, v, g, beta, dout, scale, h0, dlast_state, want_dh0) -> (dq, dk, dv, dg, dbeta, dh0)
+PyObject *delta_rule_bwd(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    if (n != 10 || !plain(o[0], 4) || !plain(o[2], 4)) return not_implemented();
+    const at::Tensor &q = THPVariable_Unpack(o[0]), &v = THPVariable_Unpack(o[2]);
+    Args a(v);
+    const int64_t B = v.size(0), L = v.size(1), H = v.size(2), P = v.size(3), G = q.size(2), N = q.size(3);
+    float scale;
+    if (!a.ok || !scale_of(o[6], N, &scale)) return not_implemented();
+    void *pq = a.ptr(o[0], a.io, {B, L, G, N}), *pk = a.ptr(o[1], a.io, {B, L, G, N});
+    float *g = (float *)a.ptr(o[3], at::kFloat, {B, L, H}), *beta = (float *)a.ptr(o[4], at::kFloat, {B, L, H});
+    void *pdo = a.ptr(o[5], a.io, {B, L, H, P});
+    float *h0 = (float *)a.ptr(o[7], at::kFloat, {B, H, P, N}), *dend = (float *)a.ptr(o[8], at::kFloat, {B, H, P, N});
+    const int want = PyObject_IsTrue(o[9]);
+    if (!a.ok || want < 0) return not_implemented();
+    const at::Tensor dq = a.empty(a.io, {B, L, G, N}), dk = a.empty(a.io, {B, L, G, N}), dv = a.empty(a.io, {B, L, H, P});
+    const at::Tensor dg = a.empty(at::kFloat, {B, L, H}), dbeta = a.empty(at::kFloat, {B, L, H});
+    at::Tensor dh0;
+    if (want || o[7] != Py_None) dh0 = a.empty(at::kFloat, {B, H, P, N});
+    void *pv = data(v), *pdq = data(dq), *pdk = data(dk), *pdv = data(dv);
+    float *pdg = (float *)data(dg), *pdb = (float *)data(dbeta), *pdh = dh0.defined() ? (float *)data(dh0) : nullptr;
+    const ssm_stream st = a.stream();
+    const ssm_status s = unlocked([&] {
+        return ssm_delta_rule_bwd({B, L, H, P, G, N}, a.dtype(), pq, pk, pv, g, beta, scale, h0, pdo, dend, pdq, pdk, pdv, pdg, pdb,
+                                  pdh, st);
+    });
+    if (s != SSM_OK) return PyLong_FromLong(s);
+    PyObject *last = Py_None;
+    if (dh0.defined()) last = THPVariable_Wrap(dh0);
+    else Py_INCREF(last);
+    return Py_BuildValue("(NNNNNN)", THPVariable_Wrap(dq), THPVariable_Wrap(dk), THPVariable_Wrap(dv), THPVariable_Wrap(dg),
+                         THPVariable_Wrap(dbeta), last);
+}
+
+// (x, weight, bias, z, eps, rms, out) -> (out, mean, rstd)
+PyObject *norm_fwd(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    if (n != 7 || !THPVariable_CheckExact(o[0])) return not_implemented();
+    const at::Tensor &x = THPVariable_Unpack(o[0]);
+    if (x.layout() != at::kStrided || x.dim() < 1) return not_implemented();
+    Args a(x);
+    const int64_t dim = x.size(-1), rows = dim ? x.numel() / dim : 0;
+    const double eps = PyFloat_AsDouble(o[4]);
+    const long rms = PyLong_AsLong(o[5]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return not_implemented();
+    }
+    float *w = (float *)a.ptr(o[1], at::kFloat, {dim}), *b = (float *)a.ptr(o[2], at::kFloat, {dim});
+    void *z = a.ptr(o[3], a.io, x.sizes()), *po = a.ptr(o[6], a.io, x.sizes());
+    if (!a.ok) return not_implemented();
+    const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
+    at::Tensor mean, rstd = a.empty(at::kFloat, lead);
+    if (!rms) mean = a.empty(at::kFloat, lead);
+    PyObject *out = o[6];
+    if (out == Py_None) {
+        const at::Tensor t = a.empty(a.io, x.sizes());
+        po = data(t);
+        out = THPVariable_Wrap(t);
+    } else {
+        Py_INCREF(out);
+    }
+    void *px = data(x);
+    float *pm = mean.defined() ? (float *)data(mean) : nullptr, *pr = (float *)data(rstd);
+    const ssm_stream st = a.stream();
+    const ssm_status s = unlocked([&] {
+        return ssm_norm_fwd(rows, dim, a.dtype(), rms ? SSM_NORM_RMS : SSM_NORM_LAYER, px, w, b, z, (float)eps, po, pm, pr, st);
+    });
+    PyObject *m = Py_None;
+    if (mean.defined()) m = THPVariable_Wrap(mean);
+    else Py_INCREF(m);
+    return finish(s, Py_BuildValue("(NNN)", out, m, THPVariable_Wrap(rstd)));
+}
+
+// (x, weight, dout, rstd, mean, bias, z) -> (dx, dz, dweight, dbias)
+PyObject *norm_bwd(PyObject *, PyObject *const *o, Py_ssize_t n) {
+    if (n != 7 || !THPVariable_CheckExact(o[0])) return not_implemented();
+    const at::Tensor &x = THPVariable_Unpack(o[0]);
+    if (x.layout() != at::kStrided || x.dim() < 1) return not_implemented();
+    Args a(x);
+    const int64_t dim = x.size(-1), rows = dim ? x.numel() / dim : 0;
+    const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
+    float *w = (float *)a.ptr(o[1], at::kFloat, {dim}), *b = (float *)a.ptr(o[5], at::kFloat, {dim});
+    void *dout = a.ptr(o[2], a.io, x.sizes()), *z = a.ptr(o[6], a.io, x.sizes());
+    float *rstd = (float *)a.ptr(o[3], at::kFloat, lead), *mean = (float *)a.ptr(o[4], at::kFloat, lead);
+    if (!a.ok) return not_implemented();
+    const at::Tensor dx = a.empty(a.io, x.sizes());
+    at::Tensor dz, dw, db;
+    if (o[6] != Py_None) dz = a.empty(a.io, x.sizes());
+    if (o[1] != Py_None) dw = a.empty(at::kFloat, {dim});
+    if (o[5] != Py_None) db = a.empty(at::kFloat, {dim});
+    auto at_of = [](const at::Tensor &t) { return t.defined() ? data(t) : nullptr; };
+    void *px = data(x), *pdx = data(dx), *pdz = at_of(dz);
+    float *pw = (float *)at_of(dw), *pb = (float *)at_of(db);
+    const int mode = o[4] == Py_None ? SSM_NORM_RMS : SSM_NORM_LAYER;
+    const ssm_stream st = a.stream();
+    const ssm_status s = unlocked([&] {
+        return ssm_norm_bwd(rows, dim, a.dtype(), mode, px, w, b, z, mean, rstd, dout, pdx, pdz, pw, pb, st);
+    });
+    if (s != SSM_OK) return PyLong_FromLong(s);
+    auto wrap = [](const at::Tensor &t) {
+        if (t.defined()) return THPVariable_Wrap(t);
+        Py_INCREF(Py_None);
+        return Py_None;
+    };
+    return Py_BuildValue("(NNNN)", wrap(dx), wrap(dz), wrap(dw), wrap(db));
+}
+
+// a C++ exception of an allocation (out of memory) becomes Python's
+template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
+PyObject *guarded(PyObject *self, PyObject *const *o, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    return F(self, o, n);
+    END_HANDLE_TH_ERRORS
+}
+
+#define ENTRY(name) {#name, (PyCFunction)(void (*)(void))guarded<name>, METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {ENTRY(delta_rule_fwd), ENTRY(delta_rule_update), ENTRY(delta_rule_bwd), ENTRY(norm_fwd),
+                         ENTRY(norm_bwd), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__native(void) { return PyModule_Create(&module); }
