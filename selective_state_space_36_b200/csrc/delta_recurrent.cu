@@ -34,6 +34,25 @@ __device__ __forceinline__ float sum8(float x) {
     return x;
 }
 
+template <int N>
+__device__ __forceinline__ void sum8(float *x) {
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+}
+
+// A lane's part of a row's dot product, as four short chains.
+template <int PIECES>
+__device__ __forceinline__ float row_dot(const float (&s)[PIECES][4], const float (&x)[PIECES][4]) {
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = fmaf(s[p][e], x[p][e], d[e]);
+    return (d[0] + d[1]) + (d[2] + d[3]);
+}
+
 // Four values of a row of n at column c; zeros behind its end.
 template <typename T, bool VEC>
 __device__ __forceinline__ void row4(const T *row, int c, int n, float *v) {
@@ -88,44 +107,6 @@ __device__ __forceinline__ void get_rows(float (&s)[kRows][PIECES][4], const flo
             }
         }
     }
-}
-
-// One token for this lane's rows: o[r] = S_t q (all eight lanes), res[r] = v - a S k.
-template <int PIECES>
-__device__ __forceinline__ void token(float (&s)[kRows][PIECES][4], const float (&kk)[PIECES][4],
-                                      const float (&qq)[PIECES][4], float decay, float beta, const float (&v)[kRows],
-                                      float (&o)[kRows], float (&res)[kRows]) {
-    float dot[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};  // four short chains
-#pragma unroll
-        for (int p = 0; p < PIECES; ++p)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[r][p][e] *= decay;
-                d[e] = fmaf(s[r][p][e], kk[p][e], d[e]);
-            }
-        dot[r] = (d[0] + d[1]) + (d[2] + d[3]);
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) dot[r] = sum8(dot[r]);
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        res[r] = v[r] - dot[r];
-        const float u = beta * res[r];
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int p = 0; p < PIECES; ++p)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[r][p][e] = fmaf(u, kk[p][e], s[r][p][e]);
-                d[e] = fmaf(s[r][p][e], qq[p][e], d[e]);
-            }
-        o[r] = (d[0] + d[1]) + (d[2] + d[3]);
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) o[r] = sum8(o[r]);
 }
 
 // One token (decode) or a few: the tokens' operands straight from global
@@ -287,7 +268,19 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
     };
 
     static_assert(kThreads % kRowsPerBlock == 0, "a thread stays in its column of v");
-    float s[kRows][PIECES][4];
+    float s[kRows][PIECES][4], kk[2][PIECES][4], qq[2][PIECES][4], vv[2][kRows];
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qq[1][p][e] = 0.f;  // there is no token before the first
+    auto put_out = [&](int64_t t, const float *o) {
+        if (STORE || sub != 0) return;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            if (row0 + 4 * r < a.headdim)
+                io_traits<T>::store(static_cast<T *>(a.out) + ((b * a.seqlen + t) * a.heads + h) * a.headdim + row0 + 4 * r,
+                                    a.scale * o[r]);
+    };
     issue(0);
     small_loads(0);
     small_stores(0);
@@ -309,8 +302,9 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
         }
         const TokenStage<T, PIECES> &st = stages[(t0 / kTok) & 1];
         const int live = (int)(a.seqlen - t0 < kTok ? a.seqlen - t0 : kTok);
-        // two tokens' operands in registers: one is loaded while the other is used
-        float kk[2][PIECES][4], qq[2][PIECES][4], vv[2][kRows];
+        // Slot t % 2 of the registers holds token t's operands.  A token's S k and the
+        // last token's S q read the same state, so their sums go through one set of
+        // shuffles.
         auto operands = [&](int t, int at) {
 #pragma unroll
             for (int p = 0; p < PIECES; ++p) {
@@ -321,23 +315,49 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
             for (int r = 0; r < kRows; ++r) vv[at][r] = io_traits<T>::load_smem(&st.v[t][mine + 4 * r]);
         };
         operands(0, 0);
+        // pairs of tokens, so that the slots are compile-time; more of them unrolled
+        // outgrow the instruction cache (16 tokens: 0.25 us each)
+#pragma unroll 1
+        for (int pair = 0; pair < live; pair += 2)
 #pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            if (t >= live) break;
-            float o[kRows], res[kRows];
-            if (t + 1 < kTok) operands(t + 1, (t + 1) & 1);
-            token<PIECES>(s, kk[t & 1], qq[t & 1], st.decay[t], st.beta[t], vv[t & 1], o, res);
+            for (int at = 0; at < 2; ++at) {
+                const int t = pair + at;
+                if (t >= live) break;
+                const float decay = st.decay[t], beta_t = st.beta[t];
+                float sums[2 * kRows];
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const int row = row0 + 4 * r;
-                if (sub != 0 || row >= a.headdim) continue;
-                const int64_t at = ((b * a.seqlen + t0 + t) * a.heads + h) * a.headdim + row;
-                if (STORE) a.r[at] = res[r];
-                else io_traits<T>::store(static_cast<T *>(a.out) + at, a.scale * o[r]);
+                for (int r = 0; r < kRows; ++r) {
+                    sums[kRows + r] = row_dot<PIECES>(s[r], qq[at ^ 1]);
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[r][p][e] *= decay;
+                    sums[r] = row_dot<PIECES>(s[r], kk[at]);
+                }
+                if (t + 1 < live) operands(t + 1, at ^ 1);
+                sum8<2 * kRows>(sums);
+                if (t0 + t > 0) put_out(t0 + t - 1, sums + kRows);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const float res = vv[at][r] - sums[r], u = beta_t * res;
+                    if (STORE && sub == 0 && row0 + 4 * r < a.headdim)
+                        a.r[((b * a.seqlen + t0 + t) * a.heads + h) * a.headdim + row0 + 4 * r] = res;
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[r][p][e] = fmaf(u, kk[at][p][e], s[r][p][e]);
+                }
             }
-        }
         small_stores(t0 + kTok);
         __syncthreads();
+    }
+    {
+        float sums[kRows];
+        const bool odd = (a.seqlen - 1) & 1;  // the last token's slot
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) sums[r] = odd ? row_dot<PIECES>(s[r], qq[1]) : row_dot<PIECES>(s[r], qq[0]);
+        sum8<kRows>(sums);
+        put_out(a.seqlen - 1, sums);
     }
     if (!a.state) return;
 #pragma unroll
