@@ -174,10 +174,14 @@ struct DeltaChunkWs {
     __nv_bfloat16 *r, *e; // (batch, heads, chunks, 2, 64, pp): r and its gradient over beta
 };
 
-// The whole forward in one kernel on the tcgen05 tensor cores: dstate 64 or
+// The forward on the tcgen05 tensor cores: dstate 64 or
 // 128, headdim a multiple of 64, 16-byte aligned tensors.
+// With few heads the sequence is split into segments that run side by side
+// (delta_fused_segments > 1: needs workspace).
 bool delta_fused_eligible(const DeltaArgs &a);
-cudaError_t launch_delta_fused(const DeltaArgs &a, cudaStream_t st);
+int delta_fused_segments(const DeltaArgs &a, int sms);
+int64_t delta_fused_workspace(const DeltaArgs &a, int nseg);  // bytes
+cudaError_t launch_delta_fused(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st);
 
 cudaError_t launch_delta_prep(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
 cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);

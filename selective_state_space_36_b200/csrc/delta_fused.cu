@@ -93,6 +93,13 @@ struct FusedArgs {
     int64_t seqlen;
     int heads, rep, headdim, dstate, vtiles;
     int vec_state;  // h0 and state start 16-byte aligned
+    // sequence split: chunks per segment, segments (1: none), the states that the
+    // segments start from (batch, heads, nseg, headdim, dstate);
+    // for the segment pass: the same for the states they end with and the
+    // propagators (batch, heads, nseg, dstate, dstate)
+    int seg_chunks, nseg;
+    const float *starts;
+    float *ends, *phi;
     unsigned int *status;
 };
 
@@ -302,7 +309,11 @@ __device__ __forceinline__ void put_state(uint32_t tl, int col, const float (&s)
     tmem_st32(tl + kTS + col, r);
 }
 
-template <int NT>
+// AGG: the segment pass of a split sequence.  No output; a CTA takes a segment's
+// rows of V (from zero, the first segment from h0) to the state it ends with, or
+// takes the rows of the unit matrix through it with V = 0: the state is linear
+// in its start, S_end = S_start Phi + (S_end from zero).
+template <int NT, bool AGG>
 __global__ void __launch_bounds__(kThreadsF, 1)
 delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                    const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapO,
@@ -312,12 +323,32 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
     // an integer would turn every shared access into a generic one
     FusedSmem<NT> &sm = *reinterpret_cast<FusedSmem<NT> *>(raw + ((0u - smem_u32(raw)) & 1023u));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t bh = blockIdx.x / a.vtiles;
-    const int v0 = (int)(blockIdx.x - bh * a.vtiles) * 128;
+    // this CTA's head, segment, rows and (AGG) kind of rows
+    int64_t bh;
+    int seg, v0;
+    bool unit_rows = false;
+    if (AGG) {
+        // per head: vtiles tiles of V for each segment but the last, one of unit rows
+        // for those of them behind the first
+        const int per = (a.nseg - 1) * a.vtiles + a.nseg - 2;
+        bh = blockIdx.x / per;
+        const int i = (int)(blockIdx.x - bh * per);
+        unit_rows = i >= (a.nseg - 1) * a.vtiles;
+        seg = unit_rows ? i - (a.nseg - 1) * a.vtiles + 1 : i / a.vtiles;
+        v0 = unit_rows ? 0 : i % a.vtiles * 128;
+    } else {
+        const int per = a.nseg * a.vtiles;
+        bh = blockIdx.x / per;
+        const int i = (int)(blockIdx.x - bh * per);
+        seg = i / a.vtiles;
+        v0 = i % a.vtiles * 128;
+    }
     const int64_t b = bh / a.heads;
     const int h = (int)(bh - b * a.heads), gr = h / a.rep;
-    const int nch = (int)((a.seqlen + kC - 1) / kC);
-    const int halves = a.headdim - v0 > 64 ? 2 : 1;  // 64-column halves of V in this CTA
+    const int all_chunks = (int)((a.seqlen + kC - 1) / kC), c0 = seg * a.seg_chunks;
+    const int nch = all_chunks - c0 < a.seg_chunks ? all_chunks - c0 : a.seg_chunks;
+    const int width = unit_rows ? a.dstate : a.headdim;
+    const int halves = width - v0 > 64 ? 2 : 1;      // 64-row halves of the state in this CTA
     const int row_warps = 4 * halves;                // whose lanes hold rows of the state
 
     if (tid == 0) {
@@ -430,11 +461,13 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             for (int k = 0; k < 8; ++k)
                 mma_bf16_ts_if(el, tm + kTS, tm + operand_col(kTY, k & 3, k >> 2), dk + (((k & 3) * 2048) >> 4), id_s, true);
             mma_commit_if(el, &sm.s[st]);
-            if (!(ok = wait(&sm.u_ready, c)) || !(ok = wait(&sm.pb[st], c >> 1))) break;
             if (c + 1 < nch && !(ok = wait(&sm.kq_read, c + 1))) break;
-            fence_after_sync();
-            r_product(dh + (kHalfTile >> 4), dl + (kHalfTile >> 4), kTO2);
-            mma_commit_if(el, &sm.o);
+            if constexpr (!AGG) {
+                if (!(ok = wait(&sm.u_ready, c)) || !(ok = wait(&sm.pb[st], c >> 1))) break;
+                fence_after_sync();
+                r_product(dh + (kHalfTile >> 4), dl + (kHalfTile >> 4), kTO2);
+                mma_commit_if(el, &sm.o);
+            }
         }
         mma_commit_if(el, &sm.fin);  // whatever was issued completes before tensor memory goes away
         (void)mbar_wait_2s(&sm.fin, 0u);
@@ -447,7 +480,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         // c + 2's V comes (two steps ahead of the first chunk)
         for (int c = -2; c < nch; ++c) {
             const int st = c & 1;
-            const int32_t t0 = (c + 2) * kC;
+            const int32_t t0 = (c0 + c + 2) * kC;
             if (c >= 0 && !(ok = wait(&sm.s[st], c >> 1))) break;
             if (c + 2 < nch && el) {
                 mbar_expect_tx(&sm.ldk[st], (uint32_t)(2 * NT) * kHalfTile);
@@ -460,16 +493,19 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             if (c + 2 < nch) {
                 if (st) ++issued[1]; else ++issued[0];
             }
-            if (c >= 0) {
+            if (unit_rows) continue;
+            if (c >= 0) {  // (AGG: the rows have read V)
                 if (!(ok = wait(&sm.o_ready[st], c >> 1))) break;
-                if (el) {
+                if constexpr (!AGG) {
+                    if (el) {
 #pragma unroll 1
-                    for (int i = 0; i < halves; ++i)
-                        tma_store_3d(&mapO, h * a.headdim + v0 + 64 * i, c * kC, (int32_t)b, sm.v[st][i]);
-                    tma_store_commit();
-                    tma_store_wait_read<0>();
+                        for (int i = 0; i < halves; ++i)
+                            tma_store_3d(&mapO, h * a.headdim + v0 + 64 * i, (c0 + c) * kC, (int32_t)b, sm.v[st][i]);
+                        tma_store_commit();
+                        tma_store_wait_read<0>();
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             if (c + 2 < nch) {
                 if (el) {
@@ -495,7 +531,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         auto fetch = [&](int c) {  // this lane's two tokens; none behind the end
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int64_t t = (int64_t)c * kC + 2 * lane + i;
+                const int64_t t = (int64_t)(c0 + c) * kC + 2 * lane + i;
                 gv[i] = t < a.seqlen ? __ldg(g + t * a.heads) : 0.f;
                 bv[i] = t < a.seqlen ? __ldg(be + t * a.heads) : 0.f;
             }
@@ -564,6 +600,12 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         const int quad = warp & 3, wg = warp >> 2, r = 32 * quad + lane;
         const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
         const int64_t row = bh * a.headdim + v0 + r;
+        const float *from = AGG ? (seg == 0 && a.h0 ? a.h0 + row * a.dstate : nullptr)
+                                : (a.nseg > 1 ? a.starts + ((bh * a.nseg + seg) * a.headdim + v0 + r) * (int64_t)a.dstate
+                                              : (a.h0 ? a.h0 + row * a.dstate : nullptr));
+        float *to = AGG ? (unit_rows ? a.phi + ((bh * a.nseg + seg) * a.dstate + r) * (int64_t)a.dstate
+                                     : a.ends + ((bh * a.nseg + seg) * a.headdim + v0 + r) * (int64_t)a.dstate)
+                        : (a.state && seg == a.nseg - 1 ? a.state + row * a.dstate : nullptr);
         const int vp = (((r & 63) >> 3) << 4) + (r & 7) * 2;  // this row's place in row 0 of the V tile
       if (32 * quad < 64 * halves) {
         // the start state, where the first chunk's "last product" would have left it
@@ -573,9 +615,9 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                 const int col = 32 * (NT * wg + p);
                 uint32_t s[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) s[i] = 0;
-                if (a.h0) {
-                    const float *src = a.h0 + row * a.dstate + col;
+                for (int i = 0; i < 32; ++i) s[i] = AGG && unit_rows && col + i == r ? __float_as_uint(1.f) : 0;
+                if (from) {
+                    const float *src = from + col;
                     if (a.vec_state) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
@@ -593,6 +635,8 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             tmem_wait_st();
         }
         uint32_t vv[16], ov[16];  // this row's values of V and of the output, packed pairs of tokens
+#pragma unroll
+        for (int i = 0; i < 16; ++i) vv[i] = 0;  // unit rows have no V
         auto load_v = [&](int c) {
             const unsigned char *vt = sm.v[c & 1][r >> 6] + 32 * wg * 128;
 #pragma unroll
@@ -611,9 +655,13 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             const int st = c & 1;
             const Dec &dec = sm.dec[st];
             if (c < nch && !(ok = wait(&sm.cum[st], c >> 1))) break;
-            if (c < nch && !(ok = wait(&sm.ldv[st], c >> 1))) break;
-            if (c < nch) load_v(c);
-            if (c > 0) {
+            if (c < nch && !unit_rows) {
+                if (!(ok = wait(&sm.ldv[st], c >> 1))) break;
+                load_v(c);
+                if constexpr (AGG) signal(&sm.o_ready[st]);
+            }
+            if (AGG && c > 0) signal(&sm.o_taken[st ^ 1]);
+            if (!AGG && c > 0) {
                 if (!(ok = wait(&sm.o, c - 1))) break;
                 fence_after_sync();
                 float o1[32], o2[32];
@@ -643,8 +691,8 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                     tmem_wait_st();
                     fence_before_sync();
                     signal(&sm.s_ready[p]);
-                } else if (a.state) {
-                    float *dst = a.state + row * a.dstate + col;
+                } else if (to) {
+                    float *dst = to + col;
                     if (a.vec_state) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
@@ -675,7 +723,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                 fence_before_sync();
                 signal(&sm.r_ready);
             }
-            if (c > 0) {  // the last chunk's output over its V
+            if (!AGG && c > 0) {  // the last chunk's output over its V
                 unsigned char *vt = sm.v[st ^ 1][r >> 6] + 32 * wg * 128;
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
@@ -708,10 +756,12 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             tmem_wait_st();
             fence_before_sync();
             signal(&sm.w_ready);
-            put_terms(tl + kTX + 32 * wg, tl + kTX + 32 * wg + 16, res);
-            tmem_wait_st();
-            fence_before_sync();
-            signal(&sm.u_ready);
+            if constexpr (!AGG) {
+                put_terms(tl + kTX + 32 * wg, tl + kTX + 32 * wg + 16, res);
+                tmem_wait_st();
+                fence_before_sync();
+                signal(&sm.u_ready);
+            }
         }
       }
     }
@@ -723,10 +773,57 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// The states that the segments start from: starts[0] = h0 (a copy: the last
+// segment may write its end over it while the first still has to start),
+// starts[1] = ends[0], then starts[i + 1] = starts[i] Phi[i] + ends[i].  A block takes kJoinRows rows of one
+// head through all segments, one thread per column.
+constexpr int kJoinRows = 4;
+
+__global__ void __launch_bounds__(128) delta_join_kernel(const float *h0, const float *ends, const float *phi,
+                                                         float *starts, int nseg, int headdim, int dstate) {
+    __shared__ float s[kJoinRows][128];
+    const int tiles = headdim / kJoinRows;
+    const int64_t bh = blockIdx.x / tiles;
+    const int p0 = (int)(blockIdx.x % tiles) * kJoinRows, n = threadIdx.x;
+    if (n < dstate)
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r)
+            starts[(bh * nseg * headdim + p0 + r) * (int64_t)dstate + n] =
+                h0 ? h0[(bh * headdim + p0 + r) * (int64_t)dstate + n] : 0.f;
+    for (int seg = 0; seg < nseg - 1; ++seg) {
+        float acc[kJoinRows];
+        const int64_t at = ((bh * nseg + seg) * headdim + p0) * (int64_t)dstate + n;
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) acc[r] = n < dstate ? ends[at + r * dstate] : 0.f;
+        if (seg > 0) {
+            const float *f = phi + (bh * nseg + seg) * (int64_t)dstate * dstate + n;
+            if (n < dstate)
+#pragma unroll 8
+                for (int m = 0; m < dstate; ++m) {
+                    const float x = __ldg(f + (int64_t)m * dstate);
+#pragma unroll
+                    for (int r = 0; r < kJoinRows; ++r) acc[r] = fmaf(s[r][m], x, acc[r]);
+                }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) {
+            s[r][n] = acc[r];
+            if (n < dstate) starts[at + (int64_t)(headdim + r) * dstate] = acc[r];
+        }
+        __syncthreads();
+    }
+}
+
+// Workspace of a split into nseg segments, floats: ends, phi, starts.
+int64_t split_floats(const DeltaArgs &a, int nseg) {
+    return a.batch * a.heads * (int64_t)nseg * a.dstate * (2 * a.headdim + a.dstate);
+}
+
 template <int NT>
-cudaError_t launch_t(const DeltaArgs &a, cudaStream_t st) {
+cudaError_t launch_t(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st) {
     CUtensorMap mq, mk, mv, mo;
-    const int64_t gn = (int64_t)a.groups * a.dstate, hp = (int64_t)a.heads * a.headdim;
+    const int64_t gn = (int64_t)a.groups * a.dstate, hp = (int64_t)a.heads * a.headdim, bh = a.batch * a.heads;
     if (!encode_btw(&mq, a.q, a.batch, a.seqlen, gn, kC) || !encode_btw(&mk, a.k, a.batch, a.seqlen, gn, kC) ||
         !encode_btw(&mv, a.v, a.batch, a.seqlen, hp, kC) || !encode_btw(&mo, a.out, a.batch, a.seqlen, hp, kC))
         return cudaErrorInvalidValue;
@@ -735,12 +832,31 @@ cudaError_t launch_t(const DeltaArgs &a, cudaStream_t st) {
     f.seqlen = a.seqlen; f.heads = a.heads; f.rep = a.heads / a.groups; f.headdim = a.headdim; f.dstate = a.dstate;
     f.vtiles = (a.headdim + 127) / 128;
     f.vec_state = aligned16(a.h0) && aligned16(a.state);
+    const int chunks = (int)((a.seqlen + kC - 1) / kC);
+    f.seg_chunks = (chunks + nseg - 1) / nseg;
+    f.nseg = nseg;
     cudaError_t e = device_status_address(&f.status);
     if (e != cudaSuccess) return e;
     constexpr int bytes = (int)sizeof(FusedSmem<NT>) + 1024;
-    e = allow_smem<delta_fused_kernel<NT>, bytes>();
+    if (nseg > 1) {
+        f.ends = ws;
+        f.phi = f.ends + bh * nseg * a.headdim * a.dstate;
+        float *starts = f.phi + bh * nseg * a.dstate * (int64_t)a.dstate;
+        f.starts = starts;
+        e = allow_smem<delta_fused_kernel<NT, true>, bytes>();
+        if (e != cudaSuccess) return e;
+        const int64_t blocks = bh * ((nseg - 1) * f.vtiles + nseg - 2);
+        delta_fused_kernel<NT, true><<<(unsigned)blocks, kThreadsF, bytes, st>>>(mq, mk, mv, mo, f);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        delta_join_kernel<<<(unsigned)(bh * (a.headdim / kJoinRows)), 128, 0, st>>>(a.h0, f.ends, f.phi, starts, nseg, a.headdim,
+                                                                                  a.dstate);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    e = allow_smem<delta_fused_kernel<NT, false>, bytes>();
     if (e != cudaSuccess) return e;
-    delta_fused_kernel<NT><<<(unsigned)(a.batch * a.heads * f.vtiles), kThreadsF, bytes, st>>>(mq, mk, mv, mo, f);
+    delta_fused_kernel<NT, false><<<(unsigned)(bh * nseg * f.vtiles), kThreadsF, bytes, st>>>(mq, mk, mv, mo, f);
     return cudaGetLastError();
 }
 
@@ -754,8 +870,37 @@ bool delta_fused_eligible(const DeltaArgs &a) {
            aligned16(a.k) && aligned16(a.v) && aligned16(a.out) && encode_tiled_fn() != nullptr;
 }
 
-cudaError_t launch_delta_fused(const DeltaArgs &a, cudaStream_t st) {
-    return a.dstate == 64 ? delta::launch_t<1>(a, st) : delta::launch_t<2>(a, st);
+// Segments of the sequence.  A CTA walks over its chunks one after the other
+// (about 4 us each), so the time is that of the longest row of chunks: with few
+// heads, most SMs idle.  A split runs the chunks twice (the segment pass has the
+// unit rows besides) but side by side.  The count with the least estimated time,
+// in chunks: waves of CTAs times chunks per segment for both passes, and 3 per
+// segment for the join and the launches; one segment unless a split saves a
+// fifth.  Measured, 16 heads of 64 x 128, 32768 tokens: see delta_fused.cu's
+// head for one segment and the split.
+int delta_fused_segments(const DeltaArgs &a, int sms) {
+    const int64_t chunks = (a.seqlen + delta::kC - 1) / delta::kC, tiles = (a.headdim + 127) / 128;
+    const int64_t units = a.batch * a.heads * tiles;
+    if (units * 2 > sms || chunks < 16) return 1;
+    auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
+    int64_t best = chunks * 4 / 5;
+    int nseg = 1;
+    for (int n = 3; n <= 64 && n * 4 <= chunks; ++n) {
+        const int64_t seg = (chunks + n - 1) / n;
+        if ((chunks + seg - 1) / seg != n) continue;  // no empty segment
+        const int64_t cost = (waves(a.batch * a.heads * ((n - 1) * tiles + n - 2)) + waves(units * n)) * seg + 3 * n;
+        if (cost < best) {
+            best = cost;
+            nseg = n;
+        }
+    }
+    return nseg;
+}
+
+int64_t delta_fused_workspace(const DeltaArgs &a, int nseg) { return nseg > 1 ? 4 * delta::split_floats(a, nseg) : 0; }
+
+cudaError_t launch_delta_fused(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st) {
+    return a.dstate == 64 ? delta::launch_t<1>(a, nseg, ws, st) : delta::launch_t<2>(a, nseg, ws, st);
 }
 
 }  // namespace ssm

@@ -6,7 +6,6 @@
 #include <atomic>
 #include <mutex>
 #include <stdio.h>
-#include <stdlib.h>
 #include <string.h>
 
 #include "../../include/ssm.h"
@@ -929,9 +928,18 @@ ssm_status delta_forward(ssm_ssd_dims dims, ssm_dtype io, const void *q, const v
         if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
         return SSM_OK;
     }
-    if (ssm::delta_fused_eligible(a) && !getenv("NOFUSED")) {
-        cudaError_t e = ssm::launch_delta_fused(a, st);
+    if (ssm::delta_fused_eligible(a)) {
+        const int nseg = ssm::delta_fused_segments(a, device_sms());
+        const int64_t bytes = ssm::delta_fused_workspace(a, nseg);
+        void *mem = nullptr;
+        if (bytes > 0) {
+            cudaError_t e = workspace_alloc(&mem, (size_t)bytes, st);
+            if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
+        }
+        cudaError_t e = ssm::launch_delta_fused(a, nseg, static_cast<float *>(mem), st);
+        cudaError_t ef = mem ? cudaFreeAsync(mem, st) : cudaSuccess;
         if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
+        if (ef != cudaSuccess) return cuda_fail(ef, "workspace release");
         return SSM_OK;
     }
     const int64_t units = dims.batch * dims.heads * ((dims.seqlen + ssm::delta::kC - 1) / ssm::delta::kC);

@@ -74,6 +74,9 @@ SHAPES = [
     (1, 150, 2, 2, 200, 128, "bf16", "mixed", True),
     (1, 193, 2, 1, 130, 100, "f32", "mixed", True),
     (2, 640, 2, 1, 64, 128, "bf16", "slow", True),
+    (1, 2577, 2, 1, 64, 128, "bf16", "mixed", True),   # few heads: the sequence is split into segments
+    (1, 2560, 1, 1, 128, 64, "bf16", "slow", False),
+    (2, 1100, 1, 1, 192, 128, "bf16", "slow", True),
 ]
 
 
