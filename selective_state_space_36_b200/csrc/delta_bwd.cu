@@ -2,21 +2,23 @@
 //
 // With dS1 the gradient of the state leaving a chunk (notation of
 // delta_chunk.cuh, gam = exp G, w = exp(G_C - G)):
-//   dU  = P^T dO + w K dS1^T,   e = dU - N^T (beta dU),   dV = beta e
-//   dS0 = gam_C dS1 + (scale gam dO)^T Q - (gam beta e)^T K
+//   z   = Pb^T dO + w beta K dS1^T,   dV = z - M^T z
+//   dS0 = gam_C dS1 + (scale gam dO)^T Q - (gam dV)^T K
 // runs backwards over the chunks (delta_reverse_kernel, the mirror image of
 // delta_chain.cu: one warp per 16 state rows, everything transposed).  It needs
-// no state; it leaves dS1 and e of each chunk in the workspace.  Then, for all
+// no state; it leaves dS1 and dV of each chunk in the workspace.  Then, for all
 // chunks at once (delta_grad_kernel), with S0 and r from the forward's
-// recomputation:
-//   X  = scale lower(Gam o (dO u^T)),  E = -strict_lower(Gam o (beta e) u^T)
+// recomputation and x = scale lower(Gam o (dO r^T)), y = -strict_lower(Gam o (dV r^T)),
+// X = x beta, E = y beta (columns scaled):
 //   dQ = scale gam dO S0 + X K
-//   dK = L + R,  L = E K - gam beta e S0,  R = X^T Q + E^T K + w u dS1
-//   dbeta_t = e_t . r_t
+//   dK = L + R,  L = E K - gam dV S0,  R = X^T Q + E^T K + w beta r dS1
+//   dbeta_s = sum_t x_ts q_t . k_s + sum_t y_ts k_t . k_s + w_s (r dS1)_s . k_s
+// (beta enters R alone, as a factor of its row s: dbeta_s = k_s . R_s / beta_s,
+// without the division),
 //   dG_t = q_t . dq_t + k_t . (L_t - R_t),  dG_C += <S1, dS1>
 //   dg_t = sum of dG over the chunk's tokens from t on
 // dG needs no difference of large sums: its terms are row products that exist
-// anyway, and <S1, dS1> = gam_C <S0, dS1> + sum_t k_t . (w u dS1)_t.
+// anyway, and <S1, dS1> = gam_C <S0, dS1> + sum_t w beta (r dS1)_t . k_t.
 #include "delta_chunk.cuh"
 #include "kernel_setup.cuh"
 
@@ -96,12 +98,12 @@ __global__ void __launch_bounds__(256) delta_reverse_kernel(DeltaBwdArgs p, Delt
         bf16 *sk = reinterpret_cast<bf16 *>(st), *sq = sk + kC * ldk, *so = sq + kC * ldk, *sm = so + kC * ldv;
         const float *gam = reinterpret_cast<const float *>(sm + kMats * kC * kMatLd), *wend = gam + kC,
                     *beta = wend + kC;
-        const bf16 *sn = sm, *sp = sm + 2 * kC * kMatLd;
-        constexpr int kLow = kC * kMatLd;
+        const bf16 *sn = sm, *sp = sm + kC * kMatLd;
+        constexpr int kLow = 2 * kC * kMatLd;
         bf16 *mine = so + 16 * warp;  // this warp's columns of dO, later of its results
 
         store_state<NP>(ws.ds1 + unit * 2 * pp * NP, pp, s, v0 + 16 * warp, lane);
-        // x = dU^T = w (dS K^T) + dO^T P
+        // x = z^T = w beta (dS K^T) + dO^T Pb
         float x[kC / 8][4];
 #pragma unroll
         for (int j = 0; j < kC / 8; ++j)
@@ -126,7 +128,9 @@ __global__ void __launch_bounds__(256) delta_reverse_kernel(DeltaBwdArgs p, Delt
 #pragma unroll
         for (int j = 0; j < kC / 8; ++j) {
             const float2 w2 = *reinterpret_cast<const float2 *>(wend + 8 * j + 2 * (lane & 3));
-            x[j][0] *= w2.x; x[j][1] *= w2.y; x[j][2] *= w2.x; x[j][3] *= w2.y;
+            const float2 b2 = *reinterpret_cast<const float2 *>(beta + 8 * j + 2 * (lane & 3));
+            const float f0 = w2.x * b2.x, f1 = w2.y * b2.y;
+            x[j][0] *= f0; x[j][1] *= f1; x[j][2] *= f0; x[j][3] *= f1;
         }
         uint32_t dof[kC / 16][4];
 #pragma unroll
@@ -143,16 +147,15 @@ __global__ void __launch_bounds__(256) delta_reverse_kernel(DeltaBwdArgs p, Delt
                 mma(x[2 * jj + 1], dof[kk], fl[2], fl[3]);
             }
         }
-        // e^T = x - (beta x) N, in place: blocks of 16 tokens from the first (N is
-        // strictly lower: a block changes itself and those before it)
+        // dV^T = x - x M, in place: blocks of 16 tokens from the first (M is strictly
+        // lower: a block changes itself and those before it)
 #pragma unroll
         for (int kk = 0; kk < kC / 16; ++kk) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int j = 2 * kk + (q >> 1);
-                const float2 b2 = *reinterpret_cast<const float2 *>(beta + 8 * j + 2 * (lane & 3));
-                split(-b2.x * x[j][2 * (q & 1)], -b2.y * x[j][2 * (q & 1) + 1], hi[q], lo[q]);
+                split(-x[j][2 * (q & 1)], -x[j][2 * (q & 1) + 1], hi[q], lo[q]);
             }
 #pragma unroll
             for (int jj = 0; jj <= kk; ++jj) {
@@ -167,18 +170,15 @@ __global__ void __launch_bounds__(256) delta_reverse_kernel(DeltaBwdArgs p, Delt
                 mma(x[2 * jj + 1], hi, fl[2], fl[3]);
             }
         }
-        // e to the workspace, dV = beta e to memory
+        // dV to the workspace and to memory
         __syncwarp();
-        store_rows(ws.e + unit * 2 * kC * pp, pp, x, mine, ldv, v0 + 16 * warp, lane);
+        store_rows(ws.dv + unit * 2 * kC * pp, pp, x, mine, ldv, v0 + 16 * warp, lane);
 #pragma unroll
         for (int jj = 0; jj < kC / 16; ++jj) {
             uint32_t f[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int j = 2 * jj + (q >> 1);
-                const float2 b2 = *reinterpret_cast<const float2 *>(beta + 8 * j + 2 * (lane & 3));
-                x[j][2 * (q & 1)] *= b2.x;
-                x[j][2 * (q & 1) + 1] *= b2.y;
                 f[q] = pack(x[j][2 * (q & 1)], x[j][2 * (q & 1) + 1]);
             }
             stm4t(mine + (16 * jj + cf_row) * ldv + cf_col, f[0], f[1], f[2], f[3]);
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(256) delta_reverse_kernel(DeltaBwdArgs p, Delt
                 if (t < live && c < have) dst[t * v_ld + c] = mine[t * ldv + c];
             }
         }
-        // dS0 = gam_C dS1 + (scale gam dO)^T Q - (gam beta e)^T K
+        // dS0 = gam_C dS1 + (scale gam dO)^T Q - (gam dV)^T K
         const float whole = gam[kC - 1];
 #pragma unroll
         for (int j = 0; j < NP / 8; ++j)
@@ -266,8 +266,8 @@ struct GradSmem {  // headdim rounded up to 16 (pp) decides the sizes of the res
     bf16 x[2][kC][kMatLd], e[2][kC][kMatLd];  // X and E, high and low terms
     double cum[kC];
     float dec[kDec][kC];
-    float dg[2][kC];                          // row sums of the two halves of dstate
-    float dbeta[kC];
+    float dg[2][kC], kr[2][kC];               // row sums of the two halves of dstate: dG, k . (r dS1)
+    float db[4][kC];                          // column sums of the four row blocks: dbeta's first terms
     float part[kGradThreads / 32];
 };
 template <int NP>
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(DeltaBwdArgs p
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tb = warp & 3, half = warp >> 2;
     const int pp = (a.headdim + 15) / 16 * 16, ldp = pp + 8, lds = NP + 8;
     bf16 *so = reinterpret_cast<bf16 *>(raw + sizeof(GradSmem<NP>));  // dO
-    bf16 *sr = so + kC * ldp, *se = sr + 2 * kC * ldp;               // r, e: high and low terms
+    bf16 *sr = so + kC * ldp, *se = sr + 2 * kC * ldp;               // r, dV: high and low terms
     bf16 *ss = se + 2 * kC * ldp;                                    // S0, then dS1: high and low terms
     const int64_t nch = (a.seqlen + kC - 1) / kC;
     const int64_t bg = blockIdx.x / nch, ch = blockIdx.x - bg * nch;
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(DeltaBwdArgs p
         load_tile<VECV>(so, ldp, static_cast<const bf16 *>(p.dout) + ((b * a.seqlen + t0) * a.heads + h) * a.headdim,
                         v_ld, kC, pp, live, a.headdim, tid, kGradThreads);
         load_tile<true>(sr, ldp, ws.r + unit * 2 * kC * pp, pp, 2 * kC, pp, 2 * kC, pp, tid, kGradThreads);
-        load_tile<true>(se, ldp, ws.e + unit * 2 * kC * pp, pp, 2 * kC, pp, 2 * kC, pp, tid, kGradThreads);
+        load_tile<true>(se, ldp, ws.dv + unit * 2 * kC * pp, pp, 2 * kC, pp, 2 * kC, pp, tid, kGradThreads);
         cp_async_commit();
         load_tile<true>(ss, lds, ws.s0 + unit * 2 * pp * NP, NP, 2 * pp, NP, 2 * pp, NP, tid, kGradThreads);
         cp_async_commit();
@@ -337,14 +337,15 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(DeltaBwdArgs p
         }
         cp_async_wait<1>();
         __syncthreads();
-        // X = scale Gam beta_s (dO_t . r_s), E = -Gam beta_t beta_s (e_t . r_s): this
-        // warp's 16 rows and its half of the columns, blocks up to the diagonal
+        // x = scale Gam (dO_t . r_s), y = -Gam (dV_t . r_s): this warp's 16 rows and
+        // its half of the columns, blocks up to the diagonal; q_t . k_s and k_t . k_s
+        // beside them for dbeta
         {
-            float cx[4][4], ce[4][4];
+            float cx[4][4], ce[4][4], cqk[4][4], ckk[4][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) cx[j][i] = ce[j][i] = 0.f;
+                for (int i = 0; i < 4; ++i) cx[j][i] = ce[j][i] = cqk[j][i] = ckk[j][i] = 0.f;
             if (2 * half <= tb)
                 for (int kk = 0; kk < pp / 16; ++kk) {
                     uint32_t ao[4], ah[4], al[4];
@@ -369,33 +370,62 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(DeltaBwdArgs p
                         }
                     }
                 }
+            if (2 * half <= tb)
+#pragma unroll 2
+                for (int kk = 0; kk < NP / 16; ++kk) {
+                    uint32_t aq[4], ak[4];
+                    ldm4(aq, &sm.q[16 * tb + rf_row][16 * kk + rf_col]);
+                    ldm4(ak, &sm.k[16 * tb + rf_row][16 * kk + rf_col]);
+#pragma unroll
+                    for (int jj = 0; jj < 2; ++jj) {
+                        if (2 * half + jj > tb) continue;
+                        uint32_t f[4];
+                        ldm4(f, &sm.k[16 * (2 * half + jj) + cf_row][16 * kk + cf_col]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            mma(cqk[2 * jj + i], aq, f[2 * i], f[2 * i + 1]);
+                            mma(ckk[2 * jj + i], ak, f[2 * i], f[2 * i + 1]);
+                        }
+                    }
+                }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (2 * half + (j >> 1) > tb) continue;
+                const int s = 32 * half + 8 * j + 2 * (lane & 3);
+                float cols[2] = {0.f, 0.f};
+                if (2 * half + (j >> 1) <= tb) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int t = ta + 8 * i, s = 32 * half + 8 * j + 2 * (lane & 3);
-                    float xv[2], ev[2];
+                    for (int i = 0; i < 2; ++i) {
+                        const int t = ta + 8 * i;
+                        float xv[2], ev[2];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float gam = s + c <= t ? expf((float)(sm.cum[t] - sm.cum[s + c])) * sm.dec[2][s + c] : 0.f;
-                        xv[c] = s + c <= t ? a.scale * gam * cx[j][2 * i + c] : 0.f;
-                        ev[c] = s + c < t ? -gam * sm.dec[2][t] * ce[j][2 * i + c] : 0.f;
-                        if (s + c == t) sm.dbeta[t] = ce[j][2 * i + c];
+                        for (int c = 0; c < 2; ++c) {
+                            const float gam = s + c <= t ? expf((float)(sm.cum[t] - sm.cum[s + c])) : 0.f;
+                            const float x = s + c <= t ? a.scale * gam * cx[j][2 * i + c] : 0.f;
+                            const float y = s + c < t ? -gam * ce[j][2 * i + c] : 0.f;
+                            if (s + c <= t) cols[c] += x * cqk[j][2 * i + c] + y * ckk[j][2 * i + c];
+                            xv[c] = x * sm.dec[2][s + c];
+                            ev[c] = y * sm.dec[2][s + c];
+                        }
+                        uint32_t hi, lo;
+                        split(xv[0], xv[1], hi, lo);
+                        *reinterpret_cast<uint32_t *>(&sm.x[0][t][s]) = hi;
+                        *reinterpret_cast<uint32_t *>(&sm.x[1][t][s]) = lo;
+                        split(ev[0], ev[1], hi, lo);
+                        *reinterpret_cast<uint32_t *>(&sm.e[0][t][s]) = hi;
+                        *reinterpret_cast<uint32_t *>(&sm.e[1][t][s]) = lo;
                     }
-                    uint32_t hi, lo;
-                    split(xv[0], xv[1], hi, lo);
-                    *reinterpret_cast<uint32_t *>(&sm.x[0][t][s]) = hi;
-                    *reinterpret_cast<uint32_t *>(&sm.x[1][t][s]) = lo;
-                    split(ev[0], ev[1], hi, lo);
-                    *reinterpret_cast<uint32_t *>(&sm.e[0][t][s]) = hi;
-                    *reinterpret_cast<uint32_t *>(&sm.e[1][t][s]) = lo;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) cols[c] += __shfl_xor_sync(0xffffffffu, cols[c], o);
+                    if (lane < 4) sm.db[tb][s + c] = cols[c];
                 }
             }
         }
         cp_async_wait<0>();
         __syncthreads();
-        // q = scale gam dO S0 + X K,  l = E K - gam beta e S0
+        // q = scale gam dO S0 + X K,  l = E K - gam dV S0
         float cq[NT][4], cl[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -425,7 +455,7 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(DeltaBwdArgs p
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float g = sm.dec[0][ta + 8 * i], fq = a.scale * g, fl = -g * sm.dec[2][ta + 8 * i];
+            const float g = sm.dec[0][ta + 8 * i], fq = a.scale * g, fl = -g;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 cq[j][2 * i] *= fq; cq[j][2 * i + 1] *= fq;
@@ -521,14 +551,19 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(DeltaBwdArgs p
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float f = sm.dec[1][ta + 8 * i] * sm.dec[2][ta + 8 * i];
+            float kr = 0.f;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const int n = n0 + 8 * j + 2 * (lane & 3);
                 const uint32_t kv = *reinterpret_cast<const uint32_t *>(&sm.k[ta + 8 * i][n]);
+                kr += low_of(kv) * cr[j][2 * i] + high_of(kv) * cr[j][2 * i + 1];
                 cr[j][2 * i] *= f;
                 cr[j][2 * i + 1] *= f;
-                inner += low_of(kv) * cr[j][2 * i] + high_of(kv) * cr[j][2 * i + 1];
             }
+            inner = fmaf(f, kr, inner);
+            kr += __shfl_xor_sync(0xffffffffu, kr, 1);
+            kr += __shfl_xor_sync(0xffffffffu, kr, 2);
+            if ((lane & 3) == 0) sm.kr[half][ta + 8 * i] = kr;
         }
         for (int kk = tb; kk < kC / 16; ++kk) {
             uint32_t xh[4], xl[4], eh[4], el[4];
@@ -587,8 +622,12 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(DeltaBwdArgs p
             const int64_t at = (b * a.seqlen + t0) * a.heads + h;
             if (t < live) p.dg[at + (int64_t)t * a.heads] = whole + (sum - d0);
             if (t - 1 < live) p.dg[at + (int64_t)(t - 1) * a.heads] = whole + sum;
-            if (t < live) p.dbeta[at + (int64_t)t * a.heads] = sm.dbeta[t];
-            if (t - 1 < live) p.dbeta[at + (int64_t)(t - 1) * a.heads] = sm.dbeta[t - 1];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int s = t - i;
+                const float db = (sm.db[0][s] + sm.db[1][s]) + (sm.db[2][s] + sm.db[3][s]);
+                if (s < live) p.dbeta[at + (int64_t)s * a.heads] = db + sm.dec[1][s] * (sm.kr[0][s] + sm.kr[1][s]);
+            }
         }
     }
     bf16 *dq = static_cast<bf16 *>(p.dq) + qk0, *dk = static_cast<bf16 *>(p.dk) + qk0;

@@ -1,16 +1,16 @@
 // delta_chain.cu -- the chunked gated delta rule's pass over the chunks of a
 // sequence, after delta_prep.cu.
 //
-// The columns of V (rows of the state) are independent given K, Q, N and P,
+// The columns of V (rows of the state) are independent given K, Q, M and Pb,
 // so one warp owns 16 of them for the whole sequence and keeps its slice of
 // the state, 16 x dstate, in the accumulator registers of the matrix
 // instructions.  Everything is computed transposed (state rows as the
 // instruction's rows), so that an accumulator is, without any exchange, the
 // left operand of the next product:
-//   X^T = S K^T -> r^T = (V^T - X^T gam)(I - N beta)^T -> S += (r beta w)^T K,
-//   O^T = S Q^T gam scale + (r beta)^T P^T.
+//   X^T = S K^T -> r^T = (V^T - X^T gam)(I - M)^T -> S += (r beta w)^T K,
+//   O^T = S Q^T gam scale + r^T Pb^T.
 // No block-wide exchange exists in a chunk; the block shares only the tiles of
-// K, Q, V, N and P, which cp.async brings one chunk ahead (two stages).
+// K, Q, V, M and Pb, which cp.async brings one chunk ahead (two stages).
 // Products of the state or of r take two bf16 terms of each (delta_chunk.cuh).
 #include "delta_chunk.cuh"
 #include "kernel_setup.cuh"
@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
         bf16 *sk = reinterpret_cast<bf16 *>(st), *sq = sk + kC * ldk, *sv = sq + kC * ldk, *sm = sv + kC * ldv;
         const float *gam = reinterpret_cast<const float *>(sm + kMats * kC * kMatLd), *wend = gam + kC,
                     *beta = wend + kC;
-        const bf16 *sn = sm, *sp = sm + 2 * kC * kMatLd;
-        constexpr int kLow = kC * kMatLd;  // from a high term's tile to the low term's
+        const bf16 *sn = sm, *sp = sm + kC * kMatLd;
+        constexpr int kLow = 2 * kC * kMatLd;  // from a high term's tile to the low term's
         bf16 *mine = sv + 16 * warp;       // this warp's columns of V, later of the output
 
         if constexpr (STORE) store_state<NP>(ws.s0 + (bh * nch + ch) * 2 * pp * NP, pp, s, v0 + 16 * warp, lane);
@@ -139,16 +139,15 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
                 o[j][3] *= a.scale * g2.y;
             }
         }
-        // r^T = x - (beta x) N^T, in place: blocks of 16 tokens from the last, whose
-        // own values no earlier step has changed yet (N is strictly lower)
+        // r^T = x - x M^T, in place: blocks of 16 tokens from the last, whose own
+        // values no earlier step has changed yet (M is strictly lower)
 #pragma unroll
         for (int kk = kC / 16 - 1; kk >= 0; --kk) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int j = 2 * kk + (i >> 1);
-                const float2 b2 = *reinterpret_cast<const float2 *>(beta + 8 * j + 2 * (lane & 3));
-                split(-b2.x * x[j][2 * (i & 1)], -b2.y * x[j][2 * (i & 1) + 1], hi[i], lo[i]);
+                split(-x[j][2 * (i & 1)], -x[j][2 * (i & 1) + 1], hi[i], lo[i]);
             }
 #pragma unroll
             for (int jj = kk; jj < kC / 16; ++jj) {
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
         if constexpr (STORE) {
             store_rows(ws.r + (bh * nch + ch) * 2 * kC * pp, pp, x, mine, ldv, v0 + 16 * warp, lane);
         }
-        // O^T += u^T P^T;  S = exp(G_C) S + (u w)^T K
+        // O^T += r^T Pb^T;  S = exp(G_C) S + (r beta w)^T K
         const float whole = gam[kC - 1];
 #pragma unroll
         for (int j = 0; j < NP / 8; ++j)
@@ -180,9 +179,9 @@ __global__ void __launch_bounds__(256) delta_chain_kernel(DeltaArgs a, DeltaChun
                 const int j = 2 * kk + (i >> 1);
                 const float2 b2 = *reinterpret_cast<const float2 *>(beta + 8 * j + 2 * (lane & 3));
                 const float2 w2 = *reinterpret_cast<const float2 *>(wend + 8 * j + 2 * (lane & 3));
-                const float u0 = b2.x * x[j][2 * (i & 1)], u1 = b2.y * x[j][2 * (i & 1) + 1];
-                split(u0, u1, hi[i], lo[i]);
-                split(w2.x * u0, w2.y * u1, whi[i], wlo[i]);
+                const float r0 = x[j][2 * (i & 1)], r1 = x[j][2 * (i & 1) + 1];
+                split(r0, r1, hi[i], lo[i]);
+                split(w2.x * b2.x * r0, w2.y * b2.y * r1, whi[i], wlo[i]);
             }
 #pragma unroll
             for (int jj = kk; jj < kC / 16; ++jj) {

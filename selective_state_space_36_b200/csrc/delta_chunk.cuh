@@ -5,12 +5,11 @@
 // Chunks of C = 64 tokens.  With G_t the sum of the log decays of the chunk's
 // tokens up to t and Gam_ts = exp(G_t - G_s) for s <= t, the definition's
 // recurrence inside a chunk that starts from the state S0 is
-//   r = (I - N diag(beta)) (V - diag(exp G) K S0^T),    u = beta r
-//   O = scale diag(exp G) Q S0^T + P u,                 P = scale lower(Gam o Q K^T)
-//   S1 = exp(G_C) S0 + u^T diag(exp(G_C - G)) K
-// where N solves N = Abar - Abar diag(beta) N, Abar = strict_lower(Gam o K K^T)
-// (so that I - N diag(beta) is the inverse of I + Abar diag(beta); N itself
-// has no division by beta, which may be zero).
+//   r = (I - M) (V - diag(exp G) K S0^T)
+//   O = scale diag(exp G) Q S0^T + Pb r,    Pb = scale lower(Gam o Q K^T) diag(beta)
+//   S1 = exp(G_C) S0 + (beta r)^T diag(exp(G_C - G)) K
+// where I - M is the inverse of I + L, L = strict_lower(Gam o K K^T) diag(beta).
+// Nothing is divided by beta, which may be zero.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,7 +24,7 @@ namespace delta {
 
 constexpr int kC = 64;        // tokens per chunk
 constexpr int kMatLd = 72;    // row stride of a 64 x 64 bf16 tile in shared memory (conflict-free ldmatrix)
-constexpr int kMats = 4;      // per chunk and head: N high, N low, P high, P low, each 64 x 64
+constexpr int kMats = 4;      // per chunk and head: M, Pb (high terms), M, Pb (low terms), each 64 x 64
 constexpr int kDec = 3;       // per chunk and head: exp(G_t), exp(G_C - G_t), beta_t (zero behind the end)
 
 typedef __nv_bfloat16 bf16;
@@ -171,7 +170,7 @@ struct DeltaChunkWs {
     // backward only; headdim rounded up to 16 (pp), dstate to 64 or 128 (np)
     __nv_bfloat16 *s0;    // (batch, heads, chunks, 2, pp, np): the state entering each chunk
     __nv_bfloat16 *ds1;   // the same: the gradient of the state leaving it
-    __nv_bfloat16 *r, *e; // (batch, heads, chunks, 2, 64, pp): r and its gradient over beta
+    __nv_bfloat16 *r, *dv; // (batch, heads, chunks, 2, 64, pp): r, the gradient of V
 };
 
 // The forward on the tcgen05 tensor cores: dstate 64 or

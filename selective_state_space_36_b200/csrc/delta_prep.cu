@@ -1,5 +1,5 @@
 // delta_prep.cu -- what the chunked gated delta rule needs of each chunk before
-// any state enters: the triangular matrices N and P (see delta_chunk.cuh) as
+// any state enters: the triangular matrices M and Pb (see delta_chunk.cuh) as
 // two bf16 terms each, and the decays.
 //
 // One block per (batch row, head, chunk): K K^T and Q K^T (64 x 64, exact bf16
@@ -7,9 +7,8 @@
 // blocks on and below the diagonal; the decays between tokens from sums in
 // float64, because a difference of two float32 sums of a strong decay loses
 // the digits of the small difference; then one thread per column solves
-// N = Abar - Abar diag(beta) N downwards in float32, 16 rows at a time: the
-// rows above enter as a product with broadcast reads, the 16 x 16 block on
-// the diagonal is unrolled.
+// M = L - L M downwards in float32, 16 rows at a time: the rows above enter as a
+// product with broadcast reads, the 16 x 16 block on the diagonal is unrolled.
 #include "delta_chunk.cuh"
 #include "kernel_setup.cuh"
 
@@ -18,13 +17,13 @@ namespace delta {
 namespace {
 
 constexpr int kPrepThreads = 128;
-constexpr int kAtLd = kC + 4;  // row stride of the transposed Abar: 16-byte rows, conflict-free column reads
+constexpr int kAtLd = kC + 4;  // row stride of the transposed L: 16-byte rows, conflict-free column reads
 
 template <int NP>
 struct PrepSmem {
     bf16 k[kC][NP + 8], q[kC][NP + 8];
-    float at[kC][kAtLd];  // at[s][t] = Abar[t][s]
-    float xs[kC][kC];     // xs[t][j] = beta_t N[t][j]
+    float at[kC][kAtLd];  // at[s][t] = L[t][s]
+    float xs[kC][kC];     // xs[t][j] = M[t][j]
     double cum[kC];
     float beta[kC];
 };
@@ -104,13 +103,13 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(DeltaArgs a, D
             float p[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float gam = s + e <= t ? expf((float)(sm.cum[t] - sm.cum[s + e])) : 0.f;
+                const float gam = s + e <= t ? expf((float)(sm.cum[t] - sm.cum[s + e])) * sm.beta[s + e] : 0.f;
                 p[e] = s + e <= t ? a.scale * gam * cq[j][2 * half + e] : 0.f;
                 sm.at[s + e][t] = s + e < t ? gam * ck[j][2 * half + e] : 0.f;
             }
             uint32_t hi, lo;
             split(p[0], p[1], hi, lo);
-            *reinterpret_cast<uint32_t *>(mats + 2 * kC * kC + t * kC + s) = hi;
+            *reinterpret_cast<uint32_t *>(mats + kC * kC + t * kC + s) = hi;
             *reinterpret_cast<uint32_t *>(mats + 3 * kC * kC + t * kC + s) = lo;
         }
     }
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(DeltaArgs a, D
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float x = sm.beta[t0b + i] * acc[i];
+                const float x = acc[i];
                 sm.xs[t0b + i][j] = x;
 #pragma unroll
                 for (int i2 = i + 1; i2 < 16; ++i2) acc[i2] = fmaf(-sm.at[t0b + i][t0b + i2], x, acc[i2]);
@@ -156,7 +155,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(DeltaArgs a, D
         for (int i = 0; i < 16; ++i) {
             const bf16 hi = __float2bfloat16_rn(acc[i]);
             mats[(t0b + i) * kC + j] = hi;
-            mats[kC * kC + (t0b + i) * kC + j] = __float2bfloat16_rn(acc[i] - __bfloat162float(hi));
+            mats[2 * kC * kC + (t0b + i) * kC + j] = __float2bfloat16_rn(acc[i] - __bfloat162float(hi));
         }
     }
 }

@@ -889,7 +889,7 @@ ssm::DeltaArgs delta_args(const ssm_ssd_dims &d, const void *q, const void *k, c
 }
 
 // Workspace of `units` chunks; pp, np > 0: with what the backward pass keeps of
-// each (states of pp x np, r and e of 64 x pp, two bf16 terms each).
+// each (states of pp x np, r and dV of 64 x pp, two bf16 terms each).
 cudaError_t delta_chunk_workspace(int64_t units, int64_t pp, int64_t np, void **mem, ssm::DeltaChunkWs *ws,
                                   cudaStream_t st) {
     constexpr int64_t c = ssm::delta::kC;
@@ -901,7 +901,7 @@ cudaError_t delta_chunk_workspace(int64_t units, int64_t pp, int64_t np, void **
     ws->s0 = at; at += units * state;
     ws->ds1 = at; at += units * state;
     ws->r = at; at += units * rows;
-    ws->e = at; at += units * rows;
+    ws->dv = at; at += units * rows;
     ws->dec = reinterpret_cast<float *>(at);
     return cudaSuccess;
 }
