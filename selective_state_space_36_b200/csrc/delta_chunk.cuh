@@ -181,6 +181,9 @@ bool delta_fused_eligible(const DeltaArgs &a);
 int delta_fused_segments(const DeltaArgs &a, int sms);
 int64_t delta_fused_workspace(const DeltaArgs &a, int nseg);  // bytes
 cudaError_t launch_delta_fused(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st);
+// The gradient's first half on the same kernel (out is not read): everything of
+// the workspace but ds1 and dv.
+cudaError_t launch_delta_fused_store(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
 
 cudaError_t launch_delta_prep(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
 cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);

@@ -30,11 +30,11 @@
 // decays.  They meet at mbarriers only; every wait is bounded and reports
 // through the device status word.
 #include "delta_chunk.cuh"
+#include "delta_tc.cuh"
 #include "kernel_setup.cuh"
 #include "scan_kernels.cuh"
 #include "ssm_device.cuh"
 #include "tma_maps.cuh"
-#include "umma.cuh"
 
 namespace ssm {
 namespace delta {
@@ -47,16 +47,11 @@ constexpr int kThreadsF = (kRowWarps + kMatWarps + 4) * 32;  // 16-18: products,
 // Registers per thread: 96 at launch, then by group of four warps
 constexpr int kLaunchRegs = 96, kRowRegs = 144, kMatRegs = 80, kRestRegs = 32;
 static_assert(2 * kRowRegs + 2 * kMatRegs + kRestRegs <= 5 * kLaunchRegs, "no more than the block was launched with");
-constexpr uint32_t kHalfTile = kC * 128;  // 64 rows x 128 bytes
 constexpr int kDLd = 36;                 // row stride of a 32 x 32 float32 block: 16-byte rows
 
 // tensor memory columns
 constexpr uint32_t kTX = 0, kTO1 = 64, kTY = 128, kTO2 = 192, kTS = 256, kTSh = 384, kTSl = 448;
-// R, later r (where X was) and w beta r (where Y was): tokens 32 wg .. 32 wg + 31 of
-// both terms stay within the columns that their warps have read themselves
-__host__ __device__ constexpr uint32_t operand_col(uint32_t base, int kstep, int term) {
-    return base + 32 * (kstep >> 1) + 16 * term + 8 * (kstep & 1);
-}
+// operands in two terms: R, later r (where X was) and w beta r (where Y was)
 
 struct __align__(16) Dec {         // per chunk, float32
     float gam[kC], gs[kC], wb[kC];  // exp G, scale exp G, exp(G_C - G) beta
@@ -73,6 +68,7 @@ struct FusedSmem {
     unsigned char v[2][2][kHalfTile];        // V, later the output
     unsigned char np[2][2][2 * kHalfTile];   // [M; Pb]: high, low term
     unsigned char l[2][kHalfTile];           // L: high, low term
+    unsigned char rlo[2][2][kHalfTile];      // STORE: r's low term (the high one over V)
     float ld32[kC][kDLd];                    // L's 32 x 32 diagonal blocks
     Dec dec[2];
     // Barriers whose waiters may fall a chunk behind have one per stage, so that
@@ -81,6 +77,7 @@ struct FusedSmem {
     uint64_t kqd, x, y, o, s[2];             // products complete ([K; Q] K^T first)
     uint64_t s_ready[NT], r_ready, w_ready, u_ready, o_ready[2];  // row-wise results written
     uint64_t o_taken[2];                     // O1 and O2 are in registers
+    uint64_t np_free[2];                     // STORE: the matrices have left
     uint64_t kq_read;                        // [K; Q] K^T is in registers
     uint64_t fin;
     uint32_t tmem;
@@ -100,13 +97,11 @@ struct FusedArgs {
     int seg_chunks, nseg;
     const float *starts;
     float *ends, *phi;
+    // STORE
+    bf16 *s0;
+    float *dec;
     unsigned int *status;
 };
-
-template <int N>
-__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // all eight warps of the chunk matrices; the first four of them
 __device__ __forceinline__ void mats_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -118,10 +113,6 @@ __device__ __forceinline__ bool mats_all(bool ok) {
     asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.and.pred p, 1, 256, q;\nselp.u32 %0, 1, 0, p;\n}\n"
                  : "=r"(all) : "r"((uint32_t)ok) : "memory");
     return all != 0;
-}
-
-__device__ __forceinline__ bf16 *tile_at(unsigned char *tile, int row, int col) {
-    return reinterpret_cast<bf16 *>(tile + sw128_offset(row, col >> 3) + (col & 7) * 2);
 }
 
 // ------------------------------------------------------- the chunk matrices
@@ -290,19 +281,15 @@ __device__ __forceinline__ void chunk_matrices(FusedSmem<NT> &sm, int c, int w, 
 }
 
 // ------------------------------------------------------------- row-wise work
-// 32 columns as two bf16 terms, 16 tensor memory columns each.
-__device__ __forceinline__ void put_terms(uint32_t hi_col, uint32_t lo_col, const float (&v)[32]) {
-    uint32_t hi[16], lo[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) split(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
-    tmem_st16(hi_col, hi);
-    tmem_st16(lo_col, lo);
-}
-
 // 32 columns of the state: its two terms, and gam_C of the next chunk times it
-// where the next chunk's product accumulates.
-__device__ __forceinline__ void put_state(uint32_t tl, int col, const float (&s)[32], float whole) {
-    put_terms(tl + kTSh + col / 2, tl + kTSl + col / 2, s);
+// where the next chunk's product accumulates.  `copy`: the terms also go to a
+// (2, pp, NP) array in global memory.
+__device__ __forceinline__ void put_state(uint32_t tl, int col, const float (&s)[32], float whole, bf16 *copy, int64_t to_low) {
+    uint32_t hi[16], lo[16];
+    terms(s, hi, lo);
+    tmem_st16(tl + kTSh + col / 2, hi);
+    tmem_st16(tl + kTSl + col / 2, lo);
+    if (copy) put_row_terms(copy + col, to_low, hi, lo);
     uint32_t r[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(whole * s[i]);
@@ -313,11 +300,19 @@ __device__ __forceinline__ void put_state(uint32_t tl, int col, const float (&s)
 // rows of V (from zero, the first segment from h0) to the state it ends with, or
 // takes the rows of the unit matrix through it with V = 0: the state is linear
 // in its start, S_end = S_start Phi + (S_end from zero).
-template <int NT, bool AGG>
+//
+// STORE: the gradient's first half.  No output; r, the state entering each
+// chunk, M and Pb and the decays go to the workspace (DeltaChunkWs); mapO then
+// describes r, (units x 2, 64, headdim), and mapM the matrices, (units x 2, 128,
+// 64).
+enum Mode { kOut, kAgg, kStore };
+
+template <int NT, int MODE>
 __global__ void __launch_bounds__(kThreadsF, 1)
 delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                    const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapO,
-                   const FusedArgs a) {
+                   const __grid_constant__ CUtensorMap mapM, const FusedArgs a) {
+    constexpr bool AGG = MODE == kAgg, OUT = MODE == kOut, STORE = MODE == kStore;
     extern __shared__ unsigned char raw[];
     // 1024-byte aligned by an offset, not by a rounded address: a pointer made from
     // an integer would turn every shared access into a generic one
@@ -356,6 +351,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             mbar_init(&sm.ldk[i], 1);
             mbar_init(&sm.ldv[i], 1);
             mbar_init(&sm.o_taken[i], row_warps);
+            mbar_init(&sm.np_free[i], 1);
             mbar_init(&sm.cum[i], 1);
             mbar_init(&sm.m[i], 4);
             mbar_init(&sm.pb[i], kMatWarps);
@@ -462,7 +458,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                 mma_bf16_ts_if(el, tm + kTS, tm + operand_col(kTY, k & 3, k >> 2), dk + (((k & 3) * 2048) >> 4), id_s, true);
             mma_commit_if(el, &sm.s[st]);
             if (c + 1 < nch && !(ok = wait(&sm.kq_read, c + 1))) break;
-            if constexpr (!AGG) {
+            if constexpr (OUT) {
                 if (!(ok = wait(&sm.u_ready, c)) || !(ok = wait(&sm.pb[st], c >> 1))) break;
                 fence_after_sync();
                 r_product(dh + (kHalfTile >> 4), dl + (kHalfTile >> 4), kTO2);
@@ -496,7 +492,23 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             if (unit_rows) continue;
             if (c >= 0) {  // (AGG: the rows have read V)
                 if (!(ok = wait(&sm.o_ready[st], c >> 1))) break;
-                if constexpr (!AGG) {
+                if constexpr (STORE) {
+                    if (!(ok = wait(&sm.pb[st], c >> 1)) || !(ok = wait(&sm.m[st], c >> 1))) break;
+                    if (el) {
+                        const int32_t unit2 = (int32_t)((bh * all_chunks + c) * 2);
+#pragma unroll 1
+                        for (int term = 0; term < 2; ++term) {
+                            if (v0 == 0) tma_store_3d(&mapM, 0, 0, unit2 + term, sm.np[st][term]);
+                            for (int i = 0; i < halves; ++i)
+                                tma_store_3d(&mapO, v0 + 64 * i, 0, unit2 + term, term ? sm.rlo[st][i] : sm.v[st][i]);
+                        }
+                        tma_store_commit();
+                        tma_store_wait_read<0>();
+                        mbar_arrive(&sm.np_free[st]);
+                    }
+                    __syncwarp();
+                }
+                if constexpr (OUT) {
                     if (el) {
 #pragma unroll 1
                         for (int i = 0; i < halves; ++i)
@@ -555,6 +567,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             const double end = __shfl_sync(0xffffffffu, sum, 31);
             // chunk c - 2 is done with its decays and matrices
             if (c >= 2 && !(ok = wait(&sm.o_taken[st], (c - 2) >> 1))) break;
+            if (STORE && c >= 2 && !(ok = wait(&sm.np_free[st], (c - 2) >> 1))) break;
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
@@ -566,7 +579,14 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                 dec.gs[t] = a.scale * gam;
                 dec.beta[t] = be;
                 dec.sbeta[t] = a.scale * be;
-                dec.wb[t] = ex2_approx((float)(end - cum)) * be;
+                const float wend = ex2_approx((float)(end - cum));
+                dec.wb[t] = wend * be;
+                if (STORE && v0 == 0) {
+                    float *to = a.dec + (bh * all_chunks + c) * (kDec * kC) + t;
+                    to[0] = gam;
+                    to[kC] = wend;
+                    to[2 * kC] = be;
+                }
             }
             if (lane == 31) dec.whole = ex2_approx((float)end);
             signal(&sm.cum[st]);
@@ -606,7 +626,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         float *to = AGG ? (unit_rows ? a.phi + ((bh * a.nseg + seg) * a.dstate + r) * (int64_t)a.dstate
                                      : a.ends + ((bh * a.nseg + seg) * a.headdim + v0 + r) * (int64_t)a.dstate)
                         : (a.state && seg == a.nseg - 1 ? a.state + row * a.dstate : nullptr);
-        const int vp = (((r & 63) >> 3) << 4) + (r & 7) * 2;  // this row's place in row 0 of the V tile
+        const int vp = token_place(r);
       if (32 * quad < 64 * halves) {
         // the start state, where the first chunk's "last product" would have left it
         {
@@ -637,16 +657,6 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         uint32_t vv[16], ov[16];  // this row's values of V and of the output, packed pairs of tokens
 #pragma unroll
         for (int i = 0; i < 16; ++i) vv[i] = 0;  // unit rows have no V
-        auto load_v = [&](int c) {
-            const unsigned char *vt = sm.v[c & 1][r >> 6] + 32 * wg * 128;
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                const unsigned short u0 = *reinterpret_cast<const unsigned short *>(vt + ((vp ^ ((i & 7) << 4)) + 128 * i));
-                const unsigned short u1 =
-                    *reinterpret_cast<const unsigned short *>(vt + ((vp ^ (((i + 1) & 7) << 4)) + 128 * (i + 1)));
-                vv[i / 2] = (uint32_t)u0 | ((uint32_t)u1 << 16);
-            }
-        };
         // Chunk c's state is there when chunk c - 1's last product is done.  Work that
         // no product waits for -- the last chunk's output, the next V -- stands where
         // the warp would wait for one.  The step behind the last chunk only stores the
@@ -657,11 +667,11 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             if (c < nch && !(ok = wait(&sm.cum[st], c >> 1))) break;
             if (c < nch && !unit_rows) {
                 if (!(ok = wait(&sm.ldv[st], c >> 1))) break;
-                load_v(c);
+                load_tokens(sm.v[st][r >> 6] + 32 * wg * 128, vp, vv);
                 if constexpr (AGG) signal(&sm.o_ready[st]);
             }
-            if (AGG && c > 0) signal(&sm.o_taken[st ^ 1]);
-            if (!AGG && c > 0) {
+            if (!OUT && c > 0) signal(&sm.o_taken[st ^ 1]);
+            if (OUT && c > 0) {
                 if (!(ok = wait(&sm.o, c - 1))) break;
                 fence_after_sync();
                 float o1[32], o2[32];
@@ -687,7 +697,9 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                 tmem_ld32(tl + kTS + col, s);
                 tmem_wait_ld();
                 if (c < nch) {
-                    put_state(tl, col, s, dec.whole);
+                    put_state(tl, col, s, dec.whole,
+                              STORE ? a.s0 + ((bh * all_chunks + c) * 2 * a.headdim + v0 + r) * (int64_t)a.dstate : nullptr,
+                              (int64_t)a.headdim * a.dstate);
                     tmem_wait_st();
                     fence_before_sync();
                     signal(&sm.s_ready[p]);
@@ -723,15 +735,8 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                 fence_before_sync();
                 signal(&sm.r_ready);
             }
-            if (!AGG && c > 0) {  // the last chunk's output over its V
-                unsigned char *vt = sm.v[st ^ 1][r >> 6] + 32 * wg * 128;
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    *reinterpret_cast<unsigned short *>(vt + ((vp ^ ((i & 7) << 4)) + 128 * i)) =
-                        (unsigned short)(ov[i / 2] & 0xffffu);
-                    *reinterpret_cast<unsigned short *>(vt + ((vp ^ (((i + 1) & 7) << 4)) + 128 * (i + 1))) =
-                        (unsigned short)(ov[i / 2] >> 16);
-                }
+            if (OUT && c > 0) {  // the last chunk's output over its V
+                store_tokens(sm.v[st ^ 1][r >> 6] + 32 * wg * 128, vp, ov);
                 fence_proxy_async();
                 signal(&sm.o_ready[st ^ 1]);
             }
@@ -756,11 +761,19 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             tmem_wait_st();
             fence_before_sync();
             signal(&sm.w_ready);
-            if constexpr (!AGG) {
+            if constexpr (OUT) {
                 put_terms(tl + kTX + 32 * wg, tl + kTX + 32 * wg + 16, res);
                 tmem_wait_st();
                 fence_before_sync();
                 signal(&sm.u_ready);
+            }
+            if constexpr (STORE) {
+                uint32_t hi[16], lo[16];
+                terms(res, hi, lo);
+                store_tokens(sm.v[st][r >> 6] + 32 * wg * 128, vp, hi);
+                store_tokens(sm.rlo[st][r >> 6] + 32 * wg * 128, vp, lo);
+                fence_proxy_async();
+                signal(&sm.o_ready[st]);
             }
         }
       }
@@ -843,10 +856,10 @@ cudaError_t launch_t(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st) {
         f.phi = f.ends + bh * nseg * a.headdim * a.dstate;
         float *starts = f.phi + bh * nseg * a.dstate * (int64_t)a.dstate;
         f.starts = starts;
-        e = allow_smem<delta_fused_kernel<NT, true>, bytes>();
+        e = allow_smem<delta_fused_kernel<NT, kAgg>, bytes>();
         if (e != cudaSuccess) return e;
         const int64_t blocks = bh * ((nseg - 1) * f.vtiles + nseg - 2);
-        delta_fused_kernel<NT, true><<<(unsigned)blocks, kThreadsF, bytes, st>>>(mq, mk, mv, mo, f);
+        delta_fused_kernel<NT, kAgg><<<(unsigned)blocks, kThreadsF, bytes, st>>>(mq, mk, mv, mo, mo, f);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         delta_join_kernel<<<(unsigned)(bh * (a.headdim / kJoinRows)), 128, 0, st>>>(a.h0, f.ends, f.phi, starts, nseg, a.headdim,
@@ -854,9 +867,37 @@ cudaError_t launch_t(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    e = allow_smem<delta_fused_kernel<NT, false>, bytes>();
+    e = allow_smem<delta_fused_kernel<NT, kOut>, bytes>();
     if (e != cudaSuccess) return e;
-    delta_fused_kernel<NT, false><<<(unsigned)(bh * nseg * f.vtiles), kThreadsF, bytes, st>>>(mq, mk, mv, mo, f);
+    delta_fused_kernel<NT, kOut><<<(unsigned)(bh * nseg * f.vtiles), kThreadsF, bytes, st>>>(mq, mk, mv, mo, mo, f);
+    return cudaGetLastError();
+}
+
+template <int NT>
+cudaError_t launch_store_t(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st) {
+    CUtensorMap mq, mk, mv, mr, mm;
+    const int64_t gn = (int64_t)a.groups * a.dstate, hp = (int64_t)a.heads * a.headdim, bh = a.batch * a.heads;
+    const int64_t chunks = (a.seqlen + kC - 1) / kC;
+    if (!encode_btw(&mq, a.q, a.batch, a.seqlen, gn, kC) || !encode_btw(&mk, a.k, a.batch, a.seqlen, gn, kC) ||
+        !encode_btw(&mv, a.v, a.batch, a.seqlen, hp, kC) ||
+        !encode_btw(&mr, ws.r, bh * chunks * 2, kC, a.headdim, kC) ||
+        !encode_btw(&mm, ws.mats, bh * chunks * 2, 2 * kC, kC, 2 * kC))
+        return cudaErrorInvalidValue;
+    FusedArgs f{};
+    f.g = a.g; f.beta = a.beta; f.h0 = a.h0; f.scale = a.scale;
+    f.seqlen = a.seqlen; f.heads = a.heads; f.rep = a.heads / a.groups; f.headdim = a.headdim; f.dstate = a.dstate;
+    f.vtiles = (a.headdim + 127) / 128;
+    f.vec_state = aligned16(a.h0);
+    f.seg_chunks = (int)chunks;
+    f.nseg = 1;
+    f.s0 = ws.s0;
+    f.dec = ws.dec;
+    cudaError_t e = device_status_address(&f.status);
+    if (e != cudaSuccess) return e;
+    constexpr int bytes = (int)sizeof(FusedSmem<NT>) + 1024;
+    e = allow_smem<delta_fused_kernel<NT, kStore>, bytes>();
+    if (e != cudaSuccess) return e;
+    delta_fused_kernel<NT, kStore><<<(unsigned)(bh * f.vtiles), kThreadsF, bytes, st>>>(mq, mk, mv, mr, mm, f);
     return cudaGetLastError();
 }
 
@@ -898,6 +939,10 @@ int delta_fused_segments(const DeltaArgs &a, int sms) {
 }
 
 int64_t delta_fused_workspace(const DeltaArgs &a, int nseg) { return nseg > 1 ? 4 * delta::split_floats(a, nseg) : 0; }
+
+cudaError_t launch_delta_fused_store(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st) {
+    return a.dstate == 64 ? delta::launch_store_t<1>(a, ws, st) : delta::launch_store_t<2>(a, ws, st);
+}
 
 cudaError_t launch_delta_fused(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st) {
     return a.dstate == 64 ? delta::launch_t<1>(a, nseg, ws, st) : delta::launch_t<2>(a, nseg, ws, st);

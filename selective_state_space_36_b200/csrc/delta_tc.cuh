@@ -1,0 +1,76 @@
+// delta_tc.cuh -- what the two tcgen05 kernels of the gated delta rule share (the
+// forward's delta_fused.cu, the gradient's delta_fused_bwd.cu).
+#pragma once
+
+#include "delta_chunk.cuh"
+#include "umma.cuh"
+
+namespace ssm {
+namespace delta {
+
+constexpr uint32_t kHalfTile = kC * 128;  // 64 rows x 128 bytes
+
+// Columns of a chunk operand of two terms (64 tokens x 2 terms, 64 columns from
+// `base`), K step `kstep` of 16 tokens: the tokens 32 wg .. 32 wg + 31 of both
+// terms stay within the 32 columns that their warps (wg) have read themselves, so
+// that an operand can replace the product that it was computed from.
+__host__ __device__ constexpr uint32_t operand_col(uint32_t base, int kstep, int term) {
+    return base + 32 * (kstep >> 1) + 16 * term + 8 * (kstep & 1);
+}
+
+template <int N>
+__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ bf16 *tile_at(unsigned char *tile, int row, int col) {
+    return reinterpret_cast<bf16 *>(tile + umma::sw128_offset(row, col >> 3) + (col & 7) * 2);
+}
+
+// 32 values in order as two bf16 terms, packed pairs.
+__device__ __forceinline__ void terms(const float (&v)[32], uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) split(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
+}
+
+// 32 columns as two bf16 terms, 16 tensor memory columns each.
+__device__ __forceinline__ void put_terms(uint32_t hi_col, uint32_t lo_col, const float (&v)[32]) {
+    uint32_t hi[16], lo[16];
+    terms(v, hi, lo);
+    umma::tmem_st16(hi_col, hi);
+    umma::tmem_st16(lo_col, lo);
+}
+
+// A row's 32 values, both terms, to a (2, pp, ld) array in global memory.
+__device__ __forceinline__ void put_row_terms(bf16 *at, int64_t to_low, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<uint4 *>(at + 8 * i) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+        *reinterpret_cast<uint4 *>(at + to_low + 8 * i) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+    }
+}
+
+// One state row's values of 32 tokens in a swizzled tile of 64 tokens (rows) x 64
+// state rows: `vt` the tile at the first of the tokens, `vp` the row's place in
+// its first token's line.  Packed pairs of tokens.
+__device__ __forceinline__ void load_tokens(const unsigned char *vt, int vp, uint32_t (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        const unsigned short u0 = *reinterpret_cast<const unsigned short *>(vt + ((vp ^ ((i & 7) << 4)) + 128 * i));
+        const unsigned short u1 =
+            *reinterpret_cast<const unsigned short *>(vt + ((vp ^ (((i + 1) & 7) << 4)) + 128 * (i + 1)));
+        x[i / 2] = (uint32_t)u0 | ((uint32_t)u1 << 16);
+    }
+}
+__device__ __forceinline__ void store_tokens(unsigned char *vt, int vp, const uint32_t (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        *reinterpret_cast<unsigned short *>(vt + ((vp ^ ((i & 7) << 4)) + 128 * i)) = (unsigned short)(x[i / 2] & 0xffffu);
+        *reinterpret_cast<unsigned short *>(vt + ((vp ^ (((i + 1) & 7) << 4)) + 128 * (i + 1))) =
+            (unsigned short)(x[i / 2] >> 16);
+    }
+}
+__device__ __forceinline__ int token_place(int r) { return (((r & 63) >> 3) << 4) + (r & 7) * 2; }
+
+}  // namespace delta
+}  // namespace ssm

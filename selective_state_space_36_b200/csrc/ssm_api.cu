@@ -1031,8 +1031,12 @@ ssm_status ssm_delta_rule_bwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, co
         const int sms = device_sms();
         e = delta_chunk_workspace(units, (dims.headdim + 15) / 16 * 16, dims.dstate <= 64 ? 64 : 128, &mem, &ws, st);
         if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
-        e = ssm::launch_delta_prep(p.f, ws, st);
-        if (e == cudaSuccess) e = ssm::launch_delta_chain_store(p.f, ws, sms, st);
+        if (ssm::delta_fused_eligible(p.f)) {
+            e = ssm::launch_delta_fused_store(p.f, ws, st);
+        } else {
+            e = ssm::launch_delta_prep(p.f, ws, st);
+            if (e == cudaSuccess) e = ssm::launch_delta_chain_store(p.f, ws, sms, st);
+        }
         if (e == cudaSuccess) e = ssm::launch_delta_reverse(p, ws, sms, st);
         if (e == cudaSuccess) e = ssm::launch_delta_grad(p, ws, st);
     } else {
