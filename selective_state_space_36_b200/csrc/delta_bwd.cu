@@ -318,7 +318,13 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(DeltaBwdArgs p
         load_tile<true>(sr, ldp, ws.r + unit * 2 * kC * pp, pp, 2 * kC, pp, 2 * kC, pp, tid, kGradThreads);
         load_tile<true>(se, ldp, ws.dv + unit * 2 * kC * pp, pp, 2 * kC, pp, 2 * kC, pp, tid, kGradThreads);
         cp_async_commit();
-        load_tile<true>(ss, lds, ws.s0 + unit * 2 * pp * NP, NP, 2 * pp, NP, 2 * pp, NP, tid, kGradThreads);
+        {
+            const bf16 *src = ws.s0 + unit * 2 * pp * NP;
+            for (int i = tid; i < 2 * pp * (NP / 8); i += kGradThreads) {  // 16 bytes each, in their order in memory
+                const int g = i / pp, row = i - g * pp, term = g / (NP / 8);
+                cp_async16(ss + (term * pp + row) * lds + (g - term * (NP / 8)) * 8, src + (int64_t)i * 8, true);
+            }
+        }
         cp_async_commit();
         if (tid < kDec * kC) sm.dec[tid / kC][tid % kC] = ws.dec[unit * (kDec * kC) + tid];
         if (warp == 7) {
@@ -502,13 +508,12 @@ __global__ void __launch_bounds__(kGradThreads) delta_grad_kernel(DeltaBwdArgs p
         // dS1 takes its place; <S0, dS1> on the way
         float inner = 0.f;
         {
-            const int per = NP / 8;
             const bf16 *src = ws.ds1 + unit * 2 * pp * NP;
-            for (int i = tid; i < pp * per; i += kGradThreads) {
-                const int r = i / per, c = (i - r * per) * 8;
-                bf16 *at = ss + r * lds + c;
-                const uint4 nh = *reinterpret_cast<const uint4 *>(src + (int64_t)r * NP + c);
-                const uint4 nl = *reinterpret_cast<const uint4 *>(src + (int64_t)(pp + r) * NP + c);
+            for (int i = tid; i < pp * (NP / 8); i += kGradThreads) {
+                const int g = i / pp;
+                bf16 *at = ss + (i - g * pp) * lds + g * 8;
+                const uint4 nh = *reinterpret_cast<const uint4 *>(src + (int64_t)i * 8);
+                const uint4 nl = *reinterpret_cast<const uint4 *>(src + (int64_t)pp * NP + (int64_t)i * 8);
                 const uint4 oh = *reinterpret_cast<const uint4 *>(at), ol = *reinterpret_cast<const uint4 *>(at + pp * lds);
                 const uint32_t w0[4] = {nh.x, nh.y, nh.z, nh.w}, w1[4] = {nl.x, nl.y, nl.z, nl.w};
                 const uint32_t w2[4] = {oh.x, oh.y, oh.z, oh.w}, w3[4] = {ol.x, ol.y, ol.z, ol.w};

@@ -112,8 +112,17 @@ __device__ __forceinline__ void load_tile(bf16 *s, int sld, const bf16 *g, int64
     }
 }
 
+// A stored state: two bf16 terms, each as (NP / 8, pp, 8) -- the eight columns of
+// a group row after row, so that neither a thread per row nor a quad per row
+// spreads a store over more lines than its bytes fill (row-major, the forward's
+// recomputation spent two thirds of its time in these stores).
+template <int NP>
+__device__ __forceinline__ int64_t state_at(int pp, int term, int row, int col) {
+    return ((int64_t)(term * (NP / 8) + (col >> 3)) * pp + row) * 8 + (col & 7);
+}
+
 // A warp's 16 x NP slice of a state (accumulators: rows row0 + lane / 4 (+ 8),
-// columns 8 j + 2 (lane % 4) (+ 1)) as two bf16 terms: high (pp, NP), then low.
+// columns 8 j + 2 (lane % 4) (+ 1)).
 template <int NP>
 __device__ __forceinline__ void store_state(bf16 *dst, int pp, const float (&s)[NP / 8][4], int row0, int lane) {
     if (row0 >= pp) return;
@@ -123,9 +132,9 @@ __device__ __forceinline__ void store_state(bf16 *dst, int pp, const float (&s)[
         for (int half = 0; half < 2; ++half) {
             uint32_t hi, lo;
             split(s[j][2 * half], s[j][2 * half + 1], hi, lo);
-            const int64_t at = (int64_t)(row0 + (lane >> 2) + 8 * half) * NP + 8 * j + 2 * (lane & 3);
-            *reinterpret_cast<uint32_t *>(dst + at) = hi;
-            *reinterpret_cast<uint32_t *>(dst + (int64_t)pp * NP + at) = lo;
+            const int row = row0 + (lane >> 2) + 8 * half, col = 8 * j + 2 * (lane & 3);
+            *reinterpret_cast<uint32_t *>(dst + state_at<NP>(pp, 0, row, col)) = hi;
+            *reinterpret_cast<uint32_t *>(dst + state_at<NP>(pp, 1, row, col)) = lo;
         }
 }
 
@@ -168,7 +177,7 @@ struct DeltaChunkWs {
     __nv_bfloat16 *mats;  // (batch, heads, chunks, kMats, 64, 64)
     float *dec;           // (batch, heads, chunks, kDec, 64)
     // backward only; headdim rounded up to 16 (pp), dstate to 64 or 128 (np)
-    __nv_bfloat16 *s0;    // (batch, heads, chunks, 2, pp, np): the state entering each chunk
+    __nv_bfloat16 *s0;    // (batch, heads, chunks, 2, np / 8, pp, 8): the state entering each chunk
     __nv_bfloat16 *ds1;   // the same: the gradient of the state leaving it
     __nv_bfloat16 *r, *dv; // (batch, heads, chunks, 2, 64, pp): r, the gradient of V
 };

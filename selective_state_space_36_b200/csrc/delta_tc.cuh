@@ -41,12 +41,16 @@ __device__ __forceinline__ void put_terms(uint32_t hi_col, uint32_t lo_col, cons
     umma::tmem_st16(lo_col, lo);
 }
 
-// A row's 32 values, both terms, to a (2, pp, ld) array in global memory.
-__device__ __forceinline__ void put_row_terms(bf16 *at, int64_t to_low, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
+// A row's 32 values from column `col`, both terms, into a stored state.
+template <int NP>
+__device__ __forceinline__ void put_state_row(bf16 *state, int pp, int row, int col, const uint32_t (&hi)[16],
+                                              const uint32_t (&lo)[16]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        *reinterpret_cast<uint4 *>(at + 8 * i) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-        *reinterpret_cast<uint4 *>(at + to_low + 8 * i) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+        *reinterpret_cast<uint4 *>(state + state_at<NP>(pp, 0, row, col + 8 * i)) =
+            make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+        *reinterpret_cast<uint4 *>(state + state_at<NP>(pp, 1, row, col + 8 * i)) =
+            make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
     }
 }
 
