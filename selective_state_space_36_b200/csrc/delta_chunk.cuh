@@ -198,6 +198,6 @@ cudaError_t launch_delta_prep(const DeltaArgs &a, const DeltaChunkWs &ws, cudaSt
 cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
 cudaError_t launch_delta_chain_store(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
 cudaError_t launch_delta_reverse(const DeltaBwdArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
-cudaError_t launch_delta_grad(const DeltaBwdArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
+cudaError_t launch_delta_grad(const DeltaBwdArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
 
 }  // namespace ssm

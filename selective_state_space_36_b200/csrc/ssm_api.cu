@@ -1038,7 +1038,7 @@ ssm_status ssm_delta_rule_bwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, co
             if (e == cudaSuccess) e = ssm::launch_delta_chain_store(p.f, ws, sms, st);
         }
         if (e == cudaSuccess) e = ssm::launch_delta_reverse(p, ws, sms, st);
-        if (e == cudaSuccess) e = ssm::launch_delta_grad(p, ws, st);
+        if (e == cudaSuccess) e = ssm::launch_delta_grad(p, ws, sms, st);
     } else {
         const size_t marks = (size_t)units * dims.headdim * dims.dstate, r = (size_t)tokens * dims.heads * dims.headdim;
         const size_t per_head = (size_t)tokens * dims.heads * dims.dstate;
