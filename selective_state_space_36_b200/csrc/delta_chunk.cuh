@@ -194,6 +194,11 @@ cudaError_t launch_delta_fused(const DeltaArgs &a, int nseg, float *ws, cudaStre
 // the workspace but ds1 and dv.
 cudaError_t launch_delta_fused_store(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
 
+// The pass backwards in time on tcgen05: what delta_fused_eligible asks, headdim <=
+// 128, dout and dv aligned too.
+bool delta_fused_reverse_eligible(const DeltaBwdArgs &a);
+cudaError_t launch_delta_fused_reverse(const DeltaBwdArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
+
 cudaError_t launch_delta_prep(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
 cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
 cudaError_t launch_delta_chain_store(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);

@@ -1,0 +1,448 @@
+// delta_fused_bwd.cu -- the pass backwards in time of the chunked gated delta
+// rule's gradient (formulas at delta_bwd.cu) on the sm_100a tensor cores.
+//
+// The forward kernel's mirror image (delta_fused.cu): one CTA has a head's state
+// rows as the 128 lanes of tensor memory and walks over the chunks from the last
+// to the first.  M, Pb and the decays come from the workspace, where the forward's
+// recomputation left them.  Per chunk, with dS the gradient of the state leaving it:
+//   W^T  = dO^T Pb                                  (128 x 64, K = 64)
+//   X^T  = dS K^T                                   (128 x 64, K = dstate)
+//   Y^T  = z^T M,         z = W + w beta X          (128 x 64, K = 64)
+//   dS   = gam_C dS + (scale gam dO)^T Q - (gam dV)^T K    (128 x dstate, K = 64 twice),  dV = z - Y
+// The row X - z - Y - dV - dS is what the next chunk waits for; W of the next
+// chunk and the product with Q fill the tensor cores' waits in between.  Operands
+// that are not bf16 already take two bf16 terms.
+//
+// Warps: 0-7 row-wise work (two per lane quarter, each half of the columns), 8
+// issues the products, 9 the TMA copies, 10 the decays.  They meet at mbarriers
+// only; every wait is bounded and reports through the device status word.
+#include "delta_chunk.cuh"
+#include "delta_tc.cuh"
+#include "kernel_setup.cuh"
+#include "scan_kernels.cuh"
+#include "ssm_device.cuh"
+#include "tma_maps.cuh"
+
+namespace ssm {
+namespace delta {
+namespace {
+
+using namespace umma;
+
+constexpr int kRowWarps = 8;
+constexpr int kThreadsR = (kRowWarps + 4) * 32;  // 8-10: products, copies, decays; one idle
+
+// tensor memory columns; operands of two terms: z (where X was), gam dV (where Y
+// was), scale gam dO (where W was); dO itself
+constexpr uint32_t kTX = 0, kTW = 64, kTY = 128, kTD = 192, kTS = 256, kTSh = 384, kTSl = 448;
+
+struct __align__(16) RevDec {          // per chunk
+    float gam[kC], gs[kC], wb[kC];     // exp G, scale exp G, exp(G_C - G) beta
+};
+
+template <int NT>
+struct RevSmem {
+    unsigned char kq[2][NT][2 * kHalfTile];  // per stage and 64 columns: K rows, then Q rows
+    unsigned char o[2][2][kHalfTile];        // dO, later dV's high term
+    unsigned char lo[2][2][kHalfTile];       // dV's low term
+    unsigned char np[2][2][2 * kHalfTile];   // [M; Pb]: high, low term
+    RevDec dec[2];
+    uint64_t ldk[2], ldo[2], cum[2];         // K, Q, M and Pb, dO landed; decays
+    uint64_t w, x, y, s[2];                  // products complete
+    uint64_t d_ready, g_ready, s_ready[NT], z_ready, v_ready, o_ready[2];  // row-wise results written
+    uint64_t fin;
+    uint32_t tmem;
+};
+
+struct RevArgs {
+    const float *dec, *dend;
+    float *dh0;
+    bf16 *ds1;
+    float scale;
+    int64_t seqlen;
+    int heads, rep, headdim, dstate;
+    int vec_state;  // dend and dh0 start 16-byte aligned
+    unsigned int *status;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kThreadsR, 1)
+delta_fused_reverse_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                           const __grid_constant__ CUtensorMap mapO, const __grid_constant__ CUtensorMap mapV,
+                           const __grid_constant__ CUtensorMap mapT, const __grid_constant__ CUtensorMap mapM,
+                           const RevArgs a) {
+    extern __shared__ unsigned char raw[];
+    RevSmem<NT> &sm = *reinterpret_cast<RevSmem<NT> *>(raw + ((0u - smem_u32(raw)) & 1023u));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t bh = blockIdx.x, b = bh / a.heads;
+    const int h = (int)(bh - b * a.heads), gr = h / a.rep;
+    const int nch = (int)((a.seqlen + kC - 1) / kC);
+    const int halves = a.headdim > 64 ? 2 : 1;  // 64-row halves of the state
+    const int row_warps = 4 * halves;           // whose lanes hold rows of the state
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.ldk[i], 1);
+            mbar_init(&sm.ldo[i], 1);
+            mbar_init(&sm.cum[i], 1);
+            mbar_init(&sm.s[i], 1);
+            mbar_init(&sm.o_ready[i], row_warps);
+        }
+        mbar_init(&sm.w, 1);
+        mbar_init(&sm.x, 1);
+        mbar_init(&sm.y, 1);
+        mbar_init(&sm.d_ready, row_warps);
+        mbar_init(&sm.g_ready, row_warps);
+        for (int i = 0; i < NT; ++i) mbar_init(&sm.s_ready[i], row_warps);
+        mbar_init(&sm.z_ready, row_warps);
+        mbar_init(&sm.v_ready, row_warps);
+        mbar_init(&sm.fin, 1);
+        mbar_fence_init();
+    }
+    if (warp == 0) tmem_alloc(&sm.tmem, 512);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tm = sm.tmem;
+    auto wait = [&](uint64_t *bar, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait_2s(bar, par & 1u)) != 0; };
+    bool ok = true;  // false: a wait of this warp ran out
+    auto signal = [&](uint64_t *bar) {  // one arrival per warp, after the warp's writes
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+
+    // Step c is chunk nch - 1 - c, stage c & 1.
+    if (warp == kRowWarps) {
+        // ------------------------------------------------ the products
+        const uint32_t el = elect_one();
+        constexpr uint32_t id_x = idesc_bf16(128, 64, kMajorK, kMajorK);
+        constexpr uint32_t id_m = idesc_bf16(128, 64, kMajorK, kMajorMN);
+        constexpr uint32_t id_s = idesc_bf16(128, 64 * NT, kMajorK, kMajorMN);
+        auto w_product = [&](int st) {  // dO with Pb's high terms, then its low ones
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                mma_bf16_ts_if(el, tm + kTW, tm + kTD + 8 * (k & 3),
+                               desc_sw128(smem_u32(sm.np[st][k >> 2]) + kHalfTile + (k & 3) * 2048, 2 * kHalfTile, 1024),
+                               id_m, k > 0);
+            mma_commit_if(el, &sm.w);
+        };
+        for (int c = -1; ok && c < nch; ++c) {  // (step -1: the first chunk's W only)
+            const int st = c & 1;
+            if (c >= 0) {
+                // tiles with tokens as the summed index: 64 columns, the next 64 in the next tile
+                const uint64_t dk = desc_sw128(smem_u32(sm.kq[st][0]), 2 * kHalfTile, 1024);
+                const uint64_t tile = desc_sw128(smem_u32(sm.kq[st][0]), 16, 1024);
+#pragma unroll
+                for (int part = 0; part < NT; ++part) {
+                    if (!(ok = wait(&sm.s_ready[part], c))) break;
+                    fence_after_sync();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {  // 32-column pieces `part` of both halves, high terms, then low ones
+                        const int k = 2 * NT * ((i >> 1) & 1) + 2 * part + (i & 1);
+                        mma_bf16_ts_if(el, tm + kTX, tm + (i < 4 ? kTSh : kTSl) + 8 * k,
+                                       tile + (((k / 4) * 2 * kHalfTile + (k % 4) * 32) >> 4), id_x, part > 0 || i > 0);
+                    }
+                }
+                if (!ok) break;
+                mma_commit_if(el, &sm.x);
+                if (!(ok = wait(&sm.g_ready, c))) break;
+                fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_bf16_ts_if(el, tm + kTS, tm + operand_col(kTW, k & 3, k >> 2),
+                                   dk + ((kHalfTile + (k & 3) * 2048) >> 4), id_s, true);
+                if (!(ok = wait(&sm.z_ready, c))) break;
+                fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < 12; ++k) {  // z high with high terms, z low with high, z high with low
+                    const int kk = k & 3, term = k >> 2;
+                    mma_bf16_ts_if(el, tm + kTY, tm + operand_col(kTX, kk, term == 1),
+                                   desc_sw128(smem_u32(sm.np[st][term == 2]) + kk * 2048, 2 * kHalfTile, 1024), id_m, k > 0);
+                }
+                mma_commit_if(el, &sm.y);
+            }
+            if (c + 1 < nch) {
+                if (!(ok = wait(&sm.ldk[st ^ 1], (c + 1) >> 1)) || !(ok = wait(&sm.d_ready, c + 1))) break;
+                fence_after_sync();
+                w_product(st ^ 1);
+            }
+            if (c < 0) continue;
+            if (!(ok = wait(&sm.v_ready, c))) break;
+            fence_after_sync();
+            const uint64_t dk = desc_sw128(smem_u32(sm.kq[st][0]), 2 * kHalfTile, 1024);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                mma_bf16_ts_if(el, tm + kTS, tm + operand_col(kTY, k & 3, k >> 2), dk + (((k & 3) * 2048) >> 4), id_s, true);
+            mma_commit_if(el, &sm.s[st]);
+        }
+        mma_commit_if(el, &sm.fin);  // whatever was issued completes before tensor memory goes away
+        (void)mbar_wait_2s(&sm.fin, 0u);
+        __syncwarp();
+    } else if (warp == kRowWarps + 1) {
+        // -------------------------------------------------- the copies
+        const uint32_t el = elect_one();
+        int issued[2] = {0, 0}, issued_o[2] = {0, 0};
+        // step c: chunk c + 2's tiles replace chunk c's once they are used, its dV
+        // leaves (two steps ahead of the first chunk)
+        for (int c = -2; c < nch; ++c) {
+            const int st = c & 1, next = nch - 1 - (c + 2);
+            if (c >= 0 && !(ok = wait(&sm.s[st], c >> 1))) break;
+            if (c + 2 < nch) {
+                if (el) {
+                    mbar_expect_tx(&sm.ldk[st], (uint32_t)(2 * NT + 4) * kHalfTile);
+#pragma unroll 1
+                    for (int i = 0; i < NT; ++i) {
+                        tma_load_3d(sm.kq[st][i], &mapK, gr * a.dstate + 64 * i, next * kC, (int32_t)b, &sm.ldk[st]);
+                        tma_load_3d(sm.kq[st][i] + kHalfTile, &mapQ, gr * a.dstate + 64 * i, next * kC, (int32_t)b,
+                                    &sm.ldk[st]);
+                    }
+#pragma unroll 1
+                    for (int term = 0; term < 2; ++term)
+                        tma_load_3d(sm.np[st][term], &mapM, 0, 0, (int32_t)((bh * nch + next) * 2 + term), &sm.ldk[st]);
+                }
+                if (st) ++issued[1]; else ++issued[0];
+            }
+            if (c >= 0) {
+                if (!(ok = wait(&sm.o_ready[st], c >> 1))) break;
+                if (el) {
+                    const int ch = nch - 1 - c;
+#pragma unroll 1
+                    for (int i = 0; i < halves; ++i) {
+                        tma_store_3d(&mapV, h * a.headdim + 64 * i, ch * kC, (int32_t)b, sm.o[st][i]);
+                        tma_store_3d(&mapT, 64 * i, 0, (int32_t)((bh * nch + ch) * 2), sm.o[st][i]);
+                        tma_store_3d(&mapT, 64 * i, 0, (int32_t)((bh * nch + ch) * 2 + 1), sm.lo[st][i]);
+                    }
+                    tma_store_commit();
+                    tma_store_wait_read<0>();
+                }
+                __syncwarp();
+            }
+            if (c + 2 < nch) {
+                if (el) {
+                    mbar_expect_tx(&sm.ldo[st], (uint32_t)halves * kHalfTile);
+#pragma unroll 1
+                    for (int i = 0; i < halves; ++i)
+                        tma_load_3d(sm.o[st][i], &mapO, h * a.headdim + 64 * i, next * kC, (int32_t)b, &sm.ldo[st]);
+                }
+                if (st) ++issued_o[1]; else ++issued_o[0];
+            }
+        }
+        if (el) tma_store_wait_all<0>();
+        for (int i = 0; i < 2; ++i) {  // no copy outlives the block
+            const int n = i ? issued[1] : issued[0], no = i ? issued_o[1] : issued_o[0];
+            if (n > 0) (void)mbar_wait_2s(&sm.ldk[i], (uint32_t)(n - 1) & 1u);
+            if (no > 0) (void)mbar_wait_2s(&sm.ldo[i], (uint32_t)(no - 1) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == kRowWarps + 2) {
+        // -------------------------------------------------- the decays
+        float2 g = make_float2(0.f, 0.f), we = g, be = g;
+        auto fetch = [&](int c) {
+            const float *d = a.dec + (bh * nch + nch - 1 - c) * (kDec * kC) + 2 * lane;
+            g = *reinterpret_cast<const float2 *>(d);
+            we = *reinterpret_cast<const float2 *>(d + kC);
+            be = *reinterpret_cast<const float2 *>(d + 2 * kC);
+        };
+        fetch(0);
+        for (int c = 0; c < nch; ++c) {
+            const int st = c & 1;
+            // chunk c - 2's row-wise work is done with its decays
+            if (c >= 2 && !(ok = wait(&sm.s[st], (c - 2) >> 1))) break;
+            RevDec &dec = sm.dec[st];
+            *reinterpret_cast<float2 *>(&dec.gam[2 * lane]) = g;
+            *reinterpret_cast<float2 *>(&dec.gs[2 * lane]) = make_float2(a.scale * g.x, a.scale * g.y);
+            *reinterpret_cast<float2 *>(&dec.wb[2 * lane]) = make_float2(we.x * be.x, we.y * be.y);
+            signal(&sm.cum[st]);
+            if (c + 1 < nch) fetch(c + 1);
+        }
+    } else if (warp < kRowWarps && 32 * (warp & 3) < 64 * halves) {
+        // --------------------------------------------- the row-wise work
+        const int quad = warp & 3, wg = warp >> 2, r = 32 * quad + lane;
+        const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
+        const int64_t row = bh * a.headdim + r;
+        const int vp = token_place(r);
+        // the end state's gradient, where the last "product" would have left it
+#pragma unroll 1
+        for (int p = 0; p < NT; ++p) {
+            const int col = 32 * (NT * wg + p);
+            uint32_t s[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = 0;
+            if (a.dend) {
+                const float *src = a.dend + row * a.dstate + col;
+                if (a.vec_state) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(src + i);
+                        s[i] = __float_as_uint(x.x); s[i + 1] = __float_as_uint(x.y);
+                        s[i + 2] = __float_as_uint(x.z); s[i + 3] = __float_as_uint(x.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(src[i]);
+                }
+            }
+            tmem_st32(tl + kTS + col, s);
+        }
+        tmem_wait_st();
+        uint32_t dd[16];  // this row's values of dO, packed pairs of tokens
+        float wv[32];     // W
+        auto put_grad = [&](int c) {  // dO of step c as an operand
+            if (!(ok = wait(&sm.ldo[c & 1], c >> 1))) return;
+            load_tokens(sm.o[c & 1][r >> 6] + 32 * wg * 128, vp, dd);
+            tmem_st16(tl + kTD + 16 * wg, dd);
+            tmem_wait_st();
+            fence_before_sync();
+            signal(&sm.d_ready);
+        };
+        put_grad(0);
+        for (int c = 0; ok && c <= nch; ++c) {
+            const int st = c & 1;
+            const RevDec &dec = sm.dec[st];
+            if (c < nch) {
+                // W; scale gam dO as an operand where it was
+                if (!(ok = wait(&sm.cum[st], c >> 1)) || !(ok = wait(&sm.w, c))) break;
+                fence_after_sync();
+                tmem_ld32(tl + kTW + 32 * wg, wv);
+                tmem_wait_ld();
+                float sd[32];
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 g4 = *reinterpret_cast<const float4 *>(&dec.gs[32 * wg + i]);
+                    sd[i] = g4.x * low_of(dd[i / 2]);
+                    sd[i + 1] = g4.y * high_of(dd[i / 2]);
+                    sd[i + 2] = g4.z * low_of(dd[i / 2 + 1]);
+                    sd[i + 3] = g4.w * high_of(dd[i / 2 + 1]);
+                }
+                put_terms(tl + kTW + 32 * wg, tl + kTW + 32 * wg + 16, sd);
+                tmem_wait_st();
+                fence_before_sync();
+                signal(&sm.g_ready);
+            }
+            if (c > 0 && !(ok = wait(&sm.s[st ^ 1], (c - 1) >> 1))) break;
+            fence_after_sync();
+#pragma unroll 1
+            for (int p = 0; p < NT; ++p) {
+                const int col = 32 * (NT * wg + p);
+                float s[32];
+                tmem_ld32(tl + kTS + col, s);
+                tmem_wait_ld();
+                if (c < nch) {
+                    uint32_t hi[16], lo[16];
+                    terms(s, hi, lo);
+                    tmem_st16(tl + kTSh + col / 2, hi);
+                    tmem_st16(tl + kTSl + col / 2, lo);
+                    const float whole = dec.gam[kC - 1];
+                    uint32_t next[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) next[i] = __float_as_uint(whole * s[i]);
+                    tmem_st32(tl + kTS + col, next);
+                    tmem_wait_st();
+                    fence_before_sync();
+                    signal(&sm.s_ready[p]);
+                    put_state_row<64 * NT>(a.ds1 + (bh * nch + nch - 1 - c) * 2 * a.headdim * (int64_t)a.dstate, a.headdim, r,
+                                           col, hi, lo);
+                } else if (a.dh0) {
+                    float *dst = a.dh0 + row * a.dstate + col;
+                    if (a.vec_state) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(dst + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) dst[i] = s[i];
+                    }
+                }
+            }
+            if (c == nch) break;
+            // z = W + w beta X, and z as an operand
+            if (!(ok = wait(&sm.x, c))) break;
+            fence_after_sync();
+            float z[32];
+            tmem_ld32(tl + kTX + 32 * wg, z);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 w4 = *reinterpret_cast<const float4 *>(&dec.wb[32 * wg + i]);
+                z[i] = fmaf(w4.x, z[i], wv[i]);
+                z[i + 1] = fmaf(w4.y, z[i + 1], wv[i + 1]);
+                z[i + 2] = fmaf(w4.z, z[i + 2], wv[i + 2]);
+                z[i + 3] = fmaf(w4.w, z[i + 3], wv[i + 3]);
+            }
+            put_terms(tl + kTX + 32 * wg, tl + kTX + 32 * wg + 16, z);
+            tmem_wait_st();
+            fence_before_sync();
+            signal(&sm.z_ready);
+            if (c + 1 < nch) put_grad(c + 1);
+            // dV = z - Y; -gam dV as an operand
+            if (!ok || !(ok = wait(&sm.y, c))) break;
+            fence_after_sync();
+            float y[32];
+            tmem_ld32(tl + kTY + 32 * wg, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 g4 = *reinterpret_cast<const float4 *>(&dec.gam[32 * wg + i]);
+                const float gg[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    z[i + e] -= y[i + e];
+                    y[i + e] = -gg[e] * z[i + e];
+                }
+            }
+            put_terms(tl + kTY + 32 * wg, tl + kTY + 32 * wg + 16, y);
+            tmem_wait_st();
+            fence_before_sync();
+            signal(&sm.v_ready);
+            uint32_t hi[16], lo[16];
+            terms(z, hi, lo);
+            store_tokens(sm.o[st][r >> 6] + 32 * wg * 128, vp, hi);
+            store_tokens(sm.lo[st][r >> 6] + 32 * wg * 128, vp, lo);
+            fence_proxy_async();
+            signal(&sm.o_ready[st]);
+        }
+    }
+    if (!ok && lane == 0) atomicOr(a.status, 4u);
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tm, 512);
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <int NT>
+cudaError_t launch_t(const DeltaBwdArgs &p, const DeltaChunkWs &ws, cudaStream_t st) {
+    const DeltaArgs &a = p.f;
+    CUtensorMap mq, mk, mo, mv, mt, mm;
+    const int64_t gn = (int64_t)a.groups * a.dstate, hp = (int64_t)a.heads * a.headdim;
+    const int64_t units2 = a.batch * a.heads * ((a.seqlen + kC - 1) / kC) * 2;
+    if (!encode_btw(&mq, a.q, a.batch, a.seqlen, gn, kC) || !encode_btw(&mk, a.k, a.batch, a.seqlen, gn, kC) ||
+        !encode_btw(&mo, p.dout, a.batch, a.seqlen, hp, kC) || !encode_btw(&mv, p.dv, a.batch, a.seqlen, hp, kC) ||
+        !encode_btw(&mt, ws.dv, units2, kC, a.headdim, kC) || !encode_btw(&mm, ws.mats, units2, 2 * kC, kC, 2 * kC))
+        return cudaErrorInvalidValue;
+    RevArgs f{};
+    f.dec = ws.dec; f.dend = p.dend; f.dh0 = p.dh0; f.ds1 = ws.ds1; f.scale = a.scale;
+    f.seqlen = a.seqlen; f.heads = a.heads; f.rep = a.heads / a.groups; f.headdim = a.headdim; f.dstate = a.dstate;
+    f.vec_state = aligned16(p.dend) && aligned16(p.dh0);
+    cudaError_t e = device_status_address(&f.status);
+    if (e != cudaSuccess) return e;
+    constexpr int bytes = (int)sizeof(RevSmem<NT>) + 1024;
+    static_assert(bytes <= 227 * 1024, "fits an SM");
+    e = allow_smem<delta_fused_reverse_kernel<NT>, bytes>();
+    if (e != cudaSuccess) return e;
+    delta_fused_reverse_kernel<NT><<<(unsigned)(a.batch * a.heads), kThreadsR, bytes, st>>>(mq, mk, mo, mv, mt, mm, f);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace delta
+
+bool delta_fused_reverse_eligible(const DeltaBwdArgs &p) {
+    return delta_fused_eligible(p.f) && p.f.headdim <= 128 && delta::aligned16(p.dout) && delta::aligned16(p.dv);
+}
+
+cudaError_t launch_delta_fused_reverse(const DeltaBwdArgs &p, const DeltaChunkWs &ws, cudaStream_t st) {
+    return p.f.dstate == 64 ? delta::launch_t<1>(p, ws, st) : delta::launch_t<2>(p, ws, st);
+}
+
+}  // namespace ssm
