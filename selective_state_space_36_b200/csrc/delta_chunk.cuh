@@ -198,6 +198,9 @@ cudaError_t launch_delta_fused_store(const DeltaArgs &a, const DeltaChunkWs &ws,
 // 128, dout and dv aligned too.
 bool delta_fused_reverse_eligible(const DeltaBwdArgs &a);
 cudaError_t launch_delta_fused_reverse(const DeltaBwdArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
+// dq, dk, dg and dbeta on tcgen05: that, and dq and dk aligned.
+bool delta_fused_grad_eligible(const DeltaBwdArgs &a);
+cudaError_t launch_delta_fused_grad(const DeltaBwdArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
 
 cudaError_t launch_delta_prep(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
 cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);

@@ -1,0 +1,582 @@
+// delta_fused_grad.cu -- the second half of the chunked gated delta rule's
+// gradient (formulas at delta_bwd.cu; delta_grad.cu does the same on mma.sync for
+// sizes that do not fit here) on the sm_100a tensor cores: dq, dk, dg and dbeta of
+// all chunks and heads, each a unit of its own.
+//
+// Products of a unit have tokens as rows, two sets of 64 in the 128 lanes of
+// tensor memory.  With rows of 64 one above the other in shared memory,
+//   dO, dV high, zeros, dV low, r high, r low,
+// windows of 128 rows give every sum of two-term products without a product of 64
+// rows:  (dO, dV high), (zeros, dV low), (dV low, r high), (r high, r low).
+//   [x; y]   = [dO; dV] r^T         (N = 64,     K = headdim)   scaled: X and E
+//   [dQ; L]  = [dO; dV] S0          (N = dstate, K = headdim)   scaled, then + [X; E] K
+//   [-; R]   = [-; r] dS1           (N = dstate, K = headdim)   scaled, then + X^T Q + E^T K
+// (the lanes of - hold what nothing reads).  The rows come 32 of headdim at a time,
+// with 32 rows of the states S0 and dS1, whose stored form -- groups of eight
+// columns, row after row -- is an operand as it stands; the next piece loads
+// while this one is multiplied.
+//
+// A block takes chunks in turn and sums dq and dk over a chunk's heads in
+// registers, in the order of the heads.
+// Warps: 0-7 row-wise work (two per lane quarter, each half of the columns), 8-11
+// <S0, dS1>, 12 issues the products, 13 the TMA copies, 14 the decays and the
+// sums dg and dbeta.  They meet at mbarriers only; every wait is bounded and
+// reports through the device status word.
+#include "delta_chunk.cuh"
+#include "delta_tc.cuh"
+#include "kernel_setup.cuh"
+#include "scan_kernels.cuh"
+#include "ssm_device.cuh"
+#include "tma_maps.cuh"
+
+namespace ssm {
+namespace delta {
+namespace {
+
+using namespace umma;
+
+constexpr int kRowWarps = 8, kDotWarps = 4;
+constexpr int kThreadsG = (kRowWarps + kDotWarps + 4) * 32;  // 12-14: products, copies, decays; one idle
+// Registers per thread: 128 at launch, then by group of four warps
+constexpr int kLaunchRegs = 128, kRowRegs = 184, kDotRegs = 72, kRestRegs = 72;
+static_assert(2 * kRowRegs + kDotRegs + kRestRegs <= 4 * kLaunchRegs, "no more than the block was launched with");
+constexpr int kPieceRows = 32;                      // of headdim
+constexpr uint32_t kPieceTile = kC * 2 * kPieceRows;  // 64 tokens x 32 values, 64-byte swizzle
+
+// tensor memory columns: [x; y], [Q; K] K^T, [dQ; L], [-; R]
+constexpr uint32_t kT1 = 0, kT5 = 64, kT2 = 128, kT4 = 256;
+enum : uint32_t { kRowO = 0, kRowDvHigh = 1, kRowZero = 2, kRowDvLow = 3, kRowRHigh = 4, kRowRLow = 5, kRowTiles = 6 };
+
+struct __align__(16) GradDec {                 // per head
+    float gam[kC], wend[kC], beta[kC];
+    float ch[kC], cl[kC];                      // G in units of ln 2 as two floats
+};
+
+template <int NT>
+struct GradTcSmem {
+    struct Piece {
+        unsigned char row[kRowTiles][kPieceTile];          // 64-byte swizzle
+        unsigned char s[4][8 * NT][kPieceRows * 16];       // S0 high, low, dS1 high, low
+    } piece[2];
+    unsigned char kq[2][NT][2 * kHalfTile];  // per chunk and 64 columns: Q rows, then K rows
+    unsigned char xe[2][2 * kHalfTile];      // [X; E]: high, low term
+    GradDec dec[2];
+    float dg[2][2][2 * kC];                  // per head: row sums of the two halves of dstate
+    float kr[2][2][kC];
+    float db[2][4][kC];                      // column sums of the four lane quarters
+    float inner[2][kDotWarps];               // <S0, dS1>
+    uint64_t ld[2], free[2];                 // a piece landed; is read
+    uint64_t ldkq[2], kq_taken[2];           // K and Q landed; are read
+    uint64_t cum[2], part[2];                // decays; a head's sums written
+    uint64_t acc, fin, all;                  // products complete
+    uint64_t a_ready, r_ready, taken;        // X, E, [dQ; L] scaled; R scaled; tensor memory is read
+    uint32_t tmem;
+};
+
+struct GradTcArgs {
+    const float *g, *dec;
+    bf16 *dq, *dk;
+    float *dg, *dbeta;
+    float scale;
+    int64_t seqlen;
+    int heads, groups, rep, headdim, dstate;
+    unsigned nch, chunks;  // chunks of a sequence, of all groups
+    unsigned int *status;
+};
+
+// The heads that a block goes through: chunks blockIdx.x, blockIdx.x + gridDim.x, ...,
+// each with its group's heads.
+struct Walk {
+    unsigned w, turn = 0;       // chunk; how many before it
+    int hh = 0;                 // head in the group
+    int64_t token, unit;        // the chunk's first token, counted over the batch; place in the workspace
+    int b, t0, gr, live;
+    __device__ __forceinline__ explicit Walk(const GradTcArgs &a) : w(blockIdx.x) { chunk(a); }
+    __device__ __forceinline__ void chunk(const GradTcArgs &a) {
+        const unsigned bg = w / a.nch, ch = w - bg * a.nch;
+        b = (int)(bg / (unsigned)a.groups);
+        gr = (int)(bg - (unsigned)b * (unsigned)a.groups);
+        t0 = (int)ch * kC;
+        token = b * a.seqlen + t0;
+        live = (int)(a.seqlen - t0 < kC ? a.seqlen - t0 : kC);
+        unit = ((int64_t)b * a.heads + gr * a.rep) * a.nch + ch;
+    }
+    __device__ __forceinline__ bool done(const GradTcArgs &a) const { return w >= a.chunks; }
+    __device__ __forceinline__ bool first() const { return hh == 0; }
+    __device__ __forceinline__ bool last(const GradTcArgs &a) const { return hh + 1 == a.rep; }
+    __device__ __forceinline__ int head(const GradTcArgs &a) const { return gr * a.rep + hh; }
+    __device__ __forceinline__ void next(const GradTcArgs &a) {
+        unit += a.nch;
+        if (++hh == a.rep) {
+            hh = 0;
+            ++turn;
+            w += gridDim.x;
+            if (w < a.chunks) chunk(a);
+        }
+    }
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kThreadsG, 1)
+delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                        const __grid_constant__ CUtensorMap mapO, const __grid_constant__ CUtensorMap mapV,
+                        const __grid_constant__ CUtensorMap mapR, const __grid_constant__ CUtensorMap mapS0,
+                        const __grid_constant__ CUtensorMap mapS1, const GradTcArgs a) {
+    extern __shared__ unsigned char raw[];
+    GradTcSmem<NT> &sm = *reinterpret_cast<GradTcSmem<NT> *>(raw + ((0u - smem_u32(raw)) & 1023u));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int pieces = a.headdim / kPieceRows;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.ld[i], 1);
+            mbar_init(&sm.free[i], 1 + kDotWarps);
+            mbar_init(&sm.ldkq[i], 1);
+            mbar_init(&sm.kq_taken[i], kRowWarps);
+            mbar_init(&sm.cum[i], 1);
+            mbar_init(&sm.part[i], kRowWarps + kDotWarps);
+        }
+        mbar_init(&sm.acc, 1);
+        mbar_init(&sm.fin, 1);
+        mbar_init(&sm.all, 1);
+        mbar_init(&sm.a_ready, kRowWarps);
+        mbar_init(&sm.r_ready, kRowWarps / 2);
+        mbar_init(&sm.taken, kRowWarps);
+        mbar_fence_init();
+    }
+    for (int i = tid; i < 2 * (int)kPieceTile / 16; i += kThreadsG)  // written here only
+        reinterpret_cast<uint4 *>(sm.piece[i / (kPieceTile / 16)].row[kRowZero])[i % (kPieceTile / 16)] =
+            make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
+    if (warp == 0) tmem_alloc(&sm.tmem, 512);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tm = sm.tmem;
+    auto wait = [&](uint64_t *bar, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait_2s(bar, par & 1u)) != 0; };
+    bool ok = true;  // false: a wait of this warp ran out
+    auto signal = [&](uint64_t *bar) {  // one arrival per warp, after the warp's reads and writes
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+
+    if (warp >= kRowWarps + kDotWarps) {
+        fewer_regs<kRestRegs>();
+        if (warp == kRowWarps + kDotWarps) {
+            // ------------------------------------------------ the products
+            const uint32_t el = elect_one();
+            constexpr uint32_t id_1 = idesc_bf16(128, 64, kMajorK, kMajorK);
+            constexpr uint32_t id_n = idesc_bf16(128, 64 * NT, kMajorK, kMajorMN);
+            constexpr uint32_t id_t = idesc_bf16(128, 64 * NT, kMajorMN, kMajorMN);
+            uint32_t piece = 0, j = 0;
+            for (Walk u(a); ok && !u.done(a); u.next(a), ++j) {
+                const int cs = u.turn & 1;
+                const uint32_t kq = smem_u32(sm.kq[cs][0]);
+                if (j > 0 && !(ok = wait(&sm.taken, j - 1))) break;
+                if (u.first()) {
+                    if (!(ok = wait(&sm.ldkq[cs], u.turn >> 1))) break;
+                    fence_after_sync();
+#pragma unroll
+                    for (int k = 0; k < 4 * NT; ++k) {
+                        const uint32_t at = kq + (k / 4) * 2 * kHalfTile + (k % 4) * 32;
+                        mma_bf16_if(el, tm + kT5, desc_sw128(at, 16, 1024), desc_sw128(at + kHalfTile, 16, 1024), id_1, k > 0);
+                    }
+                }
+                for (int i = 0; i < pieces; ++i, ++piece) {
+                    const int st = piece & 1;
+                    if (!(ok = wait(&sm.ld[st], piece >> 1))) break;
+                    fence_after_sync();
+                    const uint64_t rows = desc_tile(smem_u32(sm.piece[st].row[0]), 16, 512, kSwizzle64);
+                    const uint64_t states = desc_tile(smem_u32(sm.piece[st].s[0]), 128, kPieceRows * 16, kSwizzleNone);
+                    auto row = [&](uint32_t tile, int k) { return rows + ((tile * kPieceTile + k * 32) >> 4); };
+                    auto state = [&](int which, int k) { return states + ((which * 8 * NT * kPieceRows * 16 + k * 256) >> 4); };
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const bool more = i > 0 || k > 0;
+                        mma_bf16_if(el, tm + kT1, row(kRowO, k), row(kRowRHigh, k), id_1, more);
+                        mma_bf16_if(el, tm + kT2, row(kRowO, k), state(0, k), id_n, more);
+                        mma_bf16_if(el, tm + kT4, row(kRowDvLow, k), state(2, k), id_n, more);
+                        mma_bf16_if(el, tm + kT1, row(kRowO, k), row(kRowRLow, k), id_1, true);
+                        mma_bf16_if(el, tm + kT2, row(kRowO, k), state(1, k), id_n, true);
+                        mma_bf16_if(el, tm + kT4, row(kRowDvLow, k), state(3, k), id_n, true);
+                        mma_bf16_if(el, tm + kT1, row(kRowZero, k), row(kRowRHigh, k), id_1, true);
+                        mma_bf16_if(el, tm + kT2, row(kRowZero, k), state(0, k), id_n, true);
+                        mma_bf16_if(el, tm + kT4, row(kRowRHigh, k), state(2, k), id_n, true);
+                    }
+                    mma_commit_if(el, &sm.free[st]);
+                }
+                if (!ok) break;
+                mma_commit_if(el, &sm.acc);
+                // tiles with tokens as the summed index: 64 columns, the next 64 in the next tile
+                const uint64_t dq = desc_sw128(kq, 2 * kHalfTile, 1024), dk = dq + (kHalfTile >> 4);
+                if (!(ok = wait(&sm.a_ready, j))) break;
+                fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_bf16_if(el, tm + kT2, desc_sw128(smem_u32(sm.xe[k >> 2]) + (k & 3) * 32, 16, 1024),
+                                dk + (((k & 3) * 2048) >> 4), id_n, true);
+                if (!(ok = wait(&sm.r_ready, j))) break;
+                fence_after_sync();
+                // X^T and E^T in the upper 64 lanes: the tile before theirs in memory has the lower ones
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int tile = k >> 2;  // X high, E high, X low, E low
+                    mma_bf16_if(el, tm + kT4,
+                                desc_sw128(smem_u32(sm.xe[0]) + tile * kHalfTile - kHalfTile + (k & 3) * 2048, kHalfTile, 1024),
+                                ((tile & 1) ? dk : dq) + (((k & 3) * 2048) >> 4), id_t, true);
+                }
+                mma_commit_if(el, &sm.fin);
+            }
+            mma_commit_if(el, &sm.all);  // whatever was issued completes before tensor memory goes away
+            (void)mbar_wait_2s(&sm.all, 0u);
+            __syncwarp();
+        } else if (warp == kRowWarps + kDotWarps + 1) {
+            // -------------------------------------------------- the copies
+            const uint32_t el = elect_one();
+            uint32_t piece = 0, kqs = 0;
+            for (Walk u(a); ok && !u.done(a); u.next(a)) {
+                if (u.first()) {
+                    const int cs = u.turn & 1;
+                    if (u.turn >= 2 && !(ok = wait(&sm.kq_taken[cs], (u.turn - 2) >> 1))) break;
+                    if (el) {
+                        mbar_expect_tx(&sm.ldkq[cs], (uint32_t)(2 * NT) * kHalfTile);
+#pragma unroll 1
+                        for (int i = 0; i < NT; ++i) {
+                            tma_load_3d(sm.kq[cs][i], &mapQ, u.gr * a.dstate + 64 * i, u.t0, u.b, &sm.ldkq[cs]);
+                            tma_load_3d(sm.kq[cs][i] + kHalfTile, &mapK, u.gr * a.dstate + 64 * i, u.t0, u.b, &sm.ldkq[cs]);
+                        }
+                    }
+                    ++kqs;
+                }
+                for (int i = 0; i < pieces; ++i, ++piece) {
+                    const int st = piece & 1;
+                    if (piece >= 2 && !(ok = wait(&sm.free[st], (piece - 2) >> 1))) break;
+                    if (el) {
+                        auto &to = sm.piece[st];
+                        uint64_t *bar = &sm.ld[st];
+                        const int32_t unit2 = (int32_t)(2 * u.unit), x = kPieceRows * i;
+                        mbar_expect_tx(bar, 5 * kPieceTile + (uint32_t)sizeof(to.s));
+                        tma_load_3d(to.row[kRowO], &mapO, u.head(a) * a.headdim + x, u.t0, u.b, bar);
+                        tma_load_3d(to.row[kRowDvHigh], &mapV, x, 0, unit2, bar);
+                        tma_load_3d(to.row[kRowDvLow], &mapV, x, 0, unit2 + 1, bar);
+                        tma_load_3d(to.row[kRowRHigh], &mapR, x, 0, unit2, bar);
+                        tma_load_3d(to.row[kRowRLow], &mapR, x, 0, unit2 + 1, bar);
+#pragma unroll 1
+                        for (int term = 0; term < 2; ++term) {
+                            tma_load_3d(to.s[term], &mapS0, 8 * x, 0, unit2 + term, bar);
+                            tma_load_3d(to.s[2 + term], &mapS1, 8 * x, 0, unit2 + term, bar);
+                        }
+                    }
+                }
+            }
+            for (uint32_t i = 0; i < 2; ++i) {  // no copy outlives the block
+                if (piece > i) (void)mbar_wait_2s(&sm.ld[(piece - 1 - i) & 1], ((piece - 1 - i) >> 1) & 1u);
+                if (kqs > i) (void)mbar_wait_2s(&sm.ldkq[(kqs - 1 - i) & 1], ((kqs - 1 - i) >> 1) & 1u);
+            }
+            __syncwarp();
+        } else if (warp == kRowWarps + kDotWarps + 2) {
+            // ------------------------------- the decays; a head's sums dg and dbeta
+            auto decays = [&](const Walk &u, uint32_t turn) {
+                GradDec &dec = sm.dec[turn & 1];
+                const float *g = a.g + u.token * a.heads + u.head(a), *d = a.dec + u.unit * (kDec * kC) + 2 * lane;
+                const int t = 2 * lane;
+                const float g0 = t < u.live ? __ldg(g + (int64_t)t * a.heads) : 0.f;
+                const float g1 = t + 1 < u.live ? __ldg(g + (int64_t)(t + 1) * a.heads) : 0.f;
+                const float2 ga = *reinterpret_cast<const float2 *>(d), we = *reinterpret_cast<const float2 *>(d + kC),
+                             be = *reinterpret_cast<const float2 *>(d + 2 * kC);
+                constexpr double kLog2 = 1.4426950408889634;
+                const double d0 = kLog2 * fmax((double)g0, -1e4), d1 = kLog2 * fmax((double)g1, -1e4);
+                double sum = d0 + d1;
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double up = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += up;
+                }
+                const double c0 = sum - d1;
+                *reinterpret_cast<float2 *>(&dec.ch[t]) = make_float2((float)c0, (float)sum);
+                *reinterpret_cast<float2 *>(&dec.cl[t]) = make_float2((float)(c0 - (double)(float)c0), (float)(sum - (double)(float)sum));
+                *reinterpret_cast<float2 *>(&dec.gam[t]) = ga;
+                *reinterpret_cast<float2 *>(&dec.wend[t]) = we;
+                *reinterpret_cast<float2 *>(&dec.beta[t]) = be;
+                signal(&sm.cum[turn & 1]);
+            };
+            Walk ahead(a);  // two heads ahead
+            uint32_t j = 0;
+            for (uint32_t i = 0; i < 2 && !ahead.done(a); ++i, ahead.next(a)) decays(ahead, i);
+            for (Walk u(a); ok && !u.done(a); u.next(a), ++j) {
+                const int s = j & 1;
+                if (!(ok = wait(&sm.part[s], j >> 1))) break;
+                const GradDec &dec = sm.dec[s];
+                // lane i: tokens 63 - 2 i and 62 - 2 i; a prefix sum over lanes is a sum from the end
+                const int t1 = kC - 1 - 2 * lane;
+                float v[2], db[2], whole = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = t1 - i;
+                    v[i] = (sm.dg[s][0][t] + sm.dg[s][1][t]) + (sm.dg[s][0][kC + t] + sm.dg[s][1][kC + t]);
+                    const float wkr = dec.wend[t] * (sm.kr[s][0][t] + sm.kr[s][1][t]);
+                    db[i] = (sm.db[s][0][t] + sm.db[s][1][t]) + (sm.db[s][2][t] + sm.db[s][3][t]) + wkr;
+                    whole = fmaf(dec.beta[t], wkr, whole);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, o);
+                whole = fmaf(dec.gam[kC - 1], (sm.inner[s][0] + sm.inner[s][1]) + (sm.inner[s][2] + sm.inner[s][3]), whole);
+                float sum = v[0] + v[1];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float up = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += up;
+                }
+                const int64_t at = u.token * a.heads + u.head(a);
+                if (t1 < u.live) {
+                    a.dg[at + (int64_t)t1 * a.heads] = whole + (sum - v[1]);
+                    a.dbeta[at + (int64_t)t1 * a.heads] = db[0];
+                }
+                if (t1 - 1 < u.live) {
+                    a.dg[at + (int64_t)(t1 - 1) * a.heads] = whole + sum;
+                    a.dbeta[at + (int64_t)(t1 - 1) * a.heads] = db[1];
+                }
+                __syncwarp();  // all lanes have read the head's sums and decays
+                if (!ahead.done(a)) {
+                    decays(ahead, j + 2);
+                    ahead.next(a);
+                }
+            }
+        }
+    } else if (warp >= kRowWarps) {
+        // ----------------------------------------------------- <S0, dS1>
+        fewer_regs<kDotRegs>();
+        const int at = tid - kRowWarps * 32;
+        uint32_t piece = 0, j = 0;
+        for (Walk u(a); ok && !u.done(a); u.next(a), ++j) {
+            float inner = 0.f;
+            for (int i = 0; i < pieces; ++i, ++piece) {
+                const int st = piece & 1;
+                if (!(ok = wait(&sm.ld[st], piece >> 1))) break;
+                constexpr int kVecs = 8 * NT * kPieceRows;  // 16 bytes each
+                const uint4 *s0 = reinterpret_cast<const uint4 *>(sm.piece[st].s[0]);
+#pragma unroll 2
+                for (int v = at; v < kVecs; v += kDotWarps * 32) {
+                    const uint4 x0 = s0[v], x1 = s0[kVecs + v], x2 = s0[2 * kVecs + v], x3 = s0[3 * kVecs + v];
+                    const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+                    const uint32_t w2[4] = {x2.x, x2.y, x2.z, x2.w}, w3[4] = {x3.x, x3.y, x3.z, x3.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        inner = fmaf(low_of(w0[e]) + low_of(w1[e]), low_of(w2[e]) + low_of(w3[e]), inner);
+                        inner = fmaf(high_of(w0[e]) + high_of(w1[e]), high_of(w2[e]) + high_of(w3[e]), inner);
+                    }
+                }
+                signal(&sm.free[st]);
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
+            if (!(ok = wait(&sm.cum[j & 1], j >> 1))) break;  // the sums of head j - 2 are read
+            if (lane == 0) sm.inner[j & 1][warp - kRowWarps] = inner;
+            signal(&sm.part[j & 1]);
+        }
+    } else {
+        // --------------------------------------------- the row-wise work
+        more_regs<kRowRegs>();
+        const int quad = warp & 3, wg = warp >> 2, r = 32 * quad + lane, t = r & (kC - 1);
+        const int lower = quad >= 2;  // this lane has a row of y, L and R, not of x and dQ
+        const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
+        float sum[NT][32];  // dq or dk over the group's heads
+        uint32_t j = 0;
+        for (Walk u(a); !u.done(a); u.next(a), ++j) {
+            const int s = j & 1, cs = u.turn & 1;
+            const GradDec &dec = sm.dec[s];
+            if (u.first())
+#pragma unroll
+                for (int p = 0; p < NT; ++p)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[p][i] = 0.f;
+            if (!(ok = wait(&sm.cum[s], j >> 1)) || !(ok = wait(&sm.ldkq[cs], u.turn >> 1)) || !(ok = wait(&sm.acc, j))) break;
+            fence_after_sync();
+            // x = scale Gam (dO r^T) for s <= t, y = -Gam (dV r^T) for s < t; times beta_s
+            // they are X and E; times q_t . k_s or k_t . k_s, summed over t, dbeta's terms
+            float x[32], qk[32];
+            tmem_ld32(tl + kT1 + 32 * wg, x);
+            tmem_ld32(tl + kT5 + 32 * wg, qk);
+            tmem_wait_ld();
+            {
+                const float f = lower ? -1.f : a.scale, th = dec.ch[t], tw = dec.cl[t];
+                const int last = t - lower - 32 * wg;  // column, counted from this warp's first
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 h4 = *reinterpret_cast<const float4 *>(&dec.ch[32 * wg + i]);
+                    const float4 l4 = *reinterpret_cast<const float4 *>(&dec.cl[32 * wg + i]);
+                    const float4 b4 = *reinterpret_cast<const float4 *>(&dec.beta[32 * wg + i]);
+                    const float hh[4] = {h4.x, h4.y, h4.z, h4.w}, ll[4] = {l4.x, l4.y, l4.z, l4.w};
+                    const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = i + e <= last ? f * ex2_approx((th - hh[e]) + (tw - ll[e])) * x[i + e] : 0.f;
+                        qk[i + e] = i + e <= last ? v * qk[i + e] : 0.f;
+                        x[i + e] = v * bb[e];
+                    }
+                }
+                uint32_t hi[16], lo[16];
+                terms(x, hi, lo);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const uint32_t at = sw128_offset(r, 4 * wg + p);
+                    *reinterpret_cast<uint4 *>(sm.xe[0] + at) = make_uint4(hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
+                    *reinterpret_cast<uint4 *>(sm.xe[1] + at) = make_uint4(lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
+                }
+                fence_proxy_async();
+            }
+            const float gam = dec.gam[t], f2 = lower ? -gam : a.scale * gam;
+#pragma unroll 1
+            for (int p = 0; p < NT; ++p) {
+                const uint32_t at = tl + kT2 + 32 * (NT * wg + p);
+                tmem_ld32(at, x);
+                tmem_wait_ld();
+                uint32_t y[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(f2 * x[i]);
+                tmem_st32(at, y);
+            }
+            tmem_wait_st();
+            fence_before_sync();
+            signal(&sm.a_ready);
+            // row r of [Q; K]
+            auto row_of = [&](int col, int p) {
+                return *reinterpret_cast<const uint4 *>(sm.kq[cs][col >> 6] + sw128_offset(r, ((col & 63) >> 3) + p));
+            };
+            auto dot = [&](const float (&v)[32], int col) {
+                float d[2] = {0.f, 0.f};
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const uint4 q4 = row_of(col, p);
+                    const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        d[0] = fmaf(low_of(q[e]), v[8 * p + 2 * e], d[0]);
+                        d[1] = fmaf(high_of(q[e]), v[8 * p + 2 * e + 1], d[1]);
+                    }
+                }
+                return d[0] + d[1];
+            };
+            if (lower) {
+                const float fr = dec.wend[t] * dec.beta[t];
+                float kr = 0.f;
+#pragma unroll 1
+                for (int p = 0; p < NT; ++p) {
+                    const int col = 32 * (NT * wg + p);
+                    tmem_ld32(tl + kT4 + col, x);
+                    tmem_wait_ld();
+                    kr += dot(x, col);
+                    uint32_t y[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(fr * x[i]);
+                    tmem_st32(tl + kT4 + col, y);
+                }
+                tmem_wait_st();
+                fence_before_sync();
+                signal(&sm.r_ready);
+                sm.kr[s][wg][t] = kr;
+            }
+            // column sums over the warp's 32 lanes: a lane ends with its own column's
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < o; ++i) {
+                    const bool up = (lane & o) != 0;
+                    const float keep = up ? qk[i + o] : qk[i], send = up ? qk[i] : qk[i + o];
+                    qk[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                }
+            sm.db[s][quad][32 * wg + lane] = qk[0];
+            // dQ, or L and R, of this head
+            if (!(ok = wait(&sm.fin, j))) break;
+            fence_after_sync();
+            float d = 0.f;
+#pragma unroll
+            for (int p = 0; p < NT; ++p) {
+                const int col = 32 * (NT * wg + p);
+                tmem_ld32(tl + kT2 + col, x);
+                if (lower) tmem_ld32(tl + kT4 + col, qk);
+                tmem_wait_ld();
+                if (lower) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        sum[p][i] += x[i] + qk[i];
+                        x[i] -= qk[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[p][i] += x[i];
+                }
+                d += dot(x, col);
+            }
+            sm.dg[s][wg][r] = d;
+            fence_before_sync();
+            signal(&sm.part[s]);
+            signal(&sm.taken);
+            if (u.last(a)) {
+                signal(&sm.kq_taken[cs]);
+                if (t < u.live) {
+                    bf16 *dst = (lower ? a.dk : a.dq) + ((u.token + t) * a.groups + u.gr) * a.dstate + 32 * NT * wg;
+#pragma unroll
+                    for (int p = 0; p < NT; ++p)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            *reinterpret_cast<uint4 *>(dst + 32 * p + i) =
+                                make_uint4(pack(sum[p][i], sum[p][i + 1]), pack(sum[p][i + 2], sum[p][i + 3]),
+                                           pack(sum[p][i + 4], sum[p][i + 5]), pack(sum[p][i + 6], sum[p][i + 7]));
+                }
+            }
+        }
+    }
+    if (!ok && lane == 0) atomicOr(a.status, 4u);
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tm, 512);
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <int NT>
+cudaError_t launch_t(const DeltaBwdArgs &p, const DeltaChunkWs &ws, int sms, cudaStream_t st) {
+    const DeltaArgs &a = p.f;
+    CUtensorMap mq, mk, mo, mv, mr, m0, m1;
+    const int64_t gn = (int64_t)a.groups * a.dstate, hp = (int64_t)a.heads * a.headdim;
+    const int64_t nch = (a.seqlen + kC - 1) / kC, units2 = a.batch * a.heads * nch * 2;
+    const int64_t state[3] = {a.headdim * 8, 8 * NT, units2};  // groups of eight columns, row after row
+    constexpr auto sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!encode_btw(&mq, a.q, a.batch, a.seqlen, gn, kC) || !encode_btw(&mk, a.k, a.batch, a.seqlen, gn, kC) ||
+        !encode_bf16(&mo, p.dout, {hp, a.seqlen, a.batch}, {kPieceRows, kC, 1}, sw64) ||
+        !encode_bf16(&mv, ws.dv, {a.headdim, kC, units2}, {kPieceRows, kC, 1}, sw64) ||
+        !encode_bf16(&mr, ws.r, {a.headdim, kC, units2}, {kPieceRows, kC, 1}, sw64) ||
+        !encode_bf16(&m0, ws.s0, state, {kPieceRows * 8, 8 * NT, 1}, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_bf16(&m1, ws.ds1, state, {kPieceRows * 8, 8 * NT, 1}, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    GradTcArgs f{};
+    f.g = a.g; f.dec = ws.dec; f.scale = a.scale;
+    f.dq = static_cast<bf16 *>(p.dq); f.dk = static_cast<bf16 *>(p.dk); f.dg = p.dg; f.dbeta = p.dbeta;
+    f.seqlen = a.seqlen; f.heads = a.heads; f.groups = a.groups; f.rep = a.heads / a.groups;
+    f.headdim = a.headdim; f.dstate = a.dstate;
+    f.nch = (unsigned)nch;
+    f.chunks = (unsigned)(a.batch * a.groups * nch);
+    cudaError_t e = device_status_address(&f.status);
+    if (e != cudaSuccess) return e;
+    constexpr int bytes = (int)sizeof(GradTcSmem<NT>) + 1024;
+    static_assert(bytes <= 227 * 1024, "fits an SM");
+    e = allow_smem<delta_fused_grad_kernel<NT>, bytes>();
+    if (e != cudaSuccess) return e;
+    const unsigned blocks = f.chunks < (unsigned)sms ? f.chunks : (unsigned)sms;
+    delta_fused_grad_kernel<NT><<<blocks, kThreadsG, bytes, st>>>(mq, mk, mo, mv, mr, m0, m1, f);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace delta
+
+bool delta_fused_grad_eligible(const DeltaBwdArgs &p) {
+    return delta_fused_reverse_eligible(p) && delta::aligned16(p.dq) && delta::aligned16(p.dk);
+}
+
+cudaError_t launch_delta_fused_grad(const DeltaBwdArgs &p, const DeltaChunkWs &ws, int sms, cudaStream_t st) {
+    return p.f.dstate == 64 ? delta::launch_t<1>(p, ws, sms, st) : delta::launch_t<2>(p, ws, sms, st);
+}
+
+}  // namespace ssm

@@ -1040,7 +1040,9 @@ ssm_status ssm_delta_rule_bwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, co
         if (e == cudaSuccess)
             e = ssm::delta_fused_reverse_eligible(p) ? ssm::launch_delta_fused_reverse(p, ws, st)
                                                      : ssm::launch_delta_reverse(p, ws, sms, st);
-        if (e == cudaSuccess) e = ssm::launch_delta_grad(p, ws, sms, st);
+        if (e == cudaSuccess)
+            e = ssm::delta_fused_grad_eligible(p) ? ssm::launch_delta_fused_grad(p, ws, sms, st)
+                                                  : ssm::launch_delta_grad(p, ws, sms, st);
     } else {
         const size_t marks = (size_t)units * dims.headdim * dims.dstate, r = (size_t)tokens * dims.heads * dims.headdim;
         const size_t per_head = (size_t)tokens * dims.heads * dims.dstate;

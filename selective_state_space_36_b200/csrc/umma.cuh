@@ -33,17 +33,21 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
 // ------------------------------------------------------------- descriptors
 enum : uint32_t { kMajorK = 0, kMajorMN = 1 };
 
-// Shared-memory matrix descriptor (sm_100 format, version 1) of a 128-byte
-// swizzled tile starting at byte address `addr` (1024-byte aligned atom base
-// plus an in-row offset for K steps of K-major operands).
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+// Shared-memory matrix descriptor (sm_100 format, version 1) of a tile starting
+// at byte address `addr` (the swizzle pattern's start plus an in-row offset for K
+// steps of K-major operands).
+enum : uint32_t { kSwizzleNone = 0, kSwizzle128 = 2, kSwizzle64 = 4 };
+__device__ __forceinline__ uint64_t desc_tile(uint32_t addr, uint32_t lbo_bytes, uint32_t sbo_bytes, uint32_t layout) {
     uint64_t d = 0;
     d |= (uint64_t)((addr >> 4) & 0x3FFFu);
     d |= (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16;
     d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
     d |= (uint64_t)1 << 46;  // descriptor version for sm_100
-    d |= (uint64_t)2 << 61;  // layout: 128-byte swizzle
+    d |= (uint64_t)layout << 61;
     return d;
+}
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+    return desc_tile(addr, lbo_bytes, sbo_bytes, kSwizzle128);
 }
 
 // Instruction descriptor of kind::f16: bf16 A and B, fp32 accumulator,
