@@ -386,6 +386,15 @@ ssm_status ssm_ssd_scan_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *x, cons
  * 1 <= dstate <= 128 (SSM_ERR_UNSUPPORTED above); any headdim, heads a
  * multiple of groups.  A token with beta = 0 and g = 0 leaves the state as it
  * is, so rows of a padded batch end with the state of their last token.
+ *
+ * float32 tensors, and up to 32 tokens, go token by token in float32 without a
+ * workspace.  bf16 sequences go in chunks of 64 tokens on the tensor cores, as
+ * one kernel where dstate is 64 or 128, headdim a multiple of 64 and q, k, v and
+ * out start 16-byte aligned (its bounded waits: bit 2 of the device status word).
+ * With few heads the sequence is split into segments that run side by side;
+ * workspace then, per head and segment, dstate (2 headdim + dstate) floats.
+ * Other bf16 sequences take 33 KB of workspace per head and chunk.  The workspace
+ * comes from the library's pool on "stream" (see ssm_selective_scan_fwd).
  */
 ssm_status ssm_delta_rule_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, const void *k, const void *v,
                               const float *g, const float *beta, float scale, void *out, float *last_state,
@@ -401,7 +410,7 @@ ssm_status ssm_delta_rule_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, co
  *   dv        : (batch, seqlen, heads, headdim) io
  *   dg, dbeta : (batch, seqlen, heads) float32
  *   dh0       : (batch, heads, headdim, dstate) float32 or NULL (not computed).
- * headdim <= 128 here.  No atomics: equal inputs give equal bits.  The states
+ * headdim <= 128 here (SSM_ERR_UNSUPPORTED above).  No atomics: equal inputs give equal bits.  The states
  * are recomputed: the workspace holds, per head and chunk of 64 tokens, two
  * states and two (64, headdim) arrays at 4 bytes per value and 33 KB besides
  * (float32 tensors: a state per 16 tokens, and per token and head headdim +
@@ -464,8 +473,9 @@ ssm_status ssm_norm_bwd(int64_t rows, int64_t dim, ssm_dtype io, int mode, const
  * synchronising "stream".  Bit 0: a bounded wait inside the decode kernel
  * (its state copies, see ssm_selective_state_update) gave up; the outputs of
  * the launches since the last read are then not valid.  Bit 1: a bounded
- * wait inside the SSD kernel (ssm_ssd_scan_fwd) gave up.  The word is shared by
- * every launch on the device.  Returns SSM_ERR_CUDA if the copies or the
+ * wait inside the SSD kernel (ssm_ssd_scan_fwd) gave up.  Bit 2: one inside the
+ * gated delta rule's tensor-core kernels (ssm_delta_rule_fwd, _bwd) did.  The word
+ * is shared by every launch on the device.  Returns SSM_ERR_CUDA if the copies or the
  * synchronisation fail.
  */
 ssm_status ssm_get_device_status(ssm_stream stream, uint32_t *flags);

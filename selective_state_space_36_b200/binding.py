@@ -548,7 +548,8 @@ def scan_plan(batch: int, seqlen: int, dim: int, dstate: int, io: str = "bf16",
 
 def device_status(stream=None) -> int:
     """Synchronises ``stream`` and returns (and clears) the device status word:
-    bit 0 = a bounded wait in the decode kernel gave up."""
+    bit 0 = a bounded wait in the decode kernel gave up, bit 1 = one in the SSD
+    kernel, bit 2 = one in the gated delta rule's tensor-core kernels."""
     v = ctypes.c_uint32(0)
     check(lib.ssm_get_device_status(_stream_handle(stream), ctypes.byref(v)))
     return int(v.value)

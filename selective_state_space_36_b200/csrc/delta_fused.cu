@@ -281,16 +281,13 @@ __device__ __forceinline__ void chunk_matrices(FusedSmem<NT> &sm, int c, int w, 
 }
 
 // ------------------------------------------------------------- row-wise work
-// 32 columns of the state: its two terms, and gam_C of the next chunk times it
-// where the next chunk's product accumulates.  `copy`: a stored state of pp rows
-// that row `row` goes to as well.
-template <int NP>
-__device__ __forceinline__ void put_state(uint32_t tl, int col, const float (&s)[32], float whole, bf16 *copy, int pp, int row) {
-    uint32_t hi[16], lo[16];
+// 32 columns of the state: its two terms (hi, lo) as operands, and gam_C of the
+// next chunk times it where the next chunk's product accumulates.
+__device__ __forceinline__ void put_state(uint32_t tl, int col, const float (&s)[32], float whole, uint32_t (&hi)[16],
+                                          uint32_t (&lo)[16]) {
     terms(s, hi, lo);
     tmem_st16(tl + kTSh + col / 2, hi);
     tmem_st16(tl + kTSl + col / 2, lo);
-    if (copy) put_state_row<NP>(copy, pp, row, col, hi, lo);
     uint32_t r[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(whole * s[i]);
@@ -698,12 +695,14 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                 tmem_ld32(tl + kTS + col, s);
                 tmem_wait_ld();
                 if (c < nch) {
-                    put_state<64 * NT>(tl, col, s, dec.whole,
-                                       STORE ? a.s0 + (bh * all_chunks + c) * 2 * a.headdim * (int64_t)a.dstate : nullptr,
-                                       a.headdim, v0 + r);
+                    uint32_t hi[16], lo[16];
+                    put_state(tl, col, s, dec.whole, hi, lo);
                     tmem_wait_st();
                     fence_before_sync();
                     signal(&sm.s_ready[p]);
+                    if constexpr (STORE)
+                        put_state_row<64 * NT>(a.s0 + (bh * all_chunks + c) * 2 * a.headdim * (int64_t)a.dstate, a.headdim,
+                                               v0 + r, col, hi, lo);
                 } else if (to) {
                     float *dst = to + col;
                     if (a.vec_state) {

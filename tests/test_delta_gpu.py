@@ -364,6 +364,139 @@ def test_two_streams_and_a_captured_graph(lib):
             assert torch.equal(o, ro) and torch.equal(st, rs)
 
 
+@gpu
+@pytest.mark.parametrize("batch,seqlen,heads,groups,headdim,dstate", [
+    (3, 1093, 9, 3, 64, 64),      # more chunks of groups than SMs: blocks go through several, three heads each
+    (2, 1200, 10, 5, 128, 128),
+    (1, 70, 6, 1, 64, 128),       # six heads share q and k
+    (4, 64, 2, 2, 128, 64),       # one chunk a sequence
+])
+def test_gradients_of_many_units(lib, batch, seqlen, heads, groups, headdim, dstate):
+    x = R.delta_inputs(batch, seqlen, heads, groups, headdim, dstate, "bf16", 31)
+    d = dev(x)
+    got = lib.delta_rule_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["dout"], scale=0.2, h0=d["h0"],
+                             dlast_state=d["dend"])
+    ref = R.delta_grads(x, 0.2)
+    sizes = dg_sizes(x, 0.2)
+    for n in ("q", "k", "v", "g", "beta"):
+        near(got["d" + n], ref[n], "d" + n, 2, sizes if n == "g" else None)
+    near(got["dh0"], ref["h0"], "dh0", 1)
+    assert lib.device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("headdim,dstate", [(64, 64), (128, 128)])
+def test_gradients_at_limits_on_tensor_cores(lib, headdim, dstate):
+    """As test_gradients_at_limits, at sizes that the tcgen05 kernels take."""
+    x = R.delta_inputs(2, 200, 4, 2, headdim, dstate, "bf16", 37)
+    x["beta"][0, 3::5] = 0
+    x["beta"][1, 70:] = 0
+    x["g"][1, 70:] = 0          # padding
+    x["g"][0, 50] = -200.0      # exp is zero in float32
+    x["g"][0, 63] = -1e5
+    x["g"][0, 130] = -float("inf")
+    for h0, dend in ((True, False), (False, True)):
+        y = {**x, "h0": x["h0"] if h0 else None, "dend": x["dend"] if dend else None}
+        d = dev(y)
+        got = lib.delta_rule_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["dout"], scale=0.2, h0=d["h0"],
+                                 dlast_state=d["dend"], want_dh0=True)
+        finite = {**y, "g": y["g"].clamp_min(-1e5), "h0": x["h0"] if h0 else torch.zeros_like(x["h0"])}
+        ref = R.delta_grads(finite, 0.2)
+        for n in ("q", "k", "v", "g", "beta"):
+            near(got["d" + n], ref[n], "d" + n, 2, dg_sizes({**finite, "h0": y["h0"]}, 0.2) if n == "g" else None)
+        near(got["dh0"], ref["h0"], "dh0", 1)
+
+
+@gpu
+@pytest.mark.parametrize("moved", ["q", "v", "dout", "dq", "dv", "dend", "dh0"])
+def test_gradients_with_one_unaligned_tensor(lib, moved):
+    """Each tensor that a step of the gradient wants aligned, alone off the
+    alignment: the steps before and after it still fit together; and nothing
+    beside the outputs is written."""
+    batch, seqlen, heads, groups, P, N = 2, 150, 4, 2, 64, 128
+    x = R.delta_inputs(batch, seqlen, heads, groups, P, N, "bf16", 41)
+    shapes = {"dq": x["q"], "dk": x["k"], "dv": x["v"], "dg": x["g"], "dbeta": x["beta"], "dh0": x["h0"]}
+    names = ("q", "k", "v", "g", "beta", "scale", "h0", "dout", "dend", "dq", "dk", "dv", "dg", "dbeta", "dh0")
+
+    def call(which):
+        rooms, view = {}, {}
+        for n in names:
+            if n == "scale":
+                continue
+            src = shapes.get(n, x.get(n))
+            lead = 64 + (1 if n == which else 0)
+            room = torch.full((src.numel() + 128 + 1,), 7.0, dtype=src.dtype, device="cuda")
+            rooms[n], view[n] = (room, lead), room[lead:lead + src.numel()].view(src.shape)
+            if n in x:
+                view[n].copy_(x[n])
+        ptr = [0.2 if n == "scale" else view[n].data_ptr() for n in names]
+        lib.check(lib.lib.ssm_delta_rule_bwd(lib.SSMSsdDims(batch, seqlen, heads, P, groups, N), lib.SSM_BF16, *ptr,
+                                             torch.cuda.current_stream().cuda_stream))
+        torch.cuda.synchronize()
+        for n, (room, lead) in rooms.items():
+            size = view[n].numel()
+            assert (room[:lead] == 7).all() and (room[lead + size:] == 7).all(), n
+        return {n: view[n].clone() for n in shapes}
+
+    ref, got = call(None), call(moved)
+    for n in shapes:
+        near(got[n], ref[n].cpu(), n, 1 if n == "dh0" else 2, dg_sizes(x, 0.2) if n == "dg" else None)
+
+
+@gpu
+def test_split_sequence_in_a_graph_and_in_place(lib):
+    """Few heads and many tokens (segments side by side, a workspace), captured:
+    each replay goes on from the state that the last one left."""
+    x = R.delta_inputs(1, 1600, 2, 1, 64, 128, "bf16", 43, "slow")
+    d = dev(x)
+    call = lambda st: lib.delta_rule_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], scale=0.1, last_state=st)
+    st, outs, ends = d["h0"].clone(), [], []
+    for _ in range(3):
+        outs.append(call(st))
+        ends.append(st.clone())
+    held = d["h0"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(held)
+    held.copy_(d["h0"])
+    for o, e in zip(outs, ends):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, o) and torch.equal(held, e)
+    assert lib.device_status() == 0
+
+
+@gpu
+def test_explicit_stream_and_errors_of_both_marshallings(lib):
+    """Calls with a stream go through ctypes, calls without through the native
+    module: the same results, the same refusals."""
+    x = R.delta_inputs(2, 70, 4, 2, 64, 64, "bf16", 47)
+    d = dev(x)
+    five = [d[n] for n in ("q", "k", "v", "g", "beta")]
+    s = torch.cuda.current_stream()
+    assert torch.equal(lib.delta_rule_fwd(*five), lib.delta_rule_fwd(*five, stream=s))
+    a, b = (lib.delta_rule_bwd(*five, d["dout"], h0=d["h0"], **kw) for kw in ({}, {"stream": s}))
+    assert all(torch.equal(a[n], b[n]) for n in a)
+    one = [t[:, 0].contiguous() for t in five]
+    sa, sb = d["h0"].clone(), d["h0"].clone()
+    assert torch.equal(lib.delta_rule_update(sa, *one), lib.delta_rule_update(sb, *one, stream=s))
+    assert torch.equal(sa, sb)
+    bad = [
+        ({"q": d["q"].transpose(1, 2)}, ValueError), ({"k": d["k"].float()}, TypeError),
+        ({"g": d["g"].bfloat16()}, TypeError), ({"beta": d["beta"][:, :5]}, ValueError),
+        ({"v": d["v"].half()}, TypeError), ({"q": d["q"].cpu()}, ValueError),
+        ({"v": d["v"][:, :, :3].contiguous(), "g": d["g"][:, :, :3].contiguous(),
+          "beta": d["beta"][:, :, :3].contiguous()}, lib.SSMError),
+    ]
+    for change, error in bad:
+        y = [change.get(n, d[n]) for n in ("q", "k", "v", "g", "beta")]
+        for kw in ({}, {"stream": s}):
+            with pytest.raises(error):
+                lib.delta_rule_fwd(*y, **kw)
+            with pytest.raises(error):
+                lib.delta_rule_bwd(*y, change.get("v", d["dout"]), **kw)
+
+
 def test_empty_and_refused(request):
     """Host-side checks (no GPU): empty sizes are no-ops, bad arguments are named."""
     from selective_state_space_36_b200 import binding as b
