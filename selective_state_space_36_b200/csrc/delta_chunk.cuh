@@ -89,29 +89,6 @@ __device__ __forceinline__ int rows_first_col(int lane) { return (lane >> 4) * 8
 __device__ __forceinline__ int cols_first_row(int lane) { return (lane & 7) + (lane >> 4) * 8; }
 __device__ __forceinline__ int cols_first_col(int lane) { return ((lane >> 3) & 1) * 8; }
 
-// ------------------------------------------------------------- tile loads
-// rows x cols of a row-major global matrix (row stride gld elements) into
-// shared memory (row stride sld), zeros outside [0, have_rows) x [0, have_cols).
-// VEC: rows start 16-byte aligned and have_cols is a multiple of 8 (an
-// asynchronous copy of 16 bytes at a time); otherwise element by element.
-template <bool VEC>
-__device__ __forceinline__ void load_tile(bf16 *s, int sld, const bf16 *g, int64_t gld, int rows, int cols,
-                                          int have_rows, int have_cols, int tid, int nthreads) {
-    if (VEC) {
-        const int per = cols / 8;
-        for (int i = tid; i < rows * per; i += nthreads) {
-            const int r = i / per, c = (i - r * per) * 8;
-            const bool in = r < have_rows && c < have_cols;
-            cp_async16(s + r * sld + c, in ? g + r * gld + c : g, in);
-        }
-    } else {
-        for (int i = tid; i < rows * cols; i += nthreads) {
-            const int r = i / cols, c = i - r * cols;
-            s[r * sld + c] = r < have_rows && c < have_cols ? g[r * gld + c] : __float2bfloat16_rn(0.f);
-        }
-    }
-}
-
 // A stored state: two bf16 terms, each as (NP / 8, pp, 8) -- the eight columns of
 // a group row after row, so that neither a thread per row nor a quad per row
 // spreads a store over more lines than its bytes fill (row-major, the forward's
@@ -121,91 +98,53 @@ __device__ __forceinline__ int64_t state_at(int pp, int term, int row, int col) 
     return ((int64_t)(term * (NP / 8) + (col >> 3)) * pp + row) * 8 + (col & 7);
 }
 
-// A warp's 16 x NP slice of a state (accumulators: rows row0 + lane / 4 (+ 8),
-// columns 8 j + 2 (lane % 4) (+ 1)).
-template <int NP>
-__device__ __forceinline__ void store_state(bf16 *dst, int pp, const float (&s)[NP / 8][4], int row0, int lane) {
-    if (row0 >= pp) return;
-#pragma unroll
-    for (int j = 0; j < NP / 8; ++j)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t hi, lo;
-            split(s[j][2 * half], s[j][2 * half + 1], hi, lo);
-            const int row = row0 + (lane >> 2) + 8 * half, col = 8 * j + 2 * (lane & 3);
-            *reinterpret_cast<uint32_t *>(dst + state_at<NP>(pp, 0, row, col)) = hi;
-            *reinterpret_cast<uint32_t *>(dst + state_at<NP>(pp, 1, row, col)) = lo;
-        }
-}
-
-// A warp's 16 columns of a (64, pp) matrix held transposed in accumulators
-// (x[j]: columns col0 + lane / 4 (+ 8), rows 8 j + 2 (lane % 4) (+ 1)) as two
-// bf16 terms: high (64, pp), then low.  `stage`: this warp's 16 columns of a
-// shared tile of 64 rows.
-__device__ __forceinline__ void store_rows(bf16 *dst, int pp, const float (&x)[kC / 8][4], bf16 *stage, int ld,
-                                           int col0, int lane) {
-    if (col0 >= pp) return;
-    __syncwarp();
-#pragma unroll
-    for (int term = 0; term < 2; ++term) {
-#pragma unroll
-        for (int jj = 0; jj < kC / 16; ++jj) {
-            uint32_t f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t hi, lo;
-                split(x[2 * jj + (i >> 1)][2 * (i & 1)], x[2 * jj + (i >> 1)][2 * (i & 1) + 1], hi, lo);
-                f[i] = term ? lo : hi;
-            }
-            stm4t(stage + (16 * jj + cols_first_row(lane)) * ld + cols_first_col(lane), f[0], f[1], f[2], f[3]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int it = 0; it < kC / 16; ++it) {
-            const int t = 16 * it + (lane >> 1), c = 8 * (lane & 1);
-            *reinterpret_cast<uint4 *>(dst + (int64_t)(term * kC + t) * pp + col0 + c) =
-                *reinterpret_cast<const uint4 *>(stage + t * ld + c);
-        }
-        __syncwarp();
-    }
-}
-
 }  // namespace delta
 
 // Workspace of the chunked kernels; sizes in elements.
 struct DeltaChunkWs {
     __nv_bfloat16 *mats;  // (batch, heads, chunks, kMats, 64, 64)
     float *dec;           // (batch, heads, chunks, kDec, 64)
-    // backward only; headdim rounded up to 16 (pp), dstate to 64 or 128 (np)
+    // backward only; headdim rounded up to 64 (pp), dstate to 64 or 128 (np)
     __nv_bfloat16 *s0;    // (batch, heads, chunks, 2, np / 8, pp, 8): the state entering each chunk
     __nv_bfloat16 *ds1;   // the same: the gradient of the state leaving it
     __nv_bfloat16 *r, *dv; // (batch, heads, chunks, 2, 64, pp): r, the gradient of V
 };
 
-// The forward on the tcgen05 tensor cores: dstate 64 or
-// 128, headdim a multiple of 64, 16-byte aligned tensors.
-// With few heads the sequence is split into segments that run side by side
-// (delta_fused_segments > 1: needs workspace).
-bool delta_fused_eligible(const DeltaArgs &a);
+// The chunked kernels take any sizes up to these limits with tensors whose rows
+// (qk_width, v_width values) are multiples of 16 bytes and start 16-byte aligned.
+bool delta_fused_fits(const DeltaArgs &a);
+inline int delta_padded(int64_t n) { return (int)((n + 7) / 8 * 8); }           // width of a row in memory
+inline int64_t delta_state_rows(int64_t headdim) { return (headdim + 63) / 64 * 64; }  // pp, headdim <= 128
+inline int64_t delta_state_cols(int64_t dstate) { return dstate <= 64 ? 64 : 128; }    // np
+
+// The forward.  With few heads the sequence is split into segments that run side
+// by side (delta_fused_segments > 1: needs workspace).
 int delta_fused_segments(const DeltaArgs &a, int sms);
 int64_t delta_fused_workspace(const DeltaArgs &a, int nseg);  // bytes
 cudaError_t launch_delta_fused(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st);
-// The gradient's first half on the same kernel (out is not read): everything of
-// the workspace but ds1 and dv.
+// The gradient (headdim <= 128), in this order: the forward on the same kernel (out
+// is not read), which leaves everything of the workspace but ds1 and dv; the pass
+// backwards in time; dq, dk, dg and dbeta.
 cudaError_t launch_delta_fused_store(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
-
-// The pass backwards in time on tcgen05: what delta_fused_eligible asks, headdim <=
-// 128, dout and dv aligned too.
-bool delta_fused_reverse_eligible(const DeltaBwdArgs &a);
 cudaError_t launch_delta_fused_reverse(const DeltaBwdArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
-// dq, dk, dg and dbeta on tcgen05: that, and dq and dk aligned.
-bool delta_fused_grad_eligible(const DeltaBwdArgs &a);
 cudaError_t launch_delta_fused_grad(const DeltaBwdArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
 
-cudaError_t launch_delta_prep(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st);
-cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
-cudaError_t launch_delta_chain_store(const DeltaArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
-cudaError_t launch_delta_reverse(const DeltaBwdArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
-cudaError_t launch_delta_grad(const DeltaBwdArgs &a, const DeltaChunkWs &ws, int sms, cudaStream_t st);
+// Copies of bf16 matrices into rows of another width: what lies beyond the source's
+// row is zero, what lies beyond the destination's is left out.
+struct DeltaRowCopy {
+    const __nv_bfloat16 *src;
+    __nv_bfloat16 *dst;
+    int64_t rows;
+    int src_width, dst_width;
+};
+struct DeltaRowCopies {
+    static constexpr int kMost = 4;
+    DeltaRowCopy c[kMost];
+    int n = 0;
+    void add(const void *src, void *dst, int64_t rows, int src_width, int dst_width) {
+        c[n++] = {static_cast<const __nv_bfloat16 *>(src), static_cast<__nv_bfloat16 *>(dst), rows, src_width, dst_width};
+    }
+};
+cudaError_t launch_delta_copies(const DeltaRowCopies &c, int sms, cudaStream_t st);
 
 }  // namespace ssm

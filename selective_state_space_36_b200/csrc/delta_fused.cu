@@ -89,7 +89,7 @@ struct FusedArgs {
     float scale;
     int64_t seqlen;
     int heads, rep, headdim, dstate, vtiles;
-    int vec_state;  // h0 and state start 16-byte aligned
+    int vec_state;  // rows of h0 and state start 16-byte aligned
     // sequence split: chunks per segment, segments (1: none), the states that the
     // segments start from (batch, heads, nseg, headdim, dstate);
     // for the segment pass: the same for the states they end with and the
@@ -480,8 +480,8 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                 mbar_expect_tx(&sm.ldk[st], (uint32_t)(2 * NT) * kHalfTile);
 #pragma unroll 1
                 for (int i = 0; i < NT; ++i) {
-                    tma_load_3d(sm.kq[st][i], &mapK, gr * a.dstate + 64 * i, t0, (int32_t)b, &sm.ldk[st]);
-                    tma_load_3d(sm.kq[st][i] + kHalfTile, &mapQ, gr * a.dstate + 64 * i, t0, (int32_t)b, &sm.ldk[st]);
+                    tma_load_4d(sm.kq[st][i], &mapK, 64 * i, gr, t0, (int32_t)b, &sm.ldk[st]);
+                    tma_load_4d(sm.kq[st][i] + kHalfTile, &mapQ, 64 * i, gr, t0, (int32_t)b, &sm.ldk[st]);
                 }
             }
             if (c + 2 < nch) {
@@ -510,7 +510,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                     if (el) {
 #pragma unroll 1
                         for (int i = 0; i < halves; ++i)
-                            tma_store_3d(&mapO, h * a.headdim + v0 + 64 * i, (c0 + c) * kC, (int32_t)b, sm.v[st][i]);
+                            tma_store_4d(&mapO, v0 + 64 * i, h, (c0 + c) * kC, (int32_t)b, sm.v[st][i]);
                         tma_store_commit();
                         tma_store_wait_read<0>();
                     }
@@ -522,7 +522,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                     mbar_expect_tx(&sm.ldv[st], (uint32_t)halves * kHalfTile);
 #pragma unroll 1
                     for (int i = 0; i < halves; ++i)
-                        tma_load_3d(sm.v[st][i], &mapV, h * a.headdim + v0 + 64 * i, t0, (int32_t)b, &sm.ldv[st]);
+                        tma_load_4d(sm.v[st][i], &mapV, v0 + 64 * i, h, t0, (int32_t)b, &sm.ldv[st]);
                 }
                 if (st) ++issued_v[1]; else ++issued_v[0];
             }
@@ -625,6 +625,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                                      : a.ends + ((bh * a.nseg + seg) * a.headdim + v0 + r) * (int64_t)a.dstate)
                         : (a.state && seg == a.nseg - 1 ? a.state + row * a.dstate : nullptr);
         const int vp = token_place(r);
+        const int cols = v0 + r < width ? a.dstate : 0;  // of this lane's row that exist
       if (32 * quad < 64 * halves) {
         // the start state, where the first chunk's "last product" would have left it
         {
@@ -639,13 +640,15 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                     if (a.vec_state) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
+                            if (col + i >= cols) continue;
                             const float4 x = *reinterpret_cast<const float4 *>(src + i);
                             s[i] = __float_as_uint(x.x); s[i + 1] = __float_as_uint(x.y);
                             s[i + 2] = __float_as_uint(x.z); s[i + 3] = __float_as_uint(x.w);
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(src[i]);
+                        for (int i = 0; i < 32; ++i)
+                            if (col + i < cols) s[i] = __float_as_uint(src[i]);
                     }
                 }
                 tmem_st32(tl + kTS + col, s);
@@ -701,17 +704,19 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                     fence_before_sync();
                     signal(&sm.s_ready[p]);
                     if constexpr (STORE)
-                        put_state_row<64 * NT>(a.s0 + (bh * all_chunks + c) * 2 * a.headdim * (int64_t)a.dstate, a.headdim,
-                                               v0 + r, col, hi, lo);
+                        put_state_row<64 * NT>(a.s0 + (bh * all_chunks + c) * 2 * (64 * halves) * (int64_t)(64 * NT),
+                                               64 * halves, r, col, hi, lo);
                 } else if (to) {
                     float *dst = to + col;
                     if (a.vec_state) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(dst + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+                            if (col + i < cols)
+                                *reinterpret_cast<float4 *>(dst + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) dst[i] = s[i];
+                        for (int i = 0; i < 32; ++i)
+                            if (col + i < cols) dst[i] = s[i];
                     }
                 }
             }
@@ -788,45 +793,45 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 // The states that the segments start from: starts[0] = h0 (a copy: the last
 // segment may write its end over it while the first still has to start),
-// starts[1] = ends[0], then starts[i + 1] = starts[i] Phi[i] + ends[i].  A block takes kJoinRows rows of one
-// head through all segments, one thread per column.
-constexpr int kJoinRows = 4;
+// starts[1] = ends[0], then starts[i + 1] = starts[i] Phi[i] + ends[i].  A block takes
+// kJoinRows rows of one head through all segments: per segment a thread multiplies
+// a quarter of a column of Phi (32 loads at once; with the whole column, 8 at a
+// time, 10 segments took 55 us) into all the rows, then adds up one row's quarters.
+constexpr int kJoinRows = 4;  // (the last block of a head may have fewer)
 
-__global__ void __launch_bounds__(128) delta_join_kernel(const float *h0, const float *ends, const float *phi,
-                                                         float *starts, int nseg, int headdim, int dstate) {
-    __shared__ float s[kJoinRows][128];
-    const int tiles = headdim / kJoinRows;
+__global__ void __launch_bounds__(kJoinRows * 128) delta_join_kernel(const float *h0, const float *ends, const float *phi,
+                                                                     float *starts, int nseg, int headdim, int dstate) {
+    __shared__ float s[kJoinRows][128], part[kJoinRows][kJoinRows][128];
+    constexpr int kPart = 128 / kJoinRows;
+    const int tiles = (headdim + kJoinRows - 1) / kJoinRows;
     const int64_t bh = blockIdx.x / tiles;
-    const int p0 = (int)(blockIdx.x % tiles) * kJoinRows, n = threadIdx.x;
-    if (n < dstate)
-#pragma unroll
-        for (int r = 0; r < kJoinRows; ++r)
-            starts[(bh * nseg * headdim + p0 + r) * (int64_t)dstate + n] =
-                h0 ? h0[(bh * headdim + p0 + r) * (int64_t)dstate + n] : 0.f;
+    const int p0 = (int)(blockIdx.x % tiles) * kJoinRows, n = threadIdx.x & 127, r = threadIdx.x >> 7, m0 = r * kPart;
+    const bool have = n < dstate && p0 + r < headdim;
+    if (have)
+        starts[(bh * nseg * headdim + p0 + r) * (int64_t)dstate + n] = h0 ? h0[(bh * headdim + p0 + r) * (int64_t)dstate + n] : 0.f;
     for (int seg = 0; seg < nseg - 1; ++seg) {
-        float acc[kJoinRows];
-        const int64_t at = ((bh * nseg + seg) * headdim + p0) * (int64_t)dstate + n;
-#pragma unroll
-        for (int r = 0; r < kJoinRows; ++r) acc[r] = n < dstate ? ends[at + r * dstate] : 0.f;
+        const int64_t at = ((bh * nseg + seg) * headdim + p0 + r) * (int64_t)dstate + n;
+        float sum = have ? ends[at] : 0.f;
         if (seg > 0) {
-            const float *f = phi + (bh * nseg + seg) * (int64_t)dstate * dstate + n;
-            if (n < dstate)
-#pragma unroll 8
-                for (int m = 0; m < dstate; ++m) {
-                    const float x = __ldg(f + (int64_t)m * dstate);
+            const float *f = phi + ((bh * nseg + seg) * dstate + m0) * (int64_t)dstate + n;
+            float x[kPart], acc[kJoinRows] = {};
 #pragma unroll
-                    for (int r = 0; r < kJoinRows; ++r) acc[r] = fmaf(s[r][m], x, acc[r]);
-                }
+            for (int m = 0; m < kPart; ++m) x[m] = n < dstate && m0 + m < dstate ? __ldg(f + (int64_t)m * dstate) : 0.f;
+#pragma unroll
+            for (int m = 0; m < kPart; ++m)
+#pragma unroll
+                for (int i = 0; i < kJoinRows; ++i) acc[i] = fmaf(s[i][m0 + m], x[m], acc[i]);
+#pragma unroll
+            for (int i = 0; i < kJoinRows; ++i) part[r][i][n] = acc[i];
             __syncthreads();
+            sum += (part[0][r][n] + part[1][r][n]) + (part[2][r][n] + part[3][r][n]);
         }
-#pragma unroll
-        for (int r = 0; r < kJoinRows; ++r) {
-            s[r][n] = acc[r];
-            if (n < dstate) starts[at + (int64_t)(headdim + r) * dstate] = acc[r];
-        }
+        s[r][n] = sum;
+        if (have) starts[at + (int64_t)headdim * dstate] = sum;
         __syncthreads();
     }
 }
+static_assert(kJoinRows == 4, "four parts");
 
 // Workspace of a split into nseg segments, floats: ends, phi, starts.
 int64_t split_floats(const DeltaArgs &a, int nseg) {
@@ -836,15 +841,15 @@ int64_t split_floats(const DeltaArgs &a, int nseg) {
 template <int NT>
 cudaError_t launch_t(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st) {
     CUtensorMap mq, mk, mv, mo;
-    const int64_t gn = (int64_t)a.groups * a.dstate, hp = (int64_t)a.heads * a.headdim, bh = a.batch * a.heads;
-    if (!encode_btw(&mq, a.q, a.batch, a.seqlen, gn, kC) || !encode_btw(&mk, a.k, a.batch, a.seqlen, gn, kC) ||
-        !encode_btw(&mv, a.v, a.batch, a.seqlen, hp, kC) || !encode_btw(&mo, a.out, a.batch, a.seqlen, hp, kC))
+    const int64_t bh = a.batch * a.heads;
+    if (!encode_tokens(&mq, a.q, a, a.groups, a.qk_width) || !encode_tokens(&mk, a.k, a, a.groups, a.qk_width) ||
+        !encode_tokens(&mv, a.v, a, a.heads, a.v_width) || !encode_tokens(&mo, a.out, a, a.heads, a.v_width))
         return cudaErrorInvalidValue;
     FusedArgs f{};
     f.g = a.g; f.beta = a.beta; f.h0 = a.h0; f.state = a.state; f.scale = a.scale;
     f.seqlen = a.seqlen; f.heads = a.heads; f.rep = a.heads / a.groups; f.headdim = a.headdim; f.dstate = a.dstate;
     f.vtiles = (a.headdim + 127) / 128;
-    f.vec_state = aligned16(a.h0) && aligned16(a.state);
+    f.vec_state = a.dstate % 4 == 0 && aligned16(a.h0) && aligned16(a.state);
     const int chunks = (int)((a.seqlen + kC - 1) / kC);
     f.seg_chunks = (chunks + nseg - 1) / nseg;
     f.nseg = nseg;
@@ -862,7 +867,7 @@ cudaError_t launch_t(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st) {
         delta_fused_kernel<NT, kAgg><<<(unsigned)blocks, kThreadsF, bytes, st>>>(mq, mk, mv, mo, mo, f);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        delta_join_kernel<<<(unsigned)(bh * (a.headdim / kJoinRows)), 128, 0, st>>>(a.h0, f.ends, f.phi, starts, nseg, a.headdim,
+        delta_join_kernel<<<(unsigned)(bh * ((a.headdim + kJoinRows - 1) / kJoinRows)), kJoinRows * 128, 0, st>>>(a.h0, f.ends, f.phi, starts, nseg, a.headdim,
                                                                                   a.dstate);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
@@ -876,18 +881,17 @@ cudaError_t launch_t(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st) {
 template <int NT>
 cudaError_t launch_store_t(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st) {
     CUtensorMap mq, mk, mv, mr, mm;
-    const int64_t gn = (int64_t)a.groups * a.dstate, hp = (int64_t)a.heads * a.headdim, bh = a.batch * a.heads;
-    const int64_t chunks = (a.seqlen + kC - 1) / kC;
-    if (!encode_btw(&mq, a.q, a.batch, a.seqlen, gn, kC) || !encode_btw(&mk, a.k, a.batch, a.seqlen, gn, kC) ||
-        !encode_btw(&mv, a.v, a.batch, a.seqlen, hp, kC) ||
-        !encode_btw(&mr, ws.r, bh * chunks * 2, kC, a.headdim, kC) ||
+    const int64_t bh = a.batch * a.heads, chunks = (a.seqlen + kC - 1) / kC;
+    if (!encode_tokens(&mq, a.q, a, a.groups, a.qk_width) || !encode_tokens(&mk, a.k, a, a.groups, a.qk_width) ||
+        !encode_tokens(&mv, a.v, a, a.heads, a.v_width) ||
+        !encode_btw(&mr, ws.r, bh * chunks * 2, kC, delta_state_rows(a.headdim), kC) ||
         !encode_btw(&mm, ws.mats, bh * chunks * 2, 2 * kC, kC, 2 * kC))
         return cudaErrorInvalidValue;
     FusedArgs f{};
     f.g = a.g; f.beta = a.beta; f.h0 = a.h0; f.scale = a.scale;
     f.seqlen = a.seqlen; f.heads = a.heads; f.rep = a.heads / a.groups; f.headdim = a.headdim; f.dstate = a.dstate;
     f.vtiles = (a.headdim + 127) / 128;
-    f.vec_state = aligned16(a.h0);
+    f.vec_state = a.dstate % 4 == 0 && aligned16(a.h0);
     f.seg_chunks = (int)chunks;
     f.nseg = 1;
     f.s0 = ws.s0;
@@ -904,11 +908,10 @@ cudaError_t launch_store_t(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStrea
 }  // namespace
 }  // namespace delta
 
-bool delta_fused_eligible(const DeltaArgs &a) {
-    using namespace delta;
-    return (a.dstate == 64 || a.dstate == 128) && a.headdim % 64 == 0 && a.seqlen < (int64_t)1 << 30 &&
-           a.batch < (int64_t)1 << 30 && (int64_t)a.heads * a.headdim < (int64_t)1 << 30 && aligned16(a.q) &&
-           aligned16(a.k) && aligned16(a.v) && aligned16(a.out) && encode_tiled_fn() != nullptr;
+bool delta_fused_fits(const DeltaArgs &a) {
+    constexpr int64_t most = (int64_t)1 << 30;  // coordinates of the copies
+    return a.seqlen < most && a.batch < most && (int64_t)a.heads * (a.headdim + 8) < most &&
+           (int64_t)a.groups * (a.dstate + 8) < most && encode_tiled_fn() != nullptr;
 }
 
 // Segments of the sequence.  A CTA walks over its chunks one after the other
@@ -941,11 +944,11 @@ int delta_fused_segments(const DeltaArgs &a, int sms) {
 int64_t delta_fused_workspace(const DeltaArgs &a, int nseg) { return nseg > 1 ? 4 * delta::split_floats(a, nseg) : 0; }
 
 cudaError_t launch_delta_fused_store(const DeltaArgs &a, const DeltaChunkWs &ws, cudaStream_t st) {
-    return a.dstate == 64 ? delta::launch_store_t<1>(a, ws, st) : delta::launch_store_t<2>(a, ws, st);
+    return a.dstate <= 64 ? delta::launch_store_t<1>(a, ws, st) : delta::launch_store_t<2>(a, ws, st);
 }
 
 cudaError_t launch_delta_fused(const DeltaArgs &a, int nseg, float *ws, cudaStream_t st) {
-    return a.dstate == 64 ? delta::launch_t<1>(a, nseg, ws, st) : delta::launch_t<2>(a, nseg, ws, st);
+    return a.dstate <= 64 ? delta::launch_t<1>(a, nseg, ws, st) : delta::launch_t<2>(a, nseg, ws, st);
 }
 
 }  // namespace ssm

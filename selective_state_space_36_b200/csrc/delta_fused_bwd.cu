@@ -61,7 +61,7 @@ struct RevArgs {
     float scale;
     int64_t seqlen;
     int heads, rep, headdim, dstate;
-    int vec_state;  // dend and dh0 start 16-byte aligned
+    int vec_state;  // rows of dend and dh0 start 16-byte aligned
     unsigned int *status;
 };
 
@@ -192,9 +192,8 @@ delta_fused_reverse_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
                     mbar_expect_tx(&sm.ldk[st], (uint32_t)(2 * NT + 4) * kHalfTile);
 #pragma unroll 1
                     for (int i = 0; i < NT; ++i) {
-                        tma_load_3d(sm.kq[st][i], &mapK, gr * a.dstate + 64 * i, next * kC, (int32_t)b, &sm.ldk[st]);
-                        tma_load_3d(sm.kq[st][i] + kHalfTile, &mapQ, gr * a.dstate + 64 * i, next * kC, (int32_t)b,
-                                    &sm.ldk[st]);
+                        tma_load_4d(sm.kq[st][i], &mapK, 64 * i, gr, next * kC, (int32_t)b, &sm.ldk[st]);
+                        tma_load_4d(sm.kq[st][i] + kHalfTile, &mapQ, 64 * i, gr, next * kC, (int32_t)b, &sm.ldk[st]);
                     }
 #pragma unroll 1
                     for (int term = 0; term < 2; ++term)
@@ -208,7 +207,7 @@ delta_fused_reverse_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
                     const int ch = nch - 1 - c;
 #pragma unroll 1
                     for (int i = 0; i < halves; ++i) {
-                        tma_store_3d(&mapV, h * a.headdim + 64 * i, ch * kC, (int32_t)b, sm.o[st][i]);
+                        tma_store_4d(&mapV, 64 * i, h, ch * kC, (int32_t)b, sm.o[st][i]);
                         tma_store_3d(&mapT, 64 * i, 0, (int32_t)((bh * nch + ch) * 2), sm.o[st][i]);
                         tma_store_3d(&mapT, 64 * i, 0, (int32_t)((bh * nch + ch) * 2 + 1), sm.lo[st][i]);
                     }
@@ -222,7 +221,7 @@ delta_fused_reverse_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
                     mbar_expect_tx(&sm.ldo[st], (uint32_t)halves * kHalfTile);
 #pragma unroll 1
                     for (int i = 0; i < halves; ++i)
-                        tma_load_3d(sm.o[st][i], &mapO, h * a.headdim + 64 * i, next * kC, (int32_t)b, &sm.ldo[st]);
+                        tma_load_4d(sm.o[st][i], &mapO, 64 * i, h, next * kC, (int32_t)b, &sm.ldo[st]);
                 }
                 if (st) ++issued_o[1]; else ++issued_o[0];
             }
@@ -260,7 +259,7 @@ delta_fused_reverse_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
         const int quad = warp & 3, wg = warp >> 2, r = 32 * quad + lane;
         const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
         const int64_t row = bh * a.headdim + r;
-        const int vp = token_place(r);
+        const int vp = token_place(r), cols = r < a.headdim ? a.dstate : 0;  // columns of this lane's row that exist
         // the end state's gradient, where the last "product" would have left it
 #pragma unroll 1
         for (int p = 0; p < NT; ++p) {
@@ -273,13 +272,15 @@ delta_fused_reverse_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
                 if (a.vec_state) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
+                        if (col + i >= cols) continue;
                         const float4 x = *reinterpret_cast<const float4 *>(src + i);
                         s[i] = __float_as_uint(x.x); s[i + 1] = __float_as_uint(x.y);
                         s[i + 2] = __float_as_uint(x.z); s[i + 3] = __float_as_uint(x.w);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(src[i]);
+                    for (int i = 0; i < 32; ++i)
+                        if (col + i < cols) s[i] = __float_as_uint(src[i]);
                 }
             }
             tmem_st32(tl + kTS + col, s);
@@ -340,17 +341,19 @@ delta_fused_reverse_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
                     tmem_wait_st();
                     fence_before_sync();
                     signal(&sm.s_ready[p]);
-                    put_state_row<64 * NT>(a.ds1 + (bh * nch + nch - 1 - c) * 2 * a.headdim * (int64_t)a.dstate, a.headdim, r,
-                                           col, hi, lo);
+                    put_state_row<64 * NT>(a.ds1 + (bh * nch + nch - 1 - c) * 2 * (64 * halves) * (int64_t)(64 * NT),
+                                           64 * halves, r, col, hi, lo);
                 } else if (a.dh0) {
                     float *dst = a.dh0 + row * a.dstate + col;
                     if (a.vec_state) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(dst + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+                            if (col + i < cols)
+                                *reinterpret_cast<float4 *>(dst + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) dst[i] = s[i];
+                        for (int i = 0; i < 32; ++i)
+                            if (col + i < cols) dst[i] = s[i];
                     }
                 }
             }
@@ -414,16 +417,15 @@ template <int NT>
 cudaError_t launch_t(const DeltaBwdArgs &p, const DeltaChunkWs &ws, cudaStream_t st) {
     const DeltaArgs &a = p.f;
     CUtensorMap mq, mk, mo, mv, mt, mm;
-    const int64_t gn = (int64_t)a.groups * a.dstate, hp = (int64_t)a.heads * a.headdim;
     const int64_t units2 = a.batch * a.heads * ((a.seqlen + kC - 1) / kC) * 2;
-    if (!encode_btw(&mq, a.q, a.batch, a.seqlen, gn, kC) || !encode_btw(&mk, a.k, a.batch, a.seqlen, gn, kC) ||
-        !encode_btw(&mo, p.dout, a.batch, a.seqlen, hp, kC) || !encode_btw(&mv, p.dv, a.batch, a.seqlen, hp, kC) ||
-        !encode_btw(&mt, ws.dv, units2, kC, a.headdim, kC) || !encode_btw(&mm, ws.mats, units2, 2 * kC, kC, 2 * kC))
+    if (!encode_tokens(&mq, a.q, a, a.groups, a.qk_width) || !encode_tokens(&mk, a.k, a, a.groups, a.qk_width) ||
+        !encode_tokens(&mo, p.dout, a, a.heads, a.v_width) || !encode_tokens(&mv, p.dv, a, a.heads, a.v_width) ||
+        !encode_btw(&mt, ws.dv, units2, kC, delta_state_rows(a.headdim), kC) || !encode_btw(&mm, ws.mats, units2, 2 * kC, kC, 2 * kC))
         return cudaErrorInvalidValue;
     RevArgs f{};
     f.dec = ws.dec; f.dend = p.dend; f.dh0 = p.dh0; f.ds1 = ws.ds1; f.scale = a.scale;
     f.seqlen = a.seqlen; f.heads = a.heads; f.rep = a.heads / a.groups; f.headdim = a.headdim; f.dstate = a.dstate;
-    f.vec_state = aligned16(p.dend) && aligned16(p.dh0);
+    f.vec_state = a.dstate % 4 == 0 && aligned16(p.dend) && aligned16(p.dh0);
     cudaError_t e = device_status_address(&f.status);
     if (e != cudaSuccess) return e;
     constexpr int bytes = (int)sizeof(RevSmem<NT>) + 1024;
@@ -437,12 +439,8 @@ cudaError_t launch_t(const DeltaBwdArgs &p, const DeltaChunkWs &ws, cudaStream_t
 }  // namespace
 }  // namespace delta
 
-bool delta_fused_reverse_eligible(const DeltaBwdArgs &p) {
-    return delta_fused_eligible(p.f) && p.f.headdim <= 128 && delta::aligned16(p.dout) && delta::aligned16(p.dv);
-}
-
 cudaError_t launch_delta_fused_reverse(const DeltaBwdArgs &p, const DeltaChunkWs &ws, cudaStream_t st) {
-    return p.f.dstate == 64 ? delta::launch_t<1>(p, ws, st) : delta::launch_t<2>(p, ws, st);
+    return p.f.dstate <= 64 ? delta::launch_t<1>(p, ws, st) : delta::launch_t<2>(p, ws, st);
 }
 
 }  // namespace ssm

@@ -1,7 +1,6 @@
 // delta_fused_grad.cu -- the second half of the chunked gated delta rule's
-// gradient (formulas at delta_bwd.cu; delta_grad.cu does the same on mma.sync for
-// sizes that do not fit here) on the sm_100a tensor cores: dq, dk, dg and dbeta of
-// all chunks and heads, each a unit of its own.
+// gradient (formulas at delta_fused_bwd.cu) on the sm_100a tensor cores: dq, dk, dg
+// and dbeta of all chunks and heads, each a unit of its own.
 //
 // Products of a unit have tokens as rows, two sets of 64 in the 128 lanes of
 // tensor memory.  With rows of 64 one above the other in shared memory,
@@ -79,7 +78,8 @@ struct GradTcArgs {
     float *dg, *dbeta;
     float scale;
     int64_t seqlen;
-    int heads, groups, rep, headdim, dstate;
+    int heads, groups, rep, headdim;
+    int width;             // values per row of dq and dk
     unsigned nch, chunks;  // chunks of a sequence, of all groups
     unsigned int *status;
 };
@@ -125,7 +125,7 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
     extern __shared__ unsigned char raw[];
     GradTcSmem<NT> &sm = *reinterpret_cast<GradTcSmem<NT> *>(raw + ((0u - smem_u32(raw)) & 1023u));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int pieces = a.headdim / kPieceRows;
+    const int pieces = (a.headdim + kPieceRows - 1) / kPieceRows;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.ld[i], 1);
@@ -241,8 +241,8 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                         mbar_expect_tx(&sm.ldkq[cs], (uint32_t)(2 * NT) * kHalfTile);
 #pragma unroll 1
                         for (int i = 0; i < NT; ++i) {
-                            tma_load_3d(sm.kq[cs][i], &mapQ, u.gr * a.dstate + 64 * i, u.t0, u.b, &sm.ldkq[cs]);
-                            tma_load_3d(sm.kq[cs][i] + kHalfTile, &mapK, u.gr * a.dstate + 64 * i, u.t0, u.b, &sm.ldkq[cs]);
+                            tma_load_4d(sm.kq[cs][i], &mapQ, 64 * i, u.gr, u.t0, u.b, &sm.ldkq[cs]);
+                            tma_load_4d(sm.kq[cs][i] + kHalfTile, &mapK, 64 * i, u.gr, u.t0, u.b, &sm.ldkq[cs]);
                         }
                     }
                     ++kqs;
@@ -255,7 +255,7 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                         uint64_t *bar = &sm.ld[st];
                         const int32_t unit2 = (int32_t)(2 * u.unit), x = kPieceRows * i;
                         mbar_expect_tx(bar, 5 * kPieceTile + (uint32_t)sizeof(to.s));
-                        tma_load_3d(to.row[kRowO], &mapO, u.head(a) * a.headdim + x, u.t0, u.b, bar);
+                        tma_load_4d(to.row[kRowO], &mapO, x, u.head(a), u.t0, u.b, bar);
                         tma_load_3d(to.row[kRowDvHigh], &mapV, x, 0, unit2, bar);
                         tma_load_3d(to.row[kRowDvLow], &mapV, x, 0, unit2 + 1, bar);
                         tma_load_3d(to.row[kRowRHigh], &mapR, x, 0, unit2, bar);
@@ -515,14 +515,16 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
             if (u.last(a)) {
                 signal(&sm.kq_taken[cs]);
                 if (t < u.live) {
-                    bf16 *dst = (lower ? a.dk : a.dq) + ((u.token + t) * a.groups + u.gr) * a.dstate + 32 * NT * wg;
+                    bf16 *dst = (lower ? a.dk : a.dq) + ((u.token + t) * a.groups + u.gr) * a.width + 32 * NT * wg;
 #pragma unroll
                     for (int p = 0; p < NT; ++p)
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
+                        for (int i = 0; i < 32; i += 8) {
+                            if (32 * (NT * wg + p) + i >= a.width) continue;
                             *reinterpret_cast<uint4 *>(dst + 32 * p + i) =
                                 make_uint4(pack(sum[p][i], sum[p][i + 1]), pack(sum[p][i + 2], sum[p][i + 3]),
                                            pack(sum[p][i + 4], sum[p][i + 5]), pack(sum[p][i + 6], sum[p][i + 7]));
+                        }
                 }
             }
         }
@@ -533,28 +535,25 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
     if (warp == 0) tmem_dealloc(tm, 512);
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 template <int NT>
 cudaError_t launch_t(const DeltaBwdArgs &p, const DeltaChunkWs &ws, int sms, cudaStream_t st) {
     const DeltaArgs &a = p.f;
     CUtensorMap mq, mk, mo, mv, mr, m0, m1;
-    const int64_t gn = (int64_t)a.groups * a.dstate, hp = (int64_t)a.heads * a.headdim;
     const int64_t nch = (a.seqlen + kC - 1) / kC, units2 = a.batch * a.heads * nch * 2;
-    const int64_t state[3] = {a.headdim * 8, 8 * NT, units2};  // groups of eight columns, row after row
+    const int64_t pp = delta_state_rows(a.headdim), state[3] = {pp * 8, 8 * NT, units2};  // groups of eight columns, row after row
     constexpr auto sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
-    if (!encode_btw(&mq, a.q, a.batch, a.seqlen, gn, kC) || !encode_btw(&mk, a.k, a.batch, a.seqlen, gn, kC) ||
-        !encode_bf16(&mo, p.dout, {hp, a.seqlen, a.batch}, {kPieceRows, kC, 1}, sw64) ||
-        !encode_bf16(&mv, ws.dv, {a.headdim, kC, units2}, {kPieceRows, kC, 1}, sw64) ||
-        !encode_bf16(&mr, ws.r, {a.headdim, kC, units2}, {kPieceRows, kC, 1}, sw64) ||
-        !encode_bf16(&m0, ws.s0, state, {kPieceRows * 8, 8 * NT, 1}, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-        !encode_bf16(&m1, ws.ds1, state, {kPieceRows * 8, 8 * NT, 1}, CU_TENSOR_MAP_SWIZZLE_NONE))
+    if (!encode_tokens(&mq, a.q, a, a.groups, a.qk_width) || !encode_tokens(&mk, a.k, a, a.groups, a.qk_width) ||
+        !encode_bf16<4>(&mo, p.dout, {a.v_width, a.heads, a.seqlen, a.batch}, {kPieceRows, 1, kC, 1}, sw64) ||
+        !encode_bf16<3>(&mv, ws.dv, {pp, kC, units2}, {kPieceRows, kC, 1}, sw64) ||
+        !encode_bf16<3>(&mr, ws.r, {pp, kC, units2}, {kPieceRows, kC, 1}, sw64) ||
+        !encode_bf16<3>(&m0, ws.s0, state, {kPieceRows * 8, 8 * NT, 1}, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_bf16<3>(&m1, ws.ds1, state, {kPieceRows * 8, 8 * NT, 1}, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     GradTcArgs f{};
     f.g = a.g; f.dec = ws.dec; f.scale = a.scale;
     f.dq = static_cast<bf16 *>(p.dq); f.dk = static_cast<bf16 *>(p.dk); f.dg = p.dg; f.dbeta = p.dbeta;
     f.seqlen = a.seqlen; f.heads = a.heads; f.groups = a.groups; f.rep = a.heads / a.groups;
-    f.headdim = a.headdim; f.dstate = a.dstate;
+    f.headdim = a.headdim; f.width = a.qk_width;
     f.nch = (unsigned)nch;
     f.chunks = (unsigned)(a.batch * a.groups * nch);
     cudaError_t e = device_status_address(&f.status);
@@ -571,12 +570,8 @@ cudaError_t launch_t(const DeltaBwdArgs &p, const DeltaChunkWs &ws, int sms, cud
 }  // namespace
 }  // namespace delta
 
-bool delta_fused_grad_eligible(const DeltaBwdArgs &p) {
-    return delta_fused_reverse_eligible(p) && delta::aligned16(p.dq) && delta::aligned16(p.dk);
-}
-
 cudaError_t launch_delta_fused_grad(const DeltaBwdArgs &p, const DeltaChunkWs &ws, int sms, cudaStream_t st) {
-    return p.f.dstate == 64 ? delta::launch_t<1>(p, ws, sms, st) : delta::launch_t<2>(p, ws, sms, st);
+    return p.f.dstate <= 64 ? delta::launch_t<1>(p, ws, sms, st) : delta::launch_t<2>(p, ws, sms, st);
 }
 
 }  // namespace ssm

@@ -24,6 +24,9 @@ struct DeltaArgs {
     float *state;              // the same shape or null (not returned); may be h0
     int64_t batch, seqlen;
     int heads, groups, headdim, dstate;
+    // values per row of q, k and of v, out in memory: dstate and headdim, or those
+    // rounded up to a multiple of 8 in padded copies
+    int qk_width, v_width;
     // backward in float32: the state before every kDeltaStep-th token
     // (batch, heads, ceil(seqlen / kDeltaStep), headdim, dstate) and
     // r = v - a S k (batch, seqlen, heads, headdim); null: not stored

@@ -1,14 +1,21 @@
-// delta_tc.cuh -- what the two tcgen05 kernels of the gated delta rule share (the
-// forward's delta_fused.cu, the gradient's delta_fused_bwd.cu).
+// delta_tc.cuh -- what the tcgen05 kernels of the gated delta rule share
+// (delta_fused.cu, delta_fused_bwd.cu, delta_fused_grad.cu).
 #pragma once
 
 #include "delta_chunk.cuh"
+#include "tma_maps.cuh"
 #include "umma.cuh"
 
 namespace ssm {
 namespace delta {
 
 constexpr uint32_t kHalfTile = kC * 128;  // 64 rows x 128 bytes
+
+// A (batch, seqlen, heads, width) tensor as tiles of one head's 64 tokens x 64
+// values, 128-byte swizzle.
+inline bool encode_tokens(CUtensorMap *m, const void *p, const DeltaArgs &a, int heads, int width) {
+    return encode_bf16<4>(m, p, {width, heads, a.seqlen, a.batch}, {64, 1, kC, 1}, CU_TENSOR_MAP_SWIZZLE_128B);
+}
 
 // Columns of a chunk operand of two terms (64 tokens x 2 terms, 64 columns from
 // `base`), K step `kstep` of 16 tokens: the tokens 32 wg .. 32 wg + 31 of both

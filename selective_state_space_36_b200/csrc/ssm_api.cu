@@ -855,8 +855,11 @@ int device_sms() {
 }
 
 // bf16 sequences up to this many tokens run token by token (one launch, no
-// workspace), longer ones in chunks on the tensor cores.
-constexpr int64_t kDeltaRecurrentTokens = 32;
+// workspace), longer ones in chunks on the tensor cores.  Token by token, 16 and 32
+// tokens take 7.0 and 12.2 us (one sequence, 16 heads of 64 x 128) or 27 and 50 us (8
+// sequences, 32 heads of 128 x 128); one chunk takes 9.4 or 19.4 us, 2 to 6 us more
+// through padded copies.
+constexpr int64_t kDeltaRecurrentTokens = 16;
 
 // Sizes common to the delta rule's entry points; *empty: nothing to compute.
 ssm_status check_delta_dims(const ssm_ssd_dims &d, ssm_dtype io, size_t *es, bool *empty) {
@@ -885,26 +888,57 @@ ssm::DeltaArgs delta_args(const ssm_ssd_dims &d, const void *q, const void *k, c
     a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.scale = scale;
     a.batch = d.batch; a.seqlen = d.seqlen;
     a.heads = (int)d.heads; a.groups = (int)d.groups; a.headdim = (int)d.headdim; a.dstate = (int)d.dstate;
+    a.qk_width = a.dstate; a.v_width = a.headdim;
     return a;
 }
 
-// Workspace of `units` chunks; pp, np > 0: with what the backward pass keeps of
-// each (states of pp x np, r and dV of 64 x pp, two bf16 terms each).
-cudaError_t delta_chunk_workspace(int64_t units, int64_t pp, int64_t np, void **mem, ssm::DeltaChunkWs *ws,
-                                  cudaStream_t st) {
-    constexpr int64_t c = ssm::delta::kC;
-    const int64_t mats = ssm::delta::kMats * c * c, dec = ssm::delta::kDec * c, state = 2 * pp * np, rows = 2 * c * pp;
-    cudaError_t e = workspace_alloc(mem, (size_t)units * (size_t)(2 * (mats + 2 * state + 2 * rows) + 4 * dec), st);
-    if (e != cudaSuccess) return e;
-    __nv_bfloat16 *at = static_cast<__nv_bfloat16 *>(*mem);
-    ws->mats = at; at += units * mats;
-    ws->s0 = at; at += units * state;
-    ws->ds1 = at; at += units * state;
-    ws->r = at; at += units * rows;
-    ws->dv = at; at += units * rows;
-    ws->dec = reinterpret_cast<float *>(at);
-    return cudaSuccess;
-}
+// Parts of one allocation, each 256-byte aligned.
+struct Parts {
+    size_t bytes = 0;
+    size_t add(int64_t elements, size_t size) {
+        const size_t at = bytes;
+        bytes += ((size_t)elements * size + 255) / 256 * 256;
+        return at;
+    }
+};
+
+// The bf16 tensors of a chunked call that need padded copies (rows that are not
+// multiples of 16 bytes, or not on 16-byte boundaries), their places in the
+// workspace.
+struct DeltaPads {
+    static constexpr int kMost = 7;
+    struct Pad {
+        const void **p;  // replaced by the copy
+        size_t at;
+        int64_t rows;
+        int width, padded;
+        bool output;
+    } pad[kMost];
+    int n = 0;
+    void tensor(Parts *parts, const void **p, int64_t rows, int64_t width, bool output) {
+        const int padded = ssm::delta_padded(width);
+        if (padded == width && !misaligned(*p, 16)) return;
+        pad[n++] = {p, parts->add(rows * padded, 2), rows, (int)width, padded, output};
+    }
+    // Replaces the tensors by their copies, inputs filled; leave() then fills the outputs.
+    cudaError_t enter(void *mem, int sms, cudaStream_t st) {
+        ssm::DeltaRowCopies in;
+        for (int i = 0; i < n; ++i) {
+            void *copy = static_cast<char *>(mem) + pad[i].at;
+            if (pad[i].output)
+                out.add(copy, const_cast<void *>(*pad[i].p), pad[i].rows, pad[i].padded, pad[i].width);
+            else
+                in.add(*pad[i].p, copy, pad[i].rows, pad[i].width, pad[i].padded);
+            *pad[i].p = copy;
+        }
+        return ssm::launch_delta_copies(in, sms, st);
+    }
+    cudaError_t leave(int sms, cudaStream_t st) const { return ssm::launch_delta_copies(out, sms, st); }
+
+private:
+    ssm::DeltaRowCopies out;
+};
+static_assert(ssm::DeltaRowCopies::kMost >= 4, "q, k, v and dout");
 
 ssm_status delta_forward(ssm_ssd_dims dims, ssm_dtype io, const void *q, const void *k, const void *v,
                          const float *g, const float *beta, float scale, void *out, const float *h0,
@@ -923,34 +957,31 @@ ssm_status delta_forward(ssm_ssd_dims dims, ssm_dtype io, const void *q, const v
     ssm::DeltaArgs a = delta_args(dims, q, k, v, g, beta, scale);
     a.out = out; a.h0 = h0; a.state = state;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (io != SSM_BF16 || dims.seqlen <= kDeltaRecurrentTokens) {
+    if (io != SSM_BF16 || dims.seqlen <= kDeltaRecurrentTokens || !ssm::delta_fused_fits(a)) {
         cudaError_t e = ssm::launch_delta_recurrent(a, io == SSM_BF16, st);
         if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
         return SSM_OK;
     }
-    if (ssm::delta_fused_eligible(a)) {
-        const int nseg = ssm::delta_fused_segments(a, device_sms());
-        const int64_t bytes = ssm::delta_fused_workspace(a, nseg);
-        void *mem = nullptr;
-        if (bytes > 0) {
-            cudaError_t e = workspace_alloc(&mem, (size_t)bytes, st);
-            if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
-        }
-        cudaError_t e = ssm::launch_delta_fused(a, nseg, static_cast<float *>(mem), st);
-        cudaError_t ef = mem ? cudaFreeAsync(mem, st) : cudaSuccess;
-        if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
-        if (ef != cudaSuccess) return cuda_fail(ef, "workspace release");
-        return SSM_OK;
-    }
-    const int64_t units = dims.batch * dims.heads * ((dims.seqlen + ssm::delta::kC - 1) / ssm::delta::kC);
-    if (units > kMaxGridX) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+    const int sms = device_sms(), nseg = ssm::delta_fused_segments(a, sms);
+    const int64_t tokens = dims.batch * dims.seqlen;
+    Parts parts;
+    const size_t split = parts.add(ssm::delta_fused_workspace(a, nseg), 1);
+    DeltaPads pads;
+    const void *to = out;
+    pads.tensor(&parts, &a.q, tokens * dims.groups, dims.dstate, false);
+    pads.tensor(&parts, &a.k, tokens * dims.groups, dims.dstate, false);
+    pads.tensor(&parts, &a.v, tokens * dims.heads, dims.headdim, false);
+    pads.tensor(&parts, &to, tokens * dims.heads, dims.headdim, true);
+    a.qk_width = ssm::delta_padded(dims.dstate);
+    a.v_width = ssm::delta_padded(dims.headdim);
     void *mem = nullptr;
-    ssm::DeltaChunkWs ws{};
-    cudaError_t e = delta_chunk_workspace(units, 0, 0, &mem, &ws, st);
+    cudaError_t e = parts.bytes ? workspace_alloc(&mem, parts.bytes, st) : cudaSuccess;
     if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
-    e = ssm::launch_delta_prep(a, ws, st);
-    if (e == cudaSuccess) e = ssm::launch_delta_chain(a, ws, device_sms(), st);
-    cudaError_t ef = cudaFreeAsync(mem, st);
+    e = pads.enter(mem, sms, st);
+    a.out = const_cast<void *>(to);
+    if (e == cudaSuccess) e = ssm::launch_delta_fused(a, nseg, reinterpret_cast<float *>(static_cast<char *>(mem) + split), st);
+    if (e == cudaSuccess) e = pads.leave(sms, st);
+    cudaError_t ef = mem ? cudaFreeAsync(mem, st) : cudaSuccess;
     if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
     if (ef != cudaSuccess) return cuda_fail(ef, "workspace release");
     return SSM_OK;
@@ -1027,22 +1058,41 @@ ssm_status ssm_delta_rule_bwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, co
     void *mem = nullptr;
     cudaError_t e;
     if (io == SSM_BF16) {
-        ssm::DeltaChunkWs ws{};
+        if (!ssm::delta_fused_fits(p.f)) return fail(SSM_ERR_UNSUPPORTED, "sizes beyond the tensor copies' coordinates");
+        constexpr int64_t c = ssm::delta::kC;
+        const int64_t pp = ssm::delta_state_rows(dims.headdim), np = ssm::delta_state_cols(dims.dstate);
         const int sms = device_sms();
-        e = delta_chunk_workspace(units, (dims.headdim + 15) / 16 * 16, dims.dstate <= 64 ? 64 : 128, &mem, &ws, st);
+        Parts parts;
+        const size_t mats = parts.add(units * ssm::delta::kMats * c * c, 2), s0 = parts.add(units * 2 * pp * np, 2),
+                     ds1 = parts.add(units * 2 * pp * np, 2), r = parts.add(units * 2 * c * pp, 2),
+                     dvt = parts.add(units * 2 * c * pp, 2), dec = parts.add(units * ssm::delta::kDec * c, 4);
+        DeltaPads pads;
+        const void *dq_to = dq, *dk_to = dk, *dv_to = dv;
+        pads.tensor(&parts, &p.f.q, tokens * dims.groups, dims.dstate, false);
+        pads.tensor(&parts, &p.f.k, tokens * dims.groups, dims.dstate, false);
+        pads.tensor(&parts, &p.f.v, tokens * dims.heads, dims.headdim, false);
+        pads.tensor(&parts, &p.dout, tokens * dims.heads, dims.headdim, false);
+        pads.tensor(&parts, &dq_to, tokens * dims.groups, dims.dstate, true);
+        pads.tensor(&parts, &dk_to, tokens * dims.groups, dims.dstate, true);
+        pads.tensor(&parts, &dv_to, tokens * dims.heads, dims.headdim, true);
+        p.f.qk_width = ssm::delta_padded(dims.dstate);
+        p.f.v_width = ssm::delta_padded(dims.headdim);
+        e = workspace_alloc(&mem, parts.bytes, st);
         if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
-        if (ssm::delta_fused_eligible(p.f)) {
-            e = ssm::launch_delta_fused_store(p.f, ws, st);
-        } else {
-            e = ssm::launch_delta_prep(p.f, ws, st);
-            if (e == cudaSuccess) e = ssm::launch_delta_chain_store(p.f, ws, sms, st);
-        }
-        if (e == cudaSuccess)
-            e = ssm::delta_fused_reverse_eligible(p) ? ssm::launch_delta_fused_reverse(p, ws, st)
-                                                     : ssm::launch_delta_reverse(p, ws, sms, st);
-        if (e == cudaSuccess)
-            e = ssm::delta_fused_grad_eligible(p) ? ssm::launch_delta_fused_grad(p, ws, sms, st)
-                                                  : ssm::launch_delta_grad(p, ws, sms, st);
+        char *at = static_cast<char *>(mem);
+        ssm::DeltaChunkWs ws{};
+        ws.mats = reinterpret_cast<__nv_bfloat16 *>(at + mats);
+        ws.s0 = reinterpret_cast<__nv_bfloat16 *>(at + s0);
+        ws.ds1 = reinterpret_cast<__nv_bfloat16 *>(at + ds1);
+        ws.r = reinterpret_cast<__nv_bfloat16 *>(at + r);
+        ws.dv = reinterpret_cast<__nv_bfloat16 *>(at + dvt);
+        ws.dec = reinterpret_cast<float *>(at + dec);
+        e = pads.enter(mem, sms, st);
+        p.dq = const_cast<void *>(dq_to); p.dk = const_cast<void *>(dk_to); p.dv = const_cast<void *>(dv_to);
+        if (e == cudaSuccess) e = ssm::launch_delta_fused_store(p.f, ws, st);
+        if (e == cudaSuccess) e = ssm::launch_delta_fused_reverse(p, ws, st);
+        if (e == cudaSuccess) e = ssm::launch_delta_fused_grad(p, ws, sms, st);
+        if (e == cudaSuccess) e = pads.leave(sms, st);
     } else {
         const size_t marks = (size_t)units * dims.headdim * dims.dstate, r = (size_t)tokens * dims.heads * dims.headdim;
         const size_t per_head = (size_t)tokens * dims.heads * dims.dstate;

@@ -29,16 +29,23 @@ inline EncodeTiledFn encode_tiled_fn() {
     return fn;
 }
 
-// A bf16 tensor of up to three dimensions, innermost first and dense, as a tiled
-// map with boxes of `box` elements.
-inline bool encode_bf16(CUtensorMap *m, const void *p, const int64_t (&n)[3], const int (&boxes)[3], CUtensorMapSwizzle sw) {
+// A dense bf16 tensor of D dimensions, innermost first, as a tiled map with boxes
+// of `boxes` elements; what lies outside the tensor reads as zeros and is not
+// written by stores.
+template <int D>
+bool encode_bf16(CUtensorMap *m, const void *p, const int64_t (&n)[D], const int (&boxes)[D], CUtensorMapSwizzle sw) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)n[0], (cuuint64_t)n[1], (cuuint64_t)n[2]};
-    const cuuint64_t strides[2] = {(cuuint64_t)n[0] * 2, (cuuint64_t)(n[0] * n[1]) * 2};
-    const cuuint32_t box[3] = {(cuuint32_t)boxes[0], (cuuint32_t)boxes[1], (cuuint32_t)boxes[2]};
-    const cuuint32_t es[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
+    cuuint64_t dims[D], strides[D - 1], bytes = 2;
+    cuuint32_t box[D], es[D];
+    for (int i = 0; i < D; ++i) {
+        dims[i] = (cuuint64_t)n[i];
+        box[i] = (cuuint32_t)boxes[i];
+        es[i] = 1;
+        bytes *= dims[i];
+        if (i < D - 1) strides[i] = bytes;
+    }
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, const_cast<void *>(p), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -47,7 +54,7 @@ inline bool encode_bf16(CUtensorMap *m, const void *p, const int64_t (&n)[3], co
 // elements of the width x `steps` steps x 1 row, 128-byte swizzle; steps past
 // the sequence read as zeros and are not written by stores.
 inline bool encode_btw(CUtensorMap *m, const void *p, int64_t batch, int64_t seqlen, int64_t width, int steps) {
-    return encode_bf16(m, p, {width, seqlen, batch}, {64, steps, 1}, CU_TENSOR_MAP_SWIZZLE_128B);
+    return encode_bf16<3>(m, p, {width, seqlen, batch}, {64, steps, 1}, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace ssm

@@ -77,6 +77,10 @@ SHAPES = [
     (1, 2577, 2, 1, 64, 128, "bf16", "mixed", True),   # few heads: the sequence is split into segments
     (1, 2560, 1, 1, 128, 64, "bf16", "slow", False),
     (2, 1100, 1, 1, 192, 128, "bf16", "slow", True),
+    (1, 1700, 1, 1, 100, 90, "bf16", "slow", True),    # split, through padded copies
+    (1, 1100, 2, 2, 7, 9, "bf16", "mixed", True),
+    (2, 17, 2, 1, 24, 40, "bf16", "mixed", True),
+    (1, 32, 2, 1, 25, 41, "bf16", "mixed", True),
 ]
 
 
