@@ -669,7 +669,10 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
             if (c < nch && !unit_rows) {
                 if (!(ok = wait(&sm.ldv[st], c >> 1))) break;
                 load_tokens(sm.v[st][r >> 6] + 32 * wg * 128, vp, vv);
-                if constexpr (AGG) signal(&sm.o_ready[st]);
+                if constexpr (AGG) {
+                    reads_done();
+                    signal(&sm.o_ready[st]);
+                }
             }
             if (!OUT && c > 0) signal(&sm.o_taken[st ^ 1]);
             if (OUT && c > 0) {
@@ -687,6 +690,7 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
                     ov[i / 2 + 1] = pack(fmaf(g4.z, o1[i + 2], o2[i + 2]), fmaf(g4.w, o1[i + 3], o2[i + 3]));
                 }
                 fence_before_sync();
+                reads_done();
                 signal(&sm.o_taken[st ^ 1]);
             }
             if (c > 0 && !(ok = wait(&sm.s[st ^ 1], (c - 1) >> 1))) break;

@@ -10,10 +10,10 @@
 //   [x; y]   = [dO; dV] r^T         (N = 64,     K = headdim)   scaled: X and E
 //   [dQ; L]  = [dO; dV] S0          (N = dstate, K = headdim)   scaled, then + [X; E] K
 //   [-; R]   = [-; r] dS1           (N = dstate, K = headdim)   scaled, then + X^T Q + E^T K
-// (the lanes of - hold what nothing reads).  The rows come 32 of headdim at a time,
-// with 32 rows of the states S0 and dS1, whose stored form -- groups of eight
-// columns, row after row -- is an operand as it stands; the next piece loads
-// while this one is multiplied.
+// (the lanes of - hold what nothing reads).  The rows come 16 of headdim at a time,
+// with 16 rows of the states S0 and dS1, whose stored form -- groups of eight
+// columns, row after row -- is an operand as it stands; the next pieces load
+// while one is multiplied.
 //
 // A block takes chunks in turn and sums dq and dk over a chunk's heads in
 // registers, in the order of the heads.
@@ -39,11 +39,14 @@ constexpr int kThreadsG = (kRowWarps + kDotWarps + 4) * 32;  // 12-14: products,
 // Registers per thread: 128 at launch, then by group of four warps
 constexpr int kLaunchRegs = 128, kRowRegs = 184, kDotRegs = 72, kRestRegs = 72;
 static_assert(2 * kRowRegs + kDotRegs + kRestRegs <= 4 * kLaunchRegs, "no more than the block was launched with");
-constexpr int kPieceRows = 32;                      // of headdim
-constexpr uint32_t kPieceTile = kC * 2 * kPieceRows;  // 64 tokens x 32 values, 64-byte swizzle
+// Rows of headdim per piece, pieces on their way or in use.  (Pieces of 32 rows, two
+// of them: the same memory, but the first of it comes free for the next load a
+// thousand clocks later.)
+constexpr int kPieceRows = 16, kSlots = 4;
+constexpr uint32_t kPieceTile = kC * 2 * kPieceRows;  // 64 tokens x 16 values, 32-byte swizzle
 
-// tensor memory columns: [x; y], [Q; K] K^T, [dQ; L], [-; R]
-constexpr uint32_t kT1 = 0, kT5 = 64, kT2 = 128, kT4 = 256;
+// tensor memory columns: [x; y], [Q; K] K^T, [dQ; L], [-; r dS1], [-; X^T Q + E^T K]
+constexpr uint32_t kT1 = 0, kT5 = 64, kT2 = 128, kT4 = 256, kT3 = 384;
 enum : uint32_t { kRowO = 0, kRowDvHigh = 1, kRowZero = 2, kRowDvLow = 3, kRowRHigh = 4, kRowRLow = 5, kRowTiles = 6 };
 
 struct __align__(16) GradDec {                 // per head
@@ -54,9 +57,9 @@ struct __align__(16) GradDec {                 // per head
 template <int NT>
 struct GradTcSmem {
     struct Piece {
-        unsigned char row[kRowTiles][kPieceTile];          // 64-byte swizzle
+        unsigned char row[kRowTiles][kPieceTile];          // 32-byte swizzle
         unsigned char s[4][8 * NT][kPieceRows * 16];       // S0 high, low, dS1 high, low
-    } piece[2];
+    } piece[kSlots];
     unsigned char kq[2][NT][2 * kHalfTile];  // per chunk and 64 columns: Q rows, then K rows
     unsigned char xe[2][2 * kHalfTile];      // [X; E]: high, low term
     GradDec dec[2];
@@ -64,11 +67,11 @@ struct GradTcSmem {
     float kr[2][2][kC];
     float db[2][4][kC];                      // column sums of the four lane quarters
     float inner[2][kDotWarps];               // <S0, dS1>
-    uint64_t ld[2], free[2];                 // a piece landed; is read
+    uint64_t ld[kSlots], free[kSlots];       // a piece landed; is read
     uint64_t ldkq[2], kq_taken[2];           // K and Q landed; are read
     uint64_t cum[2], part[2];                // decays; a head's sums written
     uint64_t acc, fin, all;                  // products complete
-    uint64_t a_ready, r_ready, taken;        // X, E, [dQ; L] scaled; R scaled; tensor memory is read
+    uint64_t x_ready, a_ready, taken;        // X, E; [dQ; L] scaled; tensor memory is read
     uint32_t tmem;
 };
 
@@ -128,22 +131,24 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
     const int pieces = (a.headdim + kPieceRows - 1) / kPieceRows;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.ld[i], 1);
-            mbar_init(&sm.free[i], 1 + kDotWarps);
             mbar_init(&sm.ldkq[i], 1);
             mbar_init(&sm.kq_taken[i], kRowWarps);
             mbar_init(&sm.cum[i], 1);
             mbar_init(&sm.part[i], kRowWarps + kDotWarps);
         }
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&sm.ld[i], 1);
+            mbar_init(&sm.free[i], 1 + kDotWarps);
+        }
         mbar_init(&sm.acc, 1);
         mbar_init(&sm.fin, 1);
         mbar_init(&sm.all, 1);
         mbar_init(&sm.a_ready, kRowWarps);
-        mbar_init(&sm.r_ready, kRowWarps / 2);
+        mbar_init(&sm.x_ready, kRowWarps);
         mbar_init(&sm.taken, kRowWarps);
         mbar_fence_init();
     }
-    for (int i = tid; i < 2 * (int)kPieceTile / 16; i += kThreadsG)  // written here only
+    for (int i = tid; i < kSlots * (int)kPieceTile / 16; i += kThreadsG)  // written here only
         reinterpret_cast<uint4 *>(sm.piece[i / (kPieceTile / 16)].row[kRowZero])[i % (kPieceTile / 16)] =
             make_uint4(0, 0, 0, 0);
     fence_proxy_async();
@@ -182,48 +187,46 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                     }
                 }
                 for (int i = 0; i < pieces; ++i, ++piece) {
-                    const int st = piece & 1;
-                    if (!(ok = wait(&sm.ld[st], piece >> 1))) break;
+                    const int st = piece % kSlots;
+                    if (!(ok = wait(&sm.ld[st], piece / kSlots))) break;
                     fence_after_sync();
-                    const uint64_t rows = desc_tile(smem_u32(sm.piece[st].row[0]), 16, 512, kSwizzle64);
+                    const uint64_t rows = desc_tile(smem_u32(sm.piece[st].row[0]), 16, 8 * 2 * kPieceRows, kSwizzle32);
                     const uint64_t states = desc_tile(smem_u32(sm.piece[st].s[0]), 128, kPieceRows * 16, kSwizzleNone);
-                    auto row = [&](uint32_t tile, int k) { return rows + ((tile * kPieceTile + k * 32) >> 4); };
-                    auto state = [&](int which, int k) { return states + ((which * 8 * NT * kPieceRows * 16 + k * 256) >> 4); };
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const bool more = i > 0 || k > 0;
-                        mma_bf16_if(el, tm + kT1, row(kRowO, k), row(kRowRHigh, k), id_1, more);
-                        mma_bf16_if(el, tm + kT2, row(kRowO, k), state(0, k), id_n, more);
-                        mma_bf16_if(el, tm + kT4, row(kRowDvLow, k), state(2, k), id_n, more);
-                        mma_bf16_if(el, tm + kT1, row(kRowO, k), row(kRowRLow, k), id_1, true);
-                        mma_bf16_if(el, tm + kT2, row(kRowO, k), state(1, k), id_n, true);
-                        mma_bf16_if(el, tm + kT4, row(kRowDvLow, k), state(3, k), id_n, true);
-                        mma_bf16_if(el, tm + kT1, row(kRowZero, k), row(kRowRHigh, k), id_1, true);
-                        mma_bf16_if(el, tm + kT2, row(kRowZero, k), state(0, k), id_n, true);
-                        mma_bf16_if(el, tm + kT4, row(kRowRHigh, k), state(2, k), id_n, true);
-                    }
+                    auto row = [&](uint32_t tile) { return rows + ((tile * kPieceTile) >> 4); };
+                    auto state = [&](int which) { return states + ((which * 8 * NT * kPieceRows * 16) >> 4); };
+                    static_assert(kPieceRows == 16, "a piece is one step of the products");
+                    const bool more = i > 0;
+                    mma_bf16_if(el, tm + kT1, row(kRowO), row(kRowRHigh), id_1, more);
+                    mma_bf16_if(el, tm + kT2, row(kRowO), state(0), id_n, more);
+                    mma_bf16_if(el, tm + kT4, row(kRowDvLow), state(2), id_n, more);
+                    mma_bf16_if(el, tm + kT1, row(kRowO), row(kRowRLow), id_1, true);
+                    mma_bf16_if(el, tm + kT2, row(kRowO), state(1), id_n, true);
+                    mma_bf16_if(el, tm + kT4, row(kRowDvLow), state(3), id_n, true);
+                    mma_bf16_if(el, tm + kT1, row(kRowZero), row(kRowRHigh), id_1, true);
+                    mma_bf16_if(el, tm + kT2, row(kRowZero), state(0), id_n, true);
+                    mma_bf16_if(el, tm + kT4, row(kRowRHigh), state(2), id_n, true);
                     mma_commit_if(el, &sm.free[st]);
                 }
                 if (!ok) break;
                 mma_commit_if(el, &sm.acc);
                 // tiles with tokens as the summed index: 64 columns, the next 64 in the next tile
                 const uint64_t dq = desc_sw128(kq, 2 * kHalfTile, 1024), dk = dq + (kHalfTile >> 4);
+                if (!(ok = wait(&sm.x_ready, j))) break;
+                fence_after_sync();
+                // X^T and E^T in the upper 64 lanes: the tile before theirs in memory has the lower ones
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int tile = k >> 2;  // X high, E high, X low, E low
+                    mma_bf16_if(el, tm + kT3,
+                                desc_sw128(smem_u32(sm.xe[0]) + tile * kHalfTile - kHalfTile + (k & 3) * 2048, kHalfTile, 1024),
+                                ((tile & 1) ? dk : dq) + (((k & 3) * 2048) >> 4), id_t, k > 0);
+                }
                 if (!(ok = wait(&sm.a_ready, j))) break;
                 fence_after_sync();
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     mma_bf16_if(el, tm + kT2, desc_sw128(smem_u32(sm.xe[k >> 2]) + (k & 3) * 32, 16, 1024),
                                 dk + (((k & 3) * 2048) >> 4), id_n, true);
-                if (!(ok = wait(&sm.r_ready, j))) break;
-                fence_after_sync();
-                // X^T and E^T in the upper 64 lanes: the tile before theirs in memory has the lower ones
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int tile = k >> 2;  // X high, E high, X low, E low
-                    mma_bf16_if(el, tm + kT4,
-                                desc_sw128(smem_u32(sm.xe[0]) + tile * kHalfTile - kHalfTile + (k & 3) * 2048, kHalfTile, 1024),
-                                ((tile & 1) ? dk : dq) + (((k & 3) * 2048) >> 4), id_t, true);
-                }
                 mma_commit_if(el, &sm.fin);
             }
             mma_commit_if(el, &sm.all);  // whatever was issued completes before tensor memory goes away
@@ -248,8 +251,8 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                     ++kqs;
                 }
                 for (int i = 0; i < pieces; ++i, ++piece) {
-                    const int st = piece & 1;
-                    if (piece >= 2 && !(ok = wait(&sm.free[st], (piece - 2) >> 1))) break;
+                    const int st = piece % kSlots;
+                    if (piece >= kSlots && !(ok = wait(&sm.free[st], piece / kSlots - 1))) break;
                     if (el) {
                         auto &to = sm.piece[st];
                         uint64_t *bar = &sm.ld[st];
@@ -268,8 +271,9 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                     }
                 }
             }
-            for (uint32_t i = 0; i < 2; ++i) {  // no copy outlives the block
-                if (piece > i) (void)mbar_wait_2s(&sm.ld[(piece - 1 - i) & 1], ((piece - 1 - i) >> 1) & 1u);
+            for (uint32_t i = 0; i < kSlots; ++i)  // no copy outlives the block
+                if (piece > i) (void)mbar_wait_2s(&sm.ld[(piece - 1 - i) % kSlots], ((piece - 1 - i) / kSlots) & 1u);
+            for (uint32_t i = 0; i < 2; ++i) {
                 if (kqs > i) (void)mbar_wait_2s(&sm.ldkq[(kqs - 1 - i) & 1], ((kqs - 1 - i) >> 1) & 1u);
             }
             __syncwarp();
@@ -350,8 +354,8 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
         for (Walk u(a); ok && !u.done(a); u.next(a), ++j) {
             float inner = 0.f;
             for (int i = 0; i < pieces; ++i, ++piece) {
-                const int st = piece & 1;
-                if (!(ok = wait(&sm.ld[st], piece >> 1))) break;
+                const int st = piece % kSlots;
+                if (!(ok = wait(&sm.ld[st], piece / kSlots))) break;
                 constexpr int kVecs = 8 * NT * kPieceRows;  // 16 bytes each
                 const uint4 *s0 = reinterpret_cast<const uint4 *>(sm.piece[st].s[0]);
 #pragma unroll 2
@@ -365,6 +369,7 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                         inner = fmaf(high_of(w0[e]) + high_of(w1[e]), high_of(w2[e]) + high_of(w3[e]), inner);
                     }
                 }
+                reads_done();
                 signal(&sm.free[st]);
             }
             if (!ok) break;
@@ -400,7 +405,11 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
             tmem_wait_ld();
             {
                 const float f = lower ? -1.f : a.scale, th = dec.ch[t], tw = dec.cl[t];
-                const int last = t - lower - 32 * wg;  // column, counted from this warp's first
+                // bit i: column i of this warp's 32 is below the diagonal, or (x) on it.
+                // (Masks: as conditions, each of the 32 exponentials got a branch of its
+                // own, 4000 clocks instead of 1200.)
+                const int last = t - lower - 32 * wg;
+                const uint32_t keep = last < 0 ? 0u : 0xffffffffu >> (31 - (last < 31 ? last : 31));
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
                     const float4 h4 = *reinterpret_cast<const float4 *>(&dec.ch[32 * wg + i]);
@@ -410,9 +419,10 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                     const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float v = i + e <= last ? f * ex2_approx((th - hh[e]) + (tw - ll[e])) * x[i + e] : 0.f;
-                        qk[i + e] = i + e <= last ? v * qk[i + e] : 0.f;
-                        x[i + e] = v * bb[e];
+                        const uint32_t mask = (uint32_t)((int32_t)(keep << (31 - i - e)) >> 31);
+                        const float v = f * ex2_approx((th - hh[e]) + (tw - ll[e])) * x[i + e];
+                        qk[i + e] = __uint_as_float(__float_as_uint(v * qk[i + e]) & mask);
+                        x[i + e] = __uint_as_float(__float_as_uint(v * bb[e]) & mask);
                     }
                 }
                 uint32_t hi[16], lo[16];
@@ -424,6 +434,7 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                     *reinterpret_cast<uint4 *>(sm.xe[1] + at) = make_uint4(lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
                 }
                 fence_proxy_async();
+                signal(&sm.x_ready);
             }
             const float gam = dec.gam[t], f2 = lower ? -gam : a.scale * gam;
 #pragma unroll 1
@@ -439,43 +450,6 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
             tmem_wait_st();
             fence_before_sync();
             signal(&sm.a_ready);
-            // row r of [Q; K]
-            auto row_of = [&](int col, int p) {
-                return *reinterpret_cast<const uint4 *>(sm.kq[cs][col >> 6] + sw128_offset(r, ((col & 63) >> 3) + p));
-            };
-            auto dot = [&](const float (&v)[32], int col) {
-                float d[2] = {0.f, 0.f};
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const uint4 q4 = row_of(col, p);
-                    const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        d[0] = fmaf(low_of(q[e]), v[8 * p + 2 * e], d[0]);
-                        d[1] = fmaf(high_of(q[e]), v[8 * p + 2 * e + 1], d[1]);
-                    }
-                }
-                return d[0] + d[1];
-            };
-            if (lower) {
-                const float fr = dec.wend[t] * dec.beta[t];
-                float kr = 0.f;
-#pragma unroll 1
-                for (int p = 0; p < NT; ++p) {
-                    const int col = 32 * (NT * wg + p);
-                    tmem_ld32(tl + kT4 + col, x);
-                    tmem_wait_ld();
-                    kr += dot(x, col);
-                    uint32_t y[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(fr * x[i]);
-                    tmem_st32(tl + kT4 + col, y);
-                }
-                tmem_wait_st();
-                fence_before_sync();
-                signal(&sm.r_ready);
-                sm.kr[s][wg][t] = kr;
-            }
             // column sums over the warp's 32 lanes: a lane ends with its own column's
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
@@ -486,29 +460,53 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                     qk[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
                 }
             sm.db[s][quad][32 * wg + lane] = qk[0];
-            // dQ, or L and R, of this head
+            // dQ, or L and R, of this head; row r of [Q; K]
+            auto row_of = [&](int col, int p) {
+                return *reinterpret_cast<const uint4 *>(sm.kq[cs][col >> 6] + sw128_offset(r, ((col & 63) >> 3) + p));
+            };
             if (!(ok = wait(&sm.fin, j))) break;
             fence_after_sync();
-            float d = 0.f;
+            const float fr = dec.wend[t] * dec.beta[t];
+            float d[2] = {0.f, 0.f}, kr[2] = {0.f, 0.f};
 #pragma unroll
             for (int p = 0; p < NT; ++p) {
                 const int col = 32 * (NT * wg + p);
                 tmem_ld32(tl + kT2 + col, x);
-                if (lower) tmem_ld32(tl + kT4 + col, qk);
-                tmem_wait_ld();
                 if (lower) {
+                    float rs[32];
+                    tmem_ld32(tl + kT4 + col, rs);
+                    tmem_ld32(tl + kT3 + col, qk);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        sum[p][i] += x[i] + qk[i];
-                        x[i] -= qk[i];
+                    for (int i = 0; i < 32; i += 8) {
+                        const uint4 k4 = row_of(col, i / 8);
+                        const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float kv = e & 1 ? high_of(kk[e / 2]) : low_of(kk[e / 2]);
+                            kr[e & 1] = fmaf(kv, rs[i + e], kr[e & 1]);
+                            const float rr = fmaf(fr, rs[i + e], qk[i + e]);
+                            d[e & 1] = fmaf(kv, x[i + e] - rr, d[e & 1]);
+                            sum[p][i + e] += x[i + e] + rr;
+                        }
                     }
                 } else {
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) sum[p][i] += x[i];
+                    for (int i = 0; i < 32; i += 8) {
+                        const uint4 q4 = row_of(col, i / 8);
+                        const uint32_t qq[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float qv = e & 1 ? high_of(qq[e / 2]) : low_of(qq[e / 2]);
+                            d[e & 1] = fmaf(qv, x[i + e], d[e & 1]);
+                            sum[p][i + e] += x[i + e];
+                        }
+                    }
                 }
-                d += dot(x, col);
             }
-            sm.dg[s][wg][r] = d;
+            if (lower) sm.kr[s][wg][t] = kr[0] + kr[1];
+            sm.dg[s][wg][r] = d[0] + d[1];
             fence_before_sync();
             signal(&sm.part[s]);
             signal(&sm.taken);
@@ -541,11 +539,11 @@ cudaError_t launch_t(const DeltaBwdArgs &p, const DeltaChunkWs &ws, int sms, cud
     CUtensorMap mq, mk, mo, mv, mr, m0, m1;
     const int64_t nch = (a.seqlen + kC - 1) / kC, units2 = a.batch * a.heads * nch * 2;
     const int64_t pp = delta_state_rows(a.headdim), state[3] = {pp * 8, 8 * NT, units2};  // groups of eight columns, row after row
-    constexpr auto sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+    constexpr auto sw32 = CU_TENSOR_MAP_SWIZZLE_32B;
     if (!encode_tokens(&mq, a.q, a, a.groups, a.qk_width) || !encode_tokens(&mk, a.k, a, a.groups, a.qk_width) ||
-        !encode_bf16<4>(&mo, p.dout, {a.v_width, a.heads, a.seqlen, a.batch}, {kPieceRows, 1, kC, 1}, sw64) ||
-        !encode_bf16<3>(&mv, ws.dv, {pp, kC, units2}, {kPieceRows, kC, 1}, sw64) ||
-        !encode_bf16<3>(&mr, ws.r, {pp, kC, units2}, {kPieceRows, kC, 1}, sw64) ||
+        !encode_bf16<4>(&mo, p.dout, {a.v_width, a.heads, a.seqlen, a.batch}, {kPieceRows, 1, kC, 1}, sw32) ||
+        !encode_bf16<3>(&mv, ws.dv, {pp, kC, units2}, {kPieceRows, kC, 1}, sw32) ||
+        !encode_bf16<3>(&mr, ws.r, {pp, kC, units2}, {kPieceRows, kC, 1}, sw32) ||
         !encode_bf16<3>(&m0, ws.s0, state, {kPieceRows * 8, 8 * NT, 1}, CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !encode_bf16<3>(&m1, ws.ds1, state, {kPieceRows * 8, 8 * NT, 1}, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;

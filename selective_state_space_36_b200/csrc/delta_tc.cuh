@@ -25,6 +25,11 @@ __host__ __device__ constexpr uint32_t operand_col(uint32_t base, int kstep, int
     return base + 32 * (kstep >> 1) + 16 * term + 8 * (kstep & 1);
 }
 
+// Before an arrival that gives shared memory back whose values nothing stored
+// before the arrival depends on: without it, reads a warp had issued still
+// returned what the next copy brought (seen in delta_fused_grad.cu's <S0, dS1>).
+__device__ __forceinline__ void reads_done() { __threadfence_block(); }
+
 template <int N>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>

@@ -36,7 +36,7 @@ enum : uint32_t { kMajorK = 0, kMajorMN = 1 };
 // Shared-memory matrix descriptor (sm_100 format, version 1) of a tile starting
 // at byte address `addr` (the swizzle pattern's start plus an in-row offset for K
 // steps of K-major operands).
-enum : uint32_t { kSwizzleNone = 0, kSwizzle128 = 2, kSwizzle64 = 4 };
+enum : uint32_t { kSwizzleNone = 0, kSwizzle128 = 2, kSwizzle32 = 6 };
 __device__ __forceinline__ uint64_t desc_tile(uint32_t addr, uint32_t lbo_bytes, uint32_t sbo_bytes, uint32_t layout) {
     uint64_t d = 0;
     d |= (uint64_t)((addr >> 4) & 0x3FFFu);
