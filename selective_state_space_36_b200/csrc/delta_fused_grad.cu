@@ -88,14 +88,22 @@ struct GradTcArgs {
 };
 
 // The heads that a block goes through: chunks blockIdx.x, blockIdx.x + gridDim.x, ...,
-// each with its group's heads.
+// each with its group's heads.  Starts before the first of them.
 struct Walk {
-    unsigned w, turn = 0;       // chunk; how many before it
-    int hh = 0;                 // head in the group
-    int64_t token, unit;        // the chunk's first token, counted over the batch; place in the workspace
+    unsigned w, turn = ~0u;     // chunk; how many before it
+    int hh;                     // head in the group
+    int64_t token, unit = 0;    // the chunk's first token, counted over the batch; place in the workspace
     int b, t0, gr, live;
-    __device__ __forceinline__ explicit Walk(const GradTcArgs &a) : w(blockIdx.x) { chunk(a); }
-    __device__ __forceinline__ void chunk(const GradTcArgs &a) {
+    __device__ __forceinline__ explicit Walk(const GradTcArgs &a) : w(blockIdx.x - gridDim.x), hh(a.rep - 1) {}
+    // The next head; false if there is none.  (One use per role: its divisions are a
+    // large part of a role's code, and all of it has to stay in the instruction cache.)
+    __device__ __forceinline__ bool next(const GradTcArgs &a) {
+        unit += a.nch;
+        if (++hh < a.rep) return true;
+        hh = 0;
+        ++turn;
+        w += gridDim.x;
+        if (w >= a.chunks) return false;
         const unsigned bg = w / a.nch, ch = w - bg * a.nch;
         b = (int)(bg / (unsigned)a.groups);
         gr = (int)(bg - (unsigned)b * (unsigned)a.groups);
@@ -103,20 +111,11 @@ struct Walk {
         token = b * a.seqlen + t0;
         live = (int)(a.seqlen - t0 < kC ? a.seqlen - t0 : kC);
         unit = ((int64_t)b * a.heads + gr * a.rep) * a.nch + ch;
+        return true;
     }
-    __device__ __forceinline__ bool done(const GradTcArgs &a) const { return w >= a.chunks; }
     __device__ __forceinline__ bool first() const { return hh == 0; }
     __device__ __forceinline__ bool last(const GradTcArgs &a) const { return hh + 1 == a.rep; }
     __device__ __forceinline__ int head(const GradTcArgs &a) const { return gr * a.rep + hh; }
-    __device__ __forceinline__ void next(const GradTcArgs &a) {
-        unit += a.nch;
-        if (++hh == a.rep) {
-            hh = 0;
-            ++turn;
-            w += gridDim.x;
-            if (w < a.chunks) chunk(a);
-        }
-    }
 };
 
 template <int NT>
@@ -173,7 +172,8 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
             constexpr uint32_t id_n = idesc_bf16(128, 64 * NT, kMajorK, kMajorMN);
             constexpr uint32_t id_t = idesc_bf16(128, 64 * NT, kMajorMN, kMajorMN);
             uint32_t piece = 0, j = 0;
-            for (Walk u(a); ok && !u.done(a); u.next(a), ++j) {
+            Walk u(a);
+            for (; ok && u.next(a); ++j) {
                 const int cs = u.turn & 1;
                 const uint32_t kq = smem_u32(sm.kq[cs][0]);
                 if (j > 0 && !(ok = wait(&sm.taken, j - 1))) break;
@@ -236,7 +236,8 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
             // -------------------------------------------------- the copies
             const uint32_t el = elect_one();
             uint32_t piece = 0, kqs = 0;
-            for (Walk u(a); ok && !u.done(a); u.next(a)) {
+            Walk u(a);
+            while (ok && u.next(a)) {
                 if (u.first()) {
                     const int cs = u.turn & 1;
                     if (u.turn >= 2 && !(ok = wait(&sm.kq_taken[cs], (u.turn - 2) >> 1))) break;
@@ -268,6 +269,15 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                             tma_load_3d(to.s[term], &mapS0, 8 * x, 0, unit2 + term, bar);
                             tma_load_3d(to.s[2 + term], &mapS1, 8 * x, 0, unit2 + term, bar);
                         }
+                        // The states of the pieces that have no slot yet come into L2 meanwhile: all
+                        // blocks load in the same phase of a unit, and without this wait for
+                        // HBM then and leave it idle in the others (245 us).
+                        if (i < kSlots && i + kSlots < pieces)
+#pragma unroll 1
+                            for (int term = 0; term < 2; ++term) {
+                                tma_prefetch_3d(&mapS0, 8 * (x + kSlots * kPieceRows), 0, unit2 + term);
+                                tma_prefetch_3d(&mapS1, 8 * (x + kSlots * kPieceRows), 0, unit2 + term);
+                            }
                     }
                 }
             }
@@ -303,12 +313,7 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                 *reinterpret_cast<float2 *>(&dec.beta[t]) = be;
                 signal(&sm.cum[turn & 1]);
             };
-            Walk ahead(a);  // two heads ahead
-            uint32_t j = 0;
-            for (uint32_t i = 0; i < 2 && !ahead.done(a); ++i, ahead.next(a)) decays(ahead, i);
-            for (Walk u(a); ok && !u.done(a); u.next(a), ++j) {
-                const int s = j & 1;
-                if (!(ok = wait(&sm.part[s], j >> 1))) break;
+            auto sums = [&](const Walk &u, int s) {
                 const GradDec &dec = sm.dec[s];
                 // lane i: tokens 63 - 2 i and 62 - 2 i; a prefix sum over lanes is a sum from the end
                 const int t1 = kC - 1 - 2 * lane;
@@ -340,10 +345,16 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                     a.dbeta[at + (int64_t)(t1 - 1) * a.heads] = db[1];
                 }
                 __syncwarp();  // all lanes have read the head's sums and decays
-                if (!ahead.done(a)) {
-                    decays(ahead, j + 2);
-                    ahead.next(a);
+            };
+            Walk u(a), ahead(a);
+            bool more = true;
+            for (uint32_t j = 0;; ++j) {  // decays of head j, sums of head j - 2
+                const int s = j & 1;
+                if (j >= 2) {
+                    if (!u.next(a) || !(ok = wait(&sm.part[s], (j - 2) >> 1))) break;
+                    sums(u, s);
                 }
+                if (more && (more = ahead.next(a))) decays(ahead, j);
             }
         }
     } else if (warp >= kRowWarps) {
@@ -351,7 +362,8 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
         fewer_regs<kDotRegs>();
         const int at = tid - kRowWarps * 32;
         uint32_t piece = 0, j = 0;
-        for (Walk u(a); ok && !u.done(a); u.next(a), ++j) {
+        Walk u(a);
+        for (; ok && u.next(a); ++j) {
             float inner = 0.f;
             for (int i = 0; i < pieces; ++i, ++piece) {
                 const int st = piece % kSlots;
@@ -387,7 +399,8 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
         const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
         float sum[NT][32];  // dq or dk over the group's heads
         uint32_t j = 0;
-        for (Walk u(a); !u.done(a); u.next(a), ++j) {
+        Walk u(a);
+        for (; u.next(a); ++j) {
             const int s = j & 1, cs = u.turn & 1;
             const GradDec &dec = sm.dec[s];
             if (u.first())
