@@ -387,14 +387,15 @@ ssm_status ssm_ssd_scan_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *x, cons
  * multiple of groups.  A token with beta = 0 and g = 0 leaves the state as it
  * is, so rows of a padded batch end with the state of their last token.
  *
- * float32 tensors, and up to 32 tokens, go token by token in float32 without a
- * workspace.  bf16 sequences go in chunks of 64 tokens on the tensor cores, as
- * one kernel where dstate is 64 or 128, headdim a multiple of 64 and q, k, v and
- * out start 16-byte aligned (its bounded waits: bit 2 of the device status word).
- * With few heads the sequence is split into segments that run side by side;
- * workspace then, per head and segment, dstate (2 headdim + dstate) floats.
- * Other bf16 sequences take 33 KB of workspace per head and chunk.  The workspace
- * comes from the library's pool on "stream" (see ssm_selective_scan_fwd).
+ * float32 tensors, and up to 16 tokens, go token by token in float32 without a
+ * workspace.  Longer bf16 sequences go in chunks of 64 tokens on the tensor
+ * cores (bounded waits: bit 2 of the device status word; the outputs are not
+ * valid if one ran out).  Workspace, from the library's pool on "stream" (see
+ * ssm_selective_scan_fwd): with few heads the sequence is split into segments
+ * that run side by side, dstate (2 headdim + dstate) floats per head and
+ * segment; and copies of those of q, k, v and out whose rows (dstate or headdim
+ * values) are not multiples of 16 bytes on 16-byte boundaries.  out must not
+ * overlap an input.
  */
 ssm_status ssm_delta_rule_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, const void *k, const void *v,
                               const float *g, const float *beta, float scale, void *out, float *last_state,
@@ -410,12 +411,13 @@ ssm_status ssm_delta_rule_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, co
  *   dv        : (batch, seqlen, heads, headdim) io
  *   dg, dbeta : (batch, seqlen, heads) float32
  *   dh0       : (batch, heads, headdim, dstate) float32 or NULL (not computed).
- * headdim <= 128 here (SSM_ERR_UNSUPPORTED above).  No atomics: equal inputs give equal bits.  The states
- * are recomputed: the workspace holds, per head and chunk of 64 tokens, two
- * states and two (64, headdim) arrays at 4 bytes per value and 33 KB besides
- * (float32 tensors: a state per 16 tokens, and per token and head headdim +
- * 2 dstate floats), from the library's pool on "stream".  Outputs must not
- * overlap each other or any input.
+ * headdim <= 128 here (SSM_ERR_UNSUPPORTED above).  No atomics: equal inputs
+ * give equal bits.  The states are recomputed: the workspace holds, per head
+ * and chunk of 64 tokens, two states and two (64, headdim) arrays at 4 bytes per
+ * value, headdim rounded up to 64 and dstate to 64 or 128, and 33 KB besides,
+ * and padded copies as in the forward pass (float32 tensors: a state per 16
+ * tokens, and per token and head headdim + 2 dstate floats), from the library's
+ * pool on "stream".  Outputs must not overlap each other or any input.
  */
 ssm_status ssm_delta_rule_bwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, const void *k, const void *v,
                               const float *g, const float *beta, float scale, const float *h0, const void *dout,

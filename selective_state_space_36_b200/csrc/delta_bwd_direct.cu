@@ -1,5 +1,5 @@
 // delta_bwd_direct.cu -- the gated delta rule's gradient in float32 throughout,
-// for float32 tensors (the formulas of delta_bwd.cu on chunks of kDeltaStep
+// for float32 tensors (the formulas of delta_fused_bwd.cu on chunks of kDeltaStep
 // tokens, with a state per chunk from launch_delta_recurrent).
 //
 // One block per (batch row, head) walks backwards over the chunks; dS and S0
@@ -8,6 +8,9 @@
 // headdim (in dq, dk, dg, dbeta) and all of dstate (in e), so a head is not
 // divided over blocks.  e solves e = dU - Abar^T (beta e) by substitution from
 // the last token, one thread per column of V.
+//
+// Measured: 3 sequences of 600 tokens, 16 heads of 100 x 80: 2050 us, 54 us per 16
+// tokens; bound by the latency of the products' shared-memory loops (48 blocks).
 #include "delta_rule.cuh"
 #include "kernel_setup.cuh"
 #include "ssm_device.cuh"

@@ -1,6 +1,6 @@
-// delta_chunk.cuh -- device helpers shared by the chunked kernels of the gated
-// delta rule: the chunk workspace, warp-level bf16 matrix products with
-// operands split into two bf16 terms, and the loads of a chunk's tiles.
+// delta_chunk.cuh -- what the chunked kernels of the gated delta rule share: the
+// chunk workspace, values split into two bf16 terms, warp-level matrix products,
+// and their launchers.
 //
 // Chunks of C = 64 tokens.  With G_t the sum of the log decays of the chunk's
 // tokens up to t and Gam_ts = exp(G_t - G_s) for s <= t, the definition's
@@ -16,14 +16,12 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "cp_async.cuh"
 #include "delta_rule.cuh"
 
 namespace ssm {
 namespace delta {
 
 constexpr int kC = 64;        // tokens per chunk
-constexpr int kMatLd = 72;    // row stride of a 64 x 64 bf16 tile in shared memory (conflict-free ldmatrix)
 constexpr int kMats = 4;      // per chunk and head: M, Pb (high terms), M, Pb (low terms), each 64 x 64
 constexpr int kDec = 3;       // per chunk and head: exp(G_t), exp(G_C - G_t), beta_t (zero behind the end)
 
@@ -39,16 +37,6 @@ __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], const bf16 *p) {
     const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-__device__ __forceinline__ void stm4t(bf16 *p, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-    const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n"
-                 ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
-}
-__device__ __forceinline__ void stm4(bf16 *p, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-    const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};\n"
-                 ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
 }
 // an 8 x 8 block of 16-bit values, transposed within the warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -81,18 +69,16 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
     lo = pack(x - low_of(hi), y - high_of(hi));
 }
 
-// Row and column this lane addresses in a 16 x 16 block of ldmatrix.x4:
-// "rows first" gives registers (rows 0-7, 8-15) x (columns 0-7) then columns
-// 8-15; "columns first" the columns of rows 0-7, then those of rows 8-15.
+// Row and column this lane addresses in a 16 x 16 block of ldmatrix.x4 whose
+// registers are (rows 0-7, 8-15) x (columns 0-7), then columns 8-15.
 __device__ __forceinline__ int rows_first_row(int lane) { return (lane & 7) + ((lane >> 3) & 1) * 8; }
 __device__ __forceinline__ int rows_first_col(int lane) { return (lane >> 4) * 8; }
-__device__ __forceinline__ int cols_first_row(int lane) { return (lane & 7) + (lane >> 4) * 8; }
-__device__ __forceinline__ int cols_first_col(int lane) { return ((lane >> 3) & 1) * 8; }
 
 // A stored state: two bf16 terms, each as (NP / 8, pp, 8) -- the eight columns of
 // a group row after row, so that neither a thread per row nor a quad per row
 // spreads a store over more lines than its bytes fill (row-major, the forward's
-// recomputation spent two thirds of its time in these stores).
+// recomputation took 281 us instead of 217).  It is also the matrix instructions'
+// layout of an unswizzled right operand, columns first.
 template <int NP>
 __device__ __forceinline__ int64_t state_at(int pp, int term, int row, int col) {
     return ((int64_t)(term * (NP / 8) + (col >> 3)) * pp + row) * 8 + (col & 7);

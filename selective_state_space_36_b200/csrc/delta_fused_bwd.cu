@@ -1,5 +1,24 @@
-// delta_fused_bwd.cu -- the pass backwards in time of the chunked gated delta
-// rule's gradient (formulas at delta_bwd.cu) on the sm_100a tensor cores.
+// delta_fused_bwd.cu -- the chunked gated delta rule's gradient, its pass
+// backwards in time, on the sm_100a tensor cores.
+//
+// The gradient, notation of delta_chunk.cuh, with gam = exp G, w = exp(G_C - G) and
+// dS1 the gradient of the state leaving a chunk:
+//   z   = Pb^T dO + w beta K dS1^T,   dV = z - M^T z
+//   dS0 = gam_C dS1 + (scale gam dO)^T Q - (gam dV)^T K
+// runs from the last chunk to the first and needs no state (this kernel; it leaves
+// dS1 and dV of each chunk in the workspace).  Then, for all chunks at once
+// (delta_fused_grad.cu), with S0 and r from the forward's recomputation
+// (delta_fused.cu) and x = scale lower(Gam o (dO r^T)), y = -strict_lower(Gam o (dV r^T)),
+// X = x beta, E = y beta (columns scaled):
+//   dQ = scale gam dO S0 + X K
+//   dK = L + R,  L = E K - gam dV S0,  R = X^T Q + E^T K + w beta r dS1
+//   dbeta_s = sum_t x_ts q_t . k_s + sum_t y_ts k_t . k_s + w_s (r dS1)_s . k_s
+// (beta enters R alone, as a factor of its row s: dbeta_s = k_s . R_s / beta_s,
+// without the division),
+//   dG_t = q_t . dq_t + k_t . (L_t - R_t),  dG_C += <S1, dS1>
+//   dg_t = sum of dG over the chunk's tokens from t on
+// dG needs no difference of large sums: its terms are row products that exist
+// anyway, and <S1, dS1> = gam_C <S0, dS1> + sum_t w beta (r dS1)_t . k_t.
 //
 // The forward kernel's mirror image (delta_fused.cu): one CTA has a head's state
 // rows as the 128 lanes of tensor memory and walks over the chunks from the last
@@ -16,6 +35,10 @@
 // Warps: 0-7 row-wise work (two per lane quarter, each half of the columns), 8
 // issues the products, 9 the TMA copies, 10 the decays.  They meet at mbarriers
 // only; every wait is bounded and reports through the device status word.
+//
+// Measured: 4 sequences of 2048 tokens, 32 heads of 128 x 128: 168 us, 5.2 us a chunk
+// (391 us on the warp-level matrix instructions).  Bound by that chain's latency,
+// tensor pipe 23 % and HBM 46 % busy.
 #include "delta_chunk.cuh"
 #include "delta_tc.cuh"
 #include "kernel_setup.cuh"

@@ -21,6 +21,13 @@
 // <S0, dS1>, 12 issues the products, 13 the TMA copies, 14 the decays and the
 // sums dg and dbeta.  They meet at mbarriers only; every wait is bounded and
 // reports through the device status word.
+//
+// Measured: 4 sequences of 2048 tokens, 32 heads of 128 x 128 (4096 units of 208 KB): 231
+// us, 0.56 of HBM's copy rate (527 us on the warp-level matrix instructions).  A unit
+// takes 16000 clocks of an SM: 8000 for the pieces, whose loads the other blocks make
+// in the same phase, then X and E (3500), their products (2500) and the row-wise
+// end (1500), while only the next unit's first pieces load: there is no room in
+// shared memory for more of them, nor in tensor memory for a second set of sums.
 #include "delta_chunk.cuh"
 #include "delta_tc.cuh"
 #include "kernel_setup.cuh"
@@ -270,8 +277,9 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                             tma_load_3d(to.s[2 + term], &mapS1, 8 * x, 0, unit2 + term, bar);
                         }
                         // The states of the pieces that have no slot yet come into L2 meanwhile: all
-                        // blocks load in the same phase of a unit, and without this wait for
-                        // HBM then and leave it idle in the others (245 us).
+                        // blocks load in the same phase of a unit and without this would wait for
+                        // HBM then and leave it idle in the others (245 us; the rows of dO, dV and r
+                        // too: no gain, their first halves bring the lines).
                         if (i < kSlots && i + kSlots < pieces)
 #pragma unroll 1
                             for (int term = 0; term < 2; ++term) {
