@@ -52,7 +52,8 @@ struct DeltaBwdArgs {
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool bf16, cudaStream_t st);
 
 // Gradients of float32 tensors, headdim and dstate up to kDeltaMaxDstate;
-// f.marks and f.r hold what launch_delta_recurrent stored.
-cudaError_t launch_delta_bwd_direct(const DeltaBwdArgs &a, cudaStream_t st);
+// f.marks and f.r hold what launch_delta_recurrent stored.  Workspace: ds1 of the
+// shape of f.marks, es of that of f.r.
+cudaError_t launch_delta_bwd_direct(const DeltaBwdArgs &a, float *ds1, float *es, cudaStream_t st);
 
 }  // namespace ssm

@@ -1096,14 +1096,15 @@ ssm_status ssm_delta_rule_bwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, co
     } else {
         const size_t marks = (size_t)units * dims.headdim * dims.dstate, r = (size_t)tokens * dims.heads * dims.headdim;
         const size_t per_head = (size_t)tokens * dims.heads * dims.dstate;
-        e = workspace_alloc(&mem, 4 * (marks + r + 2 * per_head), st);
+        e = workspace_alloc(&mem, 4 * (2 * marks + 2 * r + 2 * per_head), st);
         if (e != cudaSuccess) return cuda_fail(e, "delta rule workspace allocation");
         p.f.marks = static_cast<float *>(mem);
         p.f.r = p.f.marks + marks;
-        p.dq_heads = p.f.r + r;
+        float *ds1 = p.f.r + r, *es = ds1 + marks;
+        p.dq_heads = es + r;
         p.dk_heads = p.dq_heads + per_head;
         e = ssm::launch_delta_recurrent(p.f, false, st);
-        if (e == cudaSuccess) e = ssm::launch_delta_bwd_direct(p, st);
+        if (e == cudaSuccess) e = ssm::launch_delta_bwd_direct(p, ds1, es, st);
     }
     cudaError_t ef = cudaFreeAsync(mem, st);
     if (e != cudaSuccess) return cuda_fail(e, "delta rule gradient launch");
