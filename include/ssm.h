@@ -386,6 +386,8 @@ ssm_status ssm_ssd_scan_fwd(ssm_ssd_dims dims, ssm_dtype io, const void *x, cons
  * 1 <= dstate <= 128 (SSM_ERR_UNSUPPORTED above); any headdim, heads a
  * multiple of groups.  A token with beta = 0 and g = 0 leaves the state as it
  * is, so rows of a padded batch end with the state of their last token.
+ * A NaN reaches what follows it in its head, and in bf16 sequences of more than
+ * 16 tokens also the tokens before it in its chunk of 64.
  *
  * float32 tensors, and up to 16 tokens, go token by token in float32 without a
  * workspace.  Longer bf16 sequences go in chunks of 64 tokens on the tensor

@@ -13,8 +13,8 @@
 //
 // Measured: 3 sequences of 600 tokens, 16 heads of 100 x 80: 372 us backwards (9.8 us
 // per 16 tokens, bound by their chain of steps) and 177 us for the rest (bound by
-// shared-memory reads, 5 per 12 products); one kernel that
-// walked over the chunks with a head per block took 2050 us.
+// shared-memory reads, 5 per 12 products); one kernel that walked over the chunks
+// with a head per block took 2050 us.
 #include "delta_rule.cuh"
 #include "kernel_setup.cuh"
 #include "ssm_device.cuh"
@@ -41,7 +41,7 @@ __device__ __forceinline__ float2 token_decay(const DeltaArgs &a, int64_t token,
 
 // A chunk's decays from its tokens', warp-wide (lanes 0 to kT - 1).
 __device__ __forceinline__ void chunk_decays(float2 gb, int lane, double *cum, float *gam, float *wend, float *beta) {
-    double sum = fmax((double)gb.x, -1e4);
+    double sum = log_decay(gb.x);
 #pragma unroll
     for (int o = 1; o < kT; o <<= 1) {
         const double up = __shfl_up_sync(0xffffffffu, sum, o);

@@ -31,8 +31,8 @@
 // through the device status word.
 //
 // Measured: 8 sequences of 2048 tokens, 32 heads of 128 x 128: 345 us (256 CTAs, two
-// waves of the SMs; 5.4 us a chunk), against 67 us for the bytes and 52 us for
-// the products.  Bound by the latency of a chunk's chain: state -> X -> R -> Y -> w
+// waves of the SMs; 5.4 us a chunk), against 67 us for the bytes and 42 us for
+// the recurrence's operations.  Bound by the latency of a chunk's chain: state -> X -> R -> Y -> w
 // beta r -> state, four products (tensor pipe busy 30 % of the time) with row-wise
 // steps between them.  One sequence of 32768 tokens, 16 heads of 64 x 128: 790 us in
 // six segments, 2045 us in one.  The same on the warp-level matrix instructions,
@@ -558,10 +558,8 @@ delta_fused_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_consta
         for (int c = 0; c < nch; ++c) {
             const int st = c & 1;
             Dec &dec = sm.dec[st];
-            // below -1e4 a decay is zero in float32 either way; the clamp keeps
-            // differences of two such sums finite
             constexpr double kLog2 = 1.4426950408889634;
-            const double d0 = kLog2 * fmax((double)gv[0], -1e4), d1 = kLog2 * fmax((double)gv[1], -1e4);
+            const double d0 = kLog2 * log_decay(gv[0]), d1 = kLog2 * log_decay(gv[1]);
             const float be2[2] = {bv[0], bv[1]};
             double sum = d0 + d1;
             if (c + 1 < nch) fetch(c + 1);

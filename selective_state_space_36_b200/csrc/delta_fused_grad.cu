@@ -306,7 +306,7 @@ delta_fused_grad_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_c
                 const float2 ga = *reinterpret_cast<const float2 *>(d), we = *reinterpret_cast<const float2 *>(d + kC),
                              be = *reinterpret_cast<const float2 *>(d + 2 * kC);
                 constexpr double kLog2 = 1.4426950408889634;
-                const double d0 = kLog2 * fmax((double)g0, -1e4), d1 = kLog2 * fmax((double)g1, -1e4);
+                const double d0 = kLog2 * log_decay(g0), d1 = kLog2 * log_decay(g1);
                 double sum = d0 + d1;
 #pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {

@@ -15,6 +15,10 @@ namespace ssm {
 
 constexpr int kDeltaMaxDstate = 128;
 
+// A log decay, for sums over a chunk: below -1e4 the decay is zero in float32
+// either way, and the clamp keeps differences of two such sums finite.  NaN stays.
+__device__ __forceinline__ double log_decay(float g) { return g < -1e4f ? -1e4 : (double)g; }
+
 struct DeltaArgs {
     const void *q, *k, *v;     // (batch, seqlen, groups, dstate) x 2, (batch, seqlen, heads, headdim)
     const float *g, *beta;     // (batch, seqlen, heads)

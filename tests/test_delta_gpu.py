@@ -312,6 +312,26 @@ def test_padding_forgetting_and_written_range(lib, seqlen):
 
 
 @gpu
+@pytest.mark.parametrize("seqlen,io", [(12, "bf16"), (300, "bf16"), (300, "f32")])
+def test_nan_reaches_what_follows_and_no_other_head(lib, seqlen, io):
+    """A NaN log decay or value makes the rest of its head NaN, not the chunks
+    before it (64 tokens) and no other head."""
+    at = seqlen // 2
+    for name in ("g", "v"):
+        x = R.delta_inputs(2, seqlen, 4, 2, 64, 64, io, 53)
+        x[name][1, at, 2] = float("nan")
+        d = dev(x)
+        end = d["h0"].clone()
+        out = lib.delta_rule_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], last_state=end).isnan().cpu()
+        got = lib.delta_rule_bwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["dout"], h0=d["h0"], dlast_state=d["dend"])
+        assert out[1, at:, 2].all() and end[1, 2].isnan().all()
+        out[1, at // 64 * 64:, 2] = False
+        assert not out.any() and not end[0].isnan().any() and not end[1, [0, 1, 3]].isnan().any()
+        assert got["dg"][1, :, 2].isnan().any() and not got["dg"][0].isnan().any()
+        assert not got["dv"][1, :, [0, 1, 3]].isnan().any()
+
+
+@gpu
 def test_unaligned_tensors(lib):
     """Tensors one element off any vector alignment give the same results."""
     x = R.delta_inputs(1, 130, 2, 1, 64, 64, "bf16", 13)
