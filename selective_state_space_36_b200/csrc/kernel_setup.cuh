@@ -44,4 +44,30 @@ cudaError_t resident_blocks(int *per_sm) {
     return cudaSuccess;
 }
 
+// A kernel that follows another one of the same call may be launched before that
+// has ended (programmatic dependent launch): its launch and set-up, 2 to 3 us,
+// then lie under the other's end.  The first calls next_may_start() as soon as
+// it likes; the second calls previous_done() in every thread before it reads
+// what the first wrote or writes what the first reads.  (For kernels whose blocks
+// fill an SM it gains nothing: the early blocks of the gated delta rule's chain
+// cost 1 to 5 %.)
+__device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), int64_t blocks, unsigned threads, size_t smem, cudaStream_t st,
+                             const A &...args) {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = dim3((unsigned)blocks);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    c.attrs = attr;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 }  // namespace ssm

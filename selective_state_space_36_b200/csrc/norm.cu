@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(NormArgs a) {
     int flip = 0;
     const int lane = threadIdx.x % TPR, slot = threadIdx.x / TPR;
     const float inv = 1.f / a.dim;
+    next_may_start();
     float w[NV][VEC], bias[NV][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -480,12 +481,14 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_columns_kernel(NormArgs a) 
 __global__ void __launch_bounds__(1024) norm_bwd_reduce_kernel(const float *partial, int parts, int dim,
                                                                float *dweight, float *dbias) {
     __shared__ float s[32][33];
-    float *dst = blockIdx.y ? dbias : dweight;
+    const int which = blockIdx.x & 1, tile = blockIdx.x >> 1;
+    float *dst = which ? dbias : dweight;
+    previous_done();
     if (!dst) return;
-    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, col = tile * 32 + lane;
     float sum = 0.f;
     if (col < dim) {
-        const float *src = partial + (int64_t)blockIdx.y * parts * dim + col;
+        const float *src = partial + (int64_t)which * parts * dim + col;
 #pragma unroll 4
         for (int p = part; p < parts; p += 32) sum += src[(int64_t)p * dim];
     }
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_reduce_kernel(const float *part
     sum = s[lane][part];  // column `part` of the block, its 32 sums over the lanes
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0 && blockIdx.x * 32 + part < dim) dst[blockIdx.x * 32 + part] = sum;
+    if (lane == 0 && tile * 32 + part < dim) dst[tile * 32 + part] = sum;
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -633,9 +636,8 @@ cudaError_t bwd_t(NormArgs a, int sms, NormAlloc alloc, cudaStream_t st) {
     }
     if (!a.partial) return e;
     if (e == cudaSuccess) {
-        const dim3 grid((unsigned)((a.dim + 31) / 32), 2);
-        norm_bwd_reduce_kernel<<<grid, 1024, 0, st>>>(a.partial, (int)p.parts, a.dim, a.dweight, a.dbias);
-        e = cudaGetLastError();
+        e = launch_dependent(norm_bwd_reduce_kernel, 2 * ((a.dim + 31) / 32), 1024, 0, st, a.partial, (int)p.parts, a.dim,
+                             a.dweight, a.dbias);
     }
     const cudaError_t ef = cudaFreeAsync(a.partial, st);
     return e != cudaSuccess ? e : ef;
