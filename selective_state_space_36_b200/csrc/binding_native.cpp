@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -46,8 +47,9 @@ struct Args {
         }
         return t.numel() ? t.data_ptr() : nullptr;
     }
+    // (past the dispatcher, which takes as long again as the allocator)
     at::Tensor empty(at::ScalarType type, at::IntArrayRef shape) const {
-        return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+        return at::detail::empty_cuda(shape, type, dev, std::nullopt);
     }
     ssm_stream stream() const {
         return reinterpret_cast<ssm_stream>(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
