@@ -13,8 +13,8 @@
 // flops per state value, so the step is bound by HBM: the loads of all
 // kRows sets are issued before the first is used (256 sequences x 32 heads of
 // 128 x 128: 165 us, the measured copy rate).  Over a sequence the state stays
-// in registers and the chain of a token's dot products bounds the kernel; k,
-// q, v, g and beta come a stage of kTok tokens ahead through shared memory.
+// in registers and the chain of dot products bounds the kernel, two tokens a
+// link; k, q, v, g and beta come a stage of kTok tokens ahead through shared memory.
 #include "cp_async.cuh"
 #include "delta_rule.cuh"
 #include "ssm_device.cuh"
@@ -197,6 +197,7 @@ struct TokenStage {
     T k[kTok][32 * PIECES], q[kTok][32 * PIECES];
     T v[kTok][kRowsPerBlock];
     float decay[kTok], beta[kTok];
+    float4 pair[kTok / 2];  // of tokens 1, 2: k1 . k2, k1 . q1, k1 . q2, k2 . q2
 };
 
 // A sequence.  ASYNC: rows of q and k are multiples of 16 bytes and start
@@ -232,10 +233,11 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
                     cp_async16(&st.q[t][c], in ? q + at : q, in);
                 }
             } else {
-                for (int i = tid; i < live * 32 * PIECES; i += kThreads) {
+                for (int i = tid; i < kTok * 32 * PIECES; i += kThreads) {
                     const int t = i / (32 * PIECES), c = i % (32 * PIECES);
-                    st.k[t][c] = c < n ? k[(t0 + t) * qk_ld + c] : T(0.f);
-                    st.q[t][c] = c < n ? q[(t0 + t) * qk_ld + c] : T(0.f);
+                    const bool in = t < live && c < n;
+                    st.k[t][c] = in ? k[(t0 + t) * qk_ld + c] : T(0.f);
+                    st.q[t][c] = in ? q[(t0 + t) * qk_ld + c] : T(0.f);
                 }
             }
         }
@@ -252,9 +254,10 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
             const int t = (tid + i * kThreads) / kRowsPerBlock, c = tid % kRowsPerBlock;
             rv[i] = t0 + t < a.seqlen && c < have ? v[(t0 + t) * v_ld + c] : T(0.f);
         }
-        if (tid < kTok && t0 + tid < a.seqlen) {
-            rg = g[(t0 + tid) * a.heads];
-            rb = beta[(t0 + tid) * a.heads];
+        if (tid < kTok) {  // behind the end: tokens that leave the state as it is
+            const bool in = t0 + tid < a.seqlen;
+            rg = in ? g[(t0 + tid) * a.heads] : 0.f;
+            rb = in ? beta[(t0 + tid) * a.heads] : 0.f;
         }
     };
     auto small_stores = [&](int64_t t0) {
@@ -268,18 +271,15 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
     };
 
     static_assert(kThreads % kRowsPerBlock == 0, "a thread stays in its column of v");
-    float s[kRows][PIECES][4], kk[2][PIECES][4], qq[2][PIECES][4], vv[2][kRows];
-#pragma unroll
-    for (int p = 0; p < PIECES; ++p)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) qq[1][p][e] = 0.f;  // there is no token before the first
-    auto put_out = [&](int64_t t, const float *o) {
-        if (STORE || sub != 0) return;
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-            if (row0 + 4 * r < a.headdim)
-                io_traits<T>::store(static_cast<T *>(a.out) + ((b * a.seqlen + t) * a.heads + h) * a.headdim + row0 + 4 * r,
-                                    a.scale * o[r]);
+    float s[kRows][PIECES][4];
+    auto put_out = [&](int64_t t, int r, float o) {
+        if (!STORE && sub == 0 && row0 + 4 * r < a.headdim)
+            io_traits<T>::store(static_cast<T *>(a.out) + ((b * a.seqlen + t) * a.heads + h) * a.headdim + row0 + 4 * r,
+                                a.scale * o);
+    };
+    auto put_r = [&](int64_t t, int r, float res) {
+        if (STORE && sub == 0 && row0 + 4 * r < a.headdim)
+            a.r[((b * a.seqlen + t) * a.heads + h) * a.headdim + row0 + 4 * r] = res;
     };
     issue(0);
     small_loads(0);
@@ -300,64 +300,88 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
                     put_row<PIECES, VEC>(a.marks + ((bh * marks + t0 / kTok) * a.headdim + row) * n, s[r], sub, n);
             }
         }
-        const TokenStage<T, PIECES> &st = stages[(t0 / kTok) & 1];
+        TokenStage<T, PIECES> &st = stages[(t0 / kTok) & 1];
         const int live = (int)(a.seqlen - t0 < kTok ? a.seqlen - t0 : kTok);
-        // Slot t % 2 of the registers holds token t's operands.  A token's S k and the
-        // last token's S q read the same state, so their sums go through one set of
-        // shuffles.
-        auto operands = [&](int t, int at) {
+        {  // the pairs' products: 8 x 4 of them, four threads each
+            const int pair = tid >> 4, which = (tid >> 2) & 3, from = tid & 3;
+            const T *x = which == 3 ? st.k[2 * pair + 1] : st.k[2 * pair];
+            const T *y = which == 0 ? st.k[2 * pair + 1] : st.q[2 * pair + (which > 1)];
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int p = 0; p < PIECES; ++p) {
-                io_traits<T>::load4_smem(&st.k[t][4 * (sub + kLanes * p)], kk[at][p]);
-                io_traits<T>::load4_smem(&st.q[t][4 * (sub + kLanes * p)], qq[at][p]);
+            for (int i = 0; i < 2 * PIECES; ++i) {
+                float xv[4], yv[4];
+                io_traits<T>::load4_smem(x + 4 * (from + 4 * i), xv);
+                io_traits<T>::load4_smem(y + 4 * (from + 4 * i), yv);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[e] = fmaf(xv[e], yv[e], d[e]);
             }
+            float sum = (d[0] + d[1]) + (d[2] + d[3]);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            static_assert(kThreads == kTok / 2 * 16, "four threads a product");
+            if (from == 0) (&st.pair[pair].x)[which] = sum;
+        }
+        __syncthreads();
+        float k1[PIECES][4], k2[PIECES][4], q1[PIECES][4], q2[PIECES][4];
+        auto row_of = [&](const T *x, float (&v)[PIECES][4]) {
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) vv[at][r] = io_traits<T>::load_smem(&st.v[t][mine + 4 * r]);
+            for (int p = 0; p < PIECES; ++p) io_traits<T>::load4_smem(x + 4 * (sub + kLanes * p), v[p]);
         };
-        operands(0, 0);
-        // pairs of tokens, so that the slots are compile-time; more of them unrolled
-        // outgrow the instruction cache (16 tokens: 0.25 us each)
+        row_of(st.k[0], k1);
+        row_of(st.k[1], k2);
+        row_of(st.q[0], q1);
+        row_of(st.q[1], q2);
+        // Two tokens at a time: the state's products with both tokens' k and q go
+        // through one set of shuffles, and the second token's come from the first's,
+        //   S1 x = a1 S x + u1 (k1 . x),  S2 = a1 a2 S + a2 u1 k1 + u2 k2.
+        // (One at a time: 245 ns a token, most of it the shuffles' latency.)
 #pragma unroll 1
-        for (int pair = 0; pair < live; pair += 2)
+        for (int t = 0; t < live; t += 2) {
+            const float2 dec = *reinterpret_cast<const float2 *>(&st.decay[t]), be = *reinterpret_cast<const float2 *>(&st.beta[t]);
+            const float4 c = st.pair[t / 2];
+            float sums[4 * kRows], vv[2][kRows];
 #pragma unroll
-            for (int at = 0; at < 2; ++at) {
-                const int t = pair + at;
-                if (t >= live) break;
-                const float decay = st.decay[t], beta_t = st.beta[t];
-                float sums[2 * kRows];
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    sums[kRows + r] = row_dot<PIECES>(s[r], qq[at ^ 1]);
-#pragma unroll
-                    for (int p = 0; p < PIECES; ++p)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[r][p][e] *= decay;
-                    sums[r] = row_dot<PIECES>(s[r], kk[at]);
-                }
-                if (t + 1 < live) operands(t + 1, at ^ 1);
-                sum8<2 * kRows>(sums);
-                if (t0 + t > 0) put_out(t0 + t - 1, sums + kRows);
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    const float res = vv[at][r] - sums[r], u = beta_t * res;
-                    if (STORE && sub == 0 && row0 + 4 * r < a.headdim)
-                        a.r[((b * a.seqlen + t0 + t) * a.heads + h) * a.headdim + row0 + 4 * r] = res;
-#pragma unroll
-                    for (int p = 0; p < PIECES; ++p)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[r][p][e] = fmaf(u, kk[at][p][e], s[r][p][e]);
+            for (int r = 0; r < kRows; ++r) {
+                vv[0][r] = io_traits<T>::load_smem(&st.v[t][mine + 4 * r]);
+                vv[1][r] = io_traits<T>::load_smem(&st.v[t + 1][mine + 4 * r]);
+                sums[4 * r] = row_dot<PIECES>(s[r], k1);
+                sums[4 * r + 1] = row_dot<PIECES>(s[r], k2);
+                if (!STORE) {
+                    sums[4 * r + 2] = row_dot<PIECES>(s[r], q1);
+                    sums[4 * r + 3] = row_dot<PIECES>(s[r], q2);
+                } else {
+                    sums[4 * r + 2] = sums[4 * r + 3] = 0.f;
                 }
             }
+            const int next = t + 2 < live ? t + 2 : t;
+            if (!STORE) {
+                row_of(st.q[next], q1);
+                row_of(st.q[next + 1], q2);
+            }
+            sum8<4 * kRows>(sums);
+            const float both = dec.x * dec.y;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float *d = sums + 4 * r;
+                const float r1 = fmaf(-dec.x, d[0], vv[0][r]), u1 = be.x * r1;
+                const float r2 = fmaf(-dec.y, fmaf(u1, c.x, dec.x * d[1]), vv[1][r]), u2 = be.y * r2;
+                const float w1 = dec.y * u1;
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[r][p][e] = fmaf(u2, k2[p][e], fmaf(w1, k1[p][e], both * s[r][p][e]));
+                put_r(t0 + t, r, r1);
+                put_out(t0 + t, r, fmaf(u1, c.y, dec.x * d[2]));
+                if (t + 1 < live) {
+                    put_r(t0 + t + 1, r, r2);
+                    put_out(t0 + t + 1, r, fmaf(u2, c.w, dec.y * fmaf(u1, c.z, dec.x * d[3])));
+                }
+            }
+            row_of(st.k[next], k1);
+            row_of(st.k[next + 1], k2);
+        }
         small_stores(t0 + kTok);
         __syncthreads();
-    }
-    {
-        float sums[kRows];
-        const bool odd = (a.seqlen - 1) & 1;  // the last token's slot
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) sums[r] = odd ? row_dot<PIECES>(s[r], qq[1]) : row_dot<PIECES>(s[r], qq[0]);
-        sum8<kRows>(sums);
-        put_out(a.seqlen - 1, sums);
     }
     if (!a.state) return;
 #pragma unroll
