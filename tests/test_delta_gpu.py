@@ -81,6 +81,9 @@ SHAPES = [
     (1, 1100, 2, 2, 7, 9, "bf16", "mixed", True),
     (2, 17, 2, 1, 24, 40, "bf16", "mixed", True),
     (1, 32, 2, 1, 25, 41, "bf16", "mixed", True),
+    (2, 35, 2, 1, 30, 96, "f32", "mixed", True),
+    (1, 19, 3, 3, 12, 70, "f32", "slow", True),
+    (1, 18, 2, 1, 20, 128, "f32", "mixed", False),
 ]
 
 
@@ -272,7 +275,7 @@ def test_resume_and_tokens_equal_one_pass(lib, io):
 @gpu
 @pytest.mark.parametrize("batch,heads,groups,headdim,dstate,io", [
     (1, 1, 1, 1, 1, "f32"), (3, 4, 2, 64, 128, "bf16"), (2, 6, 6, 128, 128, "bf16"), (5, 3, 1, 33, 20, "f32"),
-    (2, 2, 1, 17, 127, "bf16"), (1, 16, 16, 64, 128, "bf16"), (7, 2, 1, 256, 64, "bf16"), (2, 1, 1, 8, 33, "bf16")])
+    (2, 2, 1, 17, 127, "bf16"), (2, 2, 1, 17, 90, "bf16"), (3, 2, 2, 24, 96, "f32"), (1, 16, 16, 64, 128, "bf16"), (7, 2, 1, 256, 64, "bf16"), (2, 1, 1, 8, 33, "bf16")])
 def test_update(lib, batch, heads, groups, headdim, dstate, io):
     x = R.delta_inputs(batch, 1, heads, groups, headdim, dstate, io, 5)
     d = {n: v[:, 0].contiguous() if n not in ("h0", "dend") else v for n, v in dev(x).items()}
