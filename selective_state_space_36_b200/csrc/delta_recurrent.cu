@@ -82,11 +82,11 @@ __device__ __forceinline__ void put_row(float *dst, const float (&s)[PIECES][4],
 
 // The state rows of this lane, kRows sets; plain loads: the state may be
 // written back to the same place.
-template <int PIECES, bool VEC>
-__device__ __forceinline__ void get_rows(float (&s)[kRows][PIECES][4], const float *h0, int64_t bh, int row0,
+template <int PIECES, bool VEC, int ROWS>
+__device__ __forceinline__ void get_rows(float (&s)[ROWS][PIECES][4], const float *h0, int64_t bh, int row0,
                                          int headdim, int sub, int n) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
         const int row = row0 + 4 * r;
         const float *src = h0 ? h0 + (bh * headdim + row) * (int64_t)n : nullptr;
 #pragma unroll
@@ -192,10 +192,10 @@ __global__ void __launch_bounds__(kWarps * 32) delta_step_kernel(DeltaArgs a) {
 constexpr int kFewTokens = 4;  // up to this many go to delta_step_kernel
 constexpr int kTok = 16;       // tokens per stage of a sequence
 
-template <typename T, int PIECES>
+template <typename T, int PIECES, int ROWS>
 struct TokenStage {
     T k[kTok][32 * PIECES], q[kTok][32 * PIECES];
-    T v[kTok][kRowsPerBlock];
+    T v[kTok][kWarps * 4 * ROWS];
     float decay[kTok], beta[kTok];
     float4 pair[kTok / 2];  // of tokens 1, 2: k1 . k2, k1 . q1, k1 . q2, k2 . q2
 };
@@ -203,25 +203,25 @@ struct TokenStage {
 // A sequence.  ASYNC: rows of q and k are multiples of 16 bytes and start
 // aligned (copied asynchronously); VEC as above.  STORE: the backward pass's
 // first half (DeltaArgs::marks, r; no output).
-template <typename T, int PIECES, bool VEC, bool ASYNC, bool STORE>
+template <typename T, int PIECES, int ROWS, bool VEC, bool ASYNC, bool STORE>
 __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) {
-    __shared__ __align__(16) TokenStage<T, PIECES> stages[2];
-    constexpr int kThreads = kWarps * 32;
+    __shared__ __align__(16) TokenStage<T, PIECES, ROWS> stages[2];
+    constexpr int kThreads = kWarps * 32, kBlockRows = kWarps * 4 * ROWS;
     const int tid = threadIdx.x, lane = tid & 31, sub = lane & (kLanes - 1), n = a.dstate;
-    const int tiles = (a.headdim + kRowsPerBlock - 1) / kRowsPerBlock;
+    const int tiles = (a.headdim + kBlockRows - 1) / kBlockRows;
     const int64_t bh = blockIdx.x / tiles, b = bh / a.heads;
     const int tile = (int)(blockIdx.x % tiles), h = (int)(bh % a.heads), gr = h / (a.heads / a.groups);
-    const int first = tile * kRowsPerBlock, mine = (tid >> 5) * 4 * kRows + (lane >> 3), row0 = first + mine;
+    const int first = tile * kBlockRows, mine = (tid >> 5) * 4 * ROWS + (lane >> 3), row0 = first + mine;
     const int64_t qk_ld = (int64_t)a.groups * n, v_ld = (int64_t)a.heads * a.headdim;
     const T *q = static_cast<const T *>(a.q) + (b * a.seqlen * a.groups + gr) * n;
     const T *k = static_cast<const T *>(a.k) + (b * a.seqlen * a.groups + gr) * n;
     const T *v = static_cast<const T *>(a.v) + (b * a.seqlen * a.heads + h) * a.headdim + first;
     const float *g = a.g + b * a.seqlen * a.heads + h, *beta = a.beta + b * a.seqlen * a.heads + h;
-    const int have = a.headdim - first < kRowsPerBlock ? a.headdim - first : kRowsPerBlock;
+    const int have = a.headdim - first < kBlockRows ? a.headdim - first : kBlockRows;
 
     auto issue = [&](int64_t t0) {
         if (t0 < a.seqlen) {
-            TokenStage<T, PIECES> &st = stages[(t0 / kTok) & 1];
+            TokenStage<T, PIECES, ROWS> &st = stages[(t0 / kTok) & 1];
             const int live = (int)(a.seqlen - t0 < kTok ? a.seqlen - t0 : kTok);
             if (ASYNC) {
                 constexpr int E = 16 / sizeof(T), PER = 32 * PIECES / E;
@@ -245,13 +245,13 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
     };
     // v, g and beta have rows too short for asynchronous copies: loaded into
     // registers when a stage begins, put into the next stage's tile at its end
-    constexpr int kV = kTok * kRowsPerBlock / kThreads;
+    constexpr int kV = kTok * kBlockRows / kThreads;
     T rv[kV];
     float rg = 0.f, rb = 0.f;
     auto small_loads = [&](int64_t t0) {
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const int t = (tid + i * kThreads) / kRowsPerBlock, c = tid % kRowsPerBlock;
+            const int t = (tid + i * kThreads) / kBlockRows, c = tid % kBlockRows;
             rv[i] = t0 + t < a.seqlen && c < have ? v[(t0 + t) * v_ld + c] : T(0.f);
         }
         if (tid < kTok) {  // behind the end: tokens that leave the state as it is
@@ -261,17 +261,17 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
         }
     };
     auto small_stores = [&](int64_t t0) {
-        TokenStage<T, PIECES> &st = stages[(t0 / kTok) & 1];
+        TokenStage<T, PIECES, ROWS> &st = stages[(t0 / kTok) & 1];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) st.v[(tid + i * kThreads) / kRowsPerBlock][tid % kRowsPerBlock] = rv[i];
+        for (int i = 0; i < kV; ++i) st.v[(tid + i * kThreads) / kBlockRows][tid % kBlockRows] = rv[i];
         if (tid < kTok) {
             st.decay[tid] = expf(rg);
             st.beta[tid] = rb;
         }
     };
 
-    static_assert(kThreads % kRowsPerBlock == 0, "a thread stays in its column of v");
-    float s[kRows][PIECES][4];
+    static_assert(kThreads % kBlockRows == 0, "a thread stays in its column of v");
+    float s[ROWS][PIECES][4];
     auto put_out = [&](int64_t t, int r, float o) {
         if (!STORE && sub == 0 && row0 + 4 * r < a.headdim)
             io_traits<T>::store(static_cast<T *>(a.out) + ((b * a.seqlen + t) * a.heads + h) * a.headdim + row0 + 4 * r,
@@ -294,13 +294,13 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
             static_assert(kTok == kDeltaStep, "a stored state per stage");
             const int64_t marks = (a.seqlen + kTok - 1) / kTok;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
+            for (int r = 0; r < ROWS; ++r) {
                 const int row = row0 + 4 * r;
                 if (row < a.headdim)
                     put_row<PIECES, VEC>(a.marks + ((bh * marks + t0 / kTok) * a.headdim + row) * n, s[r], sub, n);
             }
         }
-        TokenStage<T, PIECES> &st = stages[(t0 / kTok) & 1];
+        TokenStage<T, PIECES, ROWS> &st = stages[(t0 / kTok) & 1];
         const int live = (int)(a.seqlen - t0 < kTok ? a.seqlen - t0 : kTok);
         {  // the pairs' products: 8 x 4 of them, four threads each
             const int pair = tid >> 4, which = (tid >> 2) & 3, from = tid & 3;
@@ -334,14 +334,14 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
         // Two tokens at a time: the state's products with both tokens' k and q go
         // through one set of shuffles, and the second token's come from the first's,
         //   S1 x = a1 S x + u1 (k1 . x),  S2 = a1 a2 S + a2 u1 k1 + u2 k2.
-        // (6 heads of 40 x 48: 182 ns a token; one at a time 245 ns.)
+        // (18 heads of 40 x 48: 170 ns a token; one at a time 245 ns.)
 #pragma unroll 1
         for (int t = 0; t < live; t += 2) {
             const float2 dec = *reinterpret_cast<const float2 *>(&st.decay[t]), be = *reinterpret_cast<const float2 *>(&st.beta[t]);
             const float4 c = st.pair[t / 2];
-            float sums[4 * kRows], vv[2][kRows];
+            float sums[4 * ROWS], vv[2][ROWS];
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
+            for (int r = 0; r < ROWS; ++r) {
                 vv[0][r] = io_traits<T>::load_smem(&st.v[t][mine + 4 * r]);
                 vv[1][r] = io_traits<T>::load_smem(&st.v[t + 1][mine + 4 * r]);
                 sums[4 * r] = row_dot<PIECES>(s[r], k1);
@@ -358,10 +358,10 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
                 row_of(st.q[next], q1);
                 row_of(st.q[next + 1], q2);
             }
-            sum8<4 * kRows>(sums);
+            sum8<4 * ROWS>(sums);
             const float both = dec.x * dec.y;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
+            for (int r = 0; r < ROWS; ++r) {
                 const float *d = sums + 4 * r;
                 const float r1 = fmaf(-dec.x, d[0], vv[0][r]), u1 = be.x * r1;
                 const float r2 = fmaf(-dec.y, fmaf(u1, c.x, dec.x * d[1]), vv[1][r]), u2 = be.y * r2;
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
     }
     if (!a.state) return;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
         const int row = row0 + 4 * r;
         if (row < a.headdim) put_row<PIECES, VEC>(a.state + (bh * a.headdim + row) * (int64_t)n, s[r], sub, n);
     }
@@ -394,34 +394,47 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
 bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 template <typename T, int PIECES, bool VEC, bool STORE>
-cudaError_t launch_pieces(const DeltaArgs &a, bool async, cudaStream_t st) {
+cudaError_t launch_pieces(const DeltaArgs &a, bool async, int sms, cudaStream_t st) {
     const int tiles = (a.headdim + kRowsPerBlock - 1) / kRowsPerBlock;
     const dim3 grid((unsigned)(a.batch * a.heads * tiles)), block(kWarps * 32);
-    if (a.seqlen <= kFewTokens && !STORE) delta_step_kernel<T, PIECES, VEC><<<grid, block, 0, st>>>(a);
-    else if (async) delta_tokens_kernel<T, PIECES, VEC, true, STORE><<<grid, block, 0, st>>>(a);
-    else delta_tokens_kernel<T, PIECES, VEC, false, STORE><<<grid, block, 0, st>>>(a);
+    if (a.seqlen <= kFewTokens && !STORE) {
+        delta_step_kernel<T, PIECES, VEC><<<grid, block, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    // One row set per warp where that still leaves SMs free: a warp's chain is shorter
+    // (18 heads of 40 x 48, 301 tokens: 52 us, two sets 56 us), the work of a row larger.
+    const int64_t small = a.batch * a.heads * ((a.headdim + kRowsPerBlock / 2 - 1) / (kRowsPerBlock / 2));
+    if (small <= sms) {
+        const unsigned blocks = (unsigned)small;
+        if (async) delta_tokens_kernel<T, PIECES, 1, VEC, true, STORE><<<blocks, block, 0, st>>>(a);
+        else delta_tokens_kernel<T, PIECES, 1, VEC, false, STORE><<<blocks, block, 0, st>>>(a);
+    } else if (async) {
+        delta_tokens_kernel<T, PIECES, kRows, VEC, true, STORE><<<grid, block, 0, st>>>(a);
+    } else {
+        delta_tokens_kernel<T, PIECES, kRows, VEC, false, STORE><<<grid, block, 0, st>>>(a);
+    }
     return cudaGetLastError();
 }
 
 template <typename T, bool STORE>
-cudaError_t launch_t(const DeltaArgs &a, cudaStream_t st) {
+cudaError_t launch_t(const DeltaArgs &a, int sms, cudaStream_t st) {
     const bool vec = a.dstate % 4 == 0 && aligned_to(a.q, 4 * sizeof(T)) && aligned_to(a.k, 4 * sizeof(T)) &&
                      aligned_to(a.h0, 16) && aligned_to(a.state, 16);
     const bool async = a.dstate * sizeof(T) % 16 == 0 && aligned_to(a.q, 16) && aligned_to(a.k, 16);
     if (a.dstate <= 32)
-        return vec ? launch_pieces<T, 1, true, STORE>(a, async, st) : launch_pieces<T, 1, false, STORE>(a, async, st);
+        return vec ? launch_pieces<T, 1, true, STORE>(a, async, sms, st) : launch_pieces<T, 1, false, STORE>(a, async, sms, st);
     if (a.dstate <= 64)
-        return vec ? launch_pieces<T, 2, true, STORE>(a, async, st) : launch_pieces<T, 2, false, STORE>(a, async, st);
+        return vec ? launch_pieces<T, 2, true, STORE>(a, async, sms, st) : launch_pieces<T, 2, false, STORE>(a, async, sms, st);
     if (a.dstate <= 96)
-        return vec ? launch_pieces<T, 3, true, STORE>(a, async, st) : launch_pieces<T, 3, false, STORE>(a, async, st);
-    return vec ? launch_pieces<T, 4, true, STORE>(a, async, st) : launch_pieces<T, 4, false, STORE>(a, async, st);
+        return vec ? launch_pieces<T, 3, true, STORE>(a, async, sms, st) : launch_pieces<T, 3, false, STORE>(a, async, sms, st);
+    return vec ? launch_pieces<T, 4, true, STORE>(a, async, sms, st) : launch_pieces<T, 4, false, STORE>(a, async, sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool bf16, cudaStream_t st) {
-    if (a.marks) return launch_t<float, true>(a, st);
-    return bf16 ? launch_t<__nv_bfloat16, false>(a, st) : launch_t<float, false>(a, st);
+cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool bf16, int sms, cudaStream_t st) {
+    if (a.marks) return launch_t<float, true>(a, sms, st);
+    return bf16 ? launch_t<__nv_bfloat16, false>(a, sms, st) : launch_t<float, false>(a, sms, st);
 }
 
 }  // namespace ssm

@@ -53,7 +53,7 @@ struct DeltaBwdArgs {
 // One warp group per few state rows, token after token in fp32: any sizes and
 // alignment, both element types (float32 only where marks are stored); the
 // decode step is seqlen == 1.
-cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool bf16, cudaStream_t st);
+cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool bf16, int sms, cudaStream_t st);
 
 // Gradients of float32 tensors, headdim and dstate up to kDeltaMaxDstate;
 // f.marks and f.r hold what launch_delta_recurrent stored.  Workspace: ds1 of the

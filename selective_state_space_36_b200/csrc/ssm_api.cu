@@ -855,10 +855,10 @@ int device_sms() {
 }
 
 // bf16 sequences up to this many tokens run token by token (one launch, no
-// workspace), longer ones in chunks on the tensor cores.  Token by token, 16 and 32
-// tokens take 7.0 and 12.2 us (one sequence, 16 heads of 64 x 128) or 27 and 50 us (8
-// sequences, 32 heads of 128 x 128); one chunk takes 9.4 or 19.4 us, 2 to 6 us more
-// through padded copies.
+// workspace), longer ones in chunks on the tensor cores.  Token by token, 16 tokens
+// take 5.3 us (one sequence, 16 heads of 64 x 128) or 24 us (8 sequences, 32 heads of
+// 128 x 128), 32 twice that; one chunk takes 9.4 or 19.4 us, 2 to 6 us more through
+// padded copies.
 constexpr int64_t kDeltaRecurrentTokens = 16;
 
 // Sizes common to the delta rule's entry points; *empty: nothing to compute.
@@ -958,7 +958,7 @@ ssm_status delta_forward(ssm_ssd_dims dims, ssm_dtype io, const void *q, const v
     a.out = out; a.h0 = h0; a.state = state;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (io != SSM_BF16 || dims.seqlen <= kDeltaRecurrentTokens || !ssm::delta_fused_fits(a)) {
-        cudaError_t e = ssm::launch_delta_recurrent(a, io == SSM_BF16, st);
+        cudaError_t e = ssm::launch_delta_recurrent(a, io == SSM_BF16, device_sms(), st);
         if (e != cudaSuccess) return cuda_fail(e, "delta rule launch");
         return SSM_OK;
     }
@@ -1103,7 +1103,7 @@ ssm_status ssm_delta_rule_bwd(ssm_ssd_dims dims, ssm_dtype io, const void *q, co
         float *ds1 = p.f.r + r, *es = ds1 + marks;
         p.dq_heads = es + r;
         p.dk_heads = p.dq_heads + per_head;
-        e = ssm::launch_delta_recurrent(p.f, false, st);
+        e = ssm::launch_delta_recurrent(p.f, false, device_sms(), st);
         if (e == cudaSuccess) e = ssm::launch_delta_bwd_direct(p, ds1, es, st);
     }
     cudaError_t ef = cudaFreeAsync(mem, st);
