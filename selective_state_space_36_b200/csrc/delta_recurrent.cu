@@ -19,6 +19,8 @@
 #include "delta_rule.cuh"
 #include "ssm_device.cuh"
 
+#include <type_traits>
+
 namespace ssm {
 namespace {
 
@@ -200,10 +202,10 @@ struct TokenStage {
     float4 pair[kTok / 2];  // of tokens 1, 2: k1 . k2, k1 . q1, k1 . q2, k2 . q2
 };
 
-// A sequence.  ASYNC: rows of q and k are multiples of 16 bytes and start
-// aligned (copied asynchronously); VEC as above.  STORE: the backward pass's
-// first half (DeltaArgs::marks, r; no output).
-template <typename T, int PIECES, int ROWS, bool VEC, bool ASYNC, bool STORE>
+// A sequence.  VEC: as above, and rows of q and k are multiples of 16 bytes and
+// start aligned (copied asynchronously).  STORE: the backward pass's first half
+// (DeltaArgs::marks, r; no output).
+template <typename T, int PIECES, int ROWS, bool VEC, bool STORE>
 __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) {
     __shared__ __align__(16) TokenStage<T, PIECES, ROWS> stages[2];
     constexpr int kThreads = kWarps * 32, kBlockRows = kWarps * 4 * ROWS;
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(kWarps * 32) delta_tokens_kernel(DeltaArgs a) 
         if (t0 < a.seqlen) {
             TokenStage<T, PIECES, ROWS> &st = stages[(t0 / kTok) & 1];
             const int live = (int)(a.seqlen - t0 < kTok ? a.seqlen - t0 : kTok);
-            if (ASYNC) {
+            if (VEC) {
                 constexpr int E = 16 / sizeof(T), PER = 32 * PIECES / E;
                 for (int i = tid; i < kTok * PER; i += kThreads) {
                     const int t = i / PER, c = (i % PER) * E;
@@ -404,15 +406,13 @@ cudaError_t launch_pieces(const DeltaArgs &a, bool async, int sms, cudaStream_t 
     // One row set per warp where that still leaves SMs free: a warp's chain is shorter
     // (18 heads of 40 x 48, 301 tokens: 52 us, two sets 56 us), the work of a row larger.
     const int64_t small = a.batch * a.heads * ((a.headdim + kRowsPerBlock / 2 - 1) / (kRowsPerBlock / 2));
-    if (small <= sms) {
-        const unsigned blocks = (unsigned)small;
-        if (async) delta_tokens_kernel<T, PIECES, 1, VEC, true, STORE><<<blocks, block, 0, st>>>(a);
-        else delta_tokens_kernel<T, PIECES, 1, VEC, false, STORE><<<blocks, block, 0, st>>>(a);
-    } else if (async) {
-        delta_tokens_kernel<T, PIECES, kRows, VEC, true, STORE><<<grid, block, 0, st>>>(a);
-    } else {
-        delta_tokens_kernel<T, PIECES, kRows, VEC, false, STORE><<<grid, block, 0, st>>>(a);
-    }
+    auto tokens = [&](auto fast) {
+        constexpr bool FAST = decltype(fast)::value;
+        if (small <= sms) delta_tokens_kernel<T, PIECES, 1, FAST, STORE><<<(unsigned)small, block, 0, st>>>(a);
+        else delta_tokens_kernel<T, PIECES, kRows, FAST, STORE><<<grid, block, 0, st>>>(a);
+    };
+    if (VEC && async) tokens(std::true_type());
+    else tokens(std::false_type());
     return cudaGetLastError();
 }
 

@@ -526,6 +526,8 @@ def test_explicit_stream_and_errors_of_both_marshallings(lib):
 
 def test_empty_and_refused(request):
     """Host-side checks (no GPU): empty sizes are no-ops, bad arguments are named."""
+    from selective_state_space_36_b200 import build
+    build.build()
     from selective_state_space_36_b200 import binding as b
     f = b.lib.ssm_delta_rule_fwd
 

@@ -57,6 +57,8 @@ CASES = [
     (3, 4096, "f32", "rms", False, True, True), (700, 1023, "bf16", "rms", True, True, True),
     (2, 8192, "bf16", "layer", True, True, True), (2, 8193, "bf16", "layer", True, True, True),
     (5, 20000, "f32", "rms", True, False, False), (3000, 24, "bf16", "layer", True, True, True),
+    (500, 1246, "bf16", "rms", True, False, True), (20, 2047, "f32", "layer", True, True, False),
+    (300, 4999, "bf16", "layer", True, True, True), (3, 5121, "bf16", "layer", True, True, False),
 ]
 
 
@@ -152,6 +154,8 @@ def test_captured_graph(lib):
 
 def test_empty_and_refused():
     """Host-side checks (no GPU)."""
+    from selective_state_space_36_b200 import build
+    build.build()
     from selective_state_space_36_b200 import binding as b
     p = dict(x=0x10000, weight=0x20000, bias=None, z=None, out=0x30000, mean=None, rstd=0x40000)
 
