@@ -507,6 +507,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // thread forward without a gate (12000 bf16 rows of 4999: 60 us, by the kernel for
 // rows of any length 111 us), else 8 (48154 rows of 1246 with the gate: forward 140
 // against 260 us, backward 281 against 617 us; 20 with the gate gain nothing).
+constexpr int kMostVectors = 4, kMostGated = 8;
 struct Shape { int tpr, nv; };
 bool shape_of(int64_t pieces, int most, Shape *s) {
     static constexpr Shape shapes[] = {{8, 1},   {16, 1},  {32, 1},  {32, 2},  {64, 2},
@@ -549,8 +550,6 @@ int64_t walkers(int64_t rows, int rows_per_block, int per_sm, int sms) {
     const int64_t all = (rows + rows_per_block - 1) / rows_per_block, most = (int64_t)per_sm * sms;
     return all < most ? all : most;
 }
-
-constexpr int kMostVectors = 4, kMostGated = 8;
 
 struct Fwd {
     static constexpr int kMostValues = 20;
