@@ -108,11 +108,12 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float (*red)[kWarpsPerBlo
 // computed.  VEC > 1: a ring of kRing - 1 rows ahead in shared memory, filled by
 // asynchronous copies; a thread reads back only what it copied itself, so no
 // barrier is involved.  VEC == 1: one row ahead in registers.
-constexpr int kRing = 4;
-
 template <typename T, int VEC, int NV, int NT>
 struct Rows {
-    static constexpr int kBytes = VEC > 1 ? kRing * NT * NV * kThreads * 16 : 0;
+    // four rows, or as many as let two blocks have an SM
+    static constexpr int kRow = NT * NV * kThreads * 16, kHalf = 113 * 1024;
+    static constexpr int kRing = 4 * kRow <= kHalf ? 4 : 3 * kRow <= kHalf ? 3 : 2;
+    static constexpr int kBytes = VEC > 1 ? kRing * kRow : 0;
     T next[VEC > 1 ? 1 : NT][NV];
     uint4 *ring;
     int put = 0, at = 0;
